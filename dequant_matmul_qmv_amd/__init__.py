@@ -6,6 +6,8 @@ launch), ``mxq_qmm`` (prefill), ``mxq_linear`` (either, plus an output bias),
 ``mxq_linear_act`` (the same for float16 or bfloat16 activations),
 ``mxq_linear_a8`` (int8 activations, quantized per row in the kernel),
 ``mxq_dequant`` (bit-exact standalone dequant) and ``mxq_pack`` (host packer),
+the serving operators around the projections, ``mxq_rope`` (rotary positions),
+``KvCache`` and ``mxq_kv_append`` (an 8-bit paged key/value cache),
 plus diagnostics (``mxq_describe``, ``mxq_describe_grouped``) and the split
 workspace controls (``mxq_release_workspaces``, ``mxq_workspace_bytes``).
 """
@@ -36,3 +38,14 @@ from ._lib import (  # noqa: F401
     mxq_workspace_bytes,
     QmvProblem,
 )
+
+# the serving operators, bound on first use: their module needs torch, which the rest imports inside its calls
+_SERVE = ("KvCache", "mxq_kv_append", "mxq_rope")
+
+
+def __getattr__(name):
+    if name in _SERVE:
+        from . import _serve
+        globals()[name] = value = getattr(_serve, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,230 @@
+"""ctypes binding of libmxq's serving operators (argument marshalling only):
+rotary positions, the 8-bit paged key/value cache and what works on it, and
+sampling.  As in ``_lib``: tensor metadata is checked, raw device pointers and
+the current HIP stream are passed on, a non-OK status becomes an exception.
+
+These calls are made once a layer for a single token, so their host time
+counts: checks are plain attribute comparisons, and the device is only
+switched when it is not the current one.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import MXQ_BF16, MXQ_F16
+
+_HALF = {torch.float16: MXQ_F16, torch.bfloat16: MXQ_BF16}
+_i32 = torch.int32
+_f32 = torch.float32
+
+
+class _CacheStruct(ctypes.Structure):
+    """ctypes mirror of ``mxq_kv_cache`` (include/mxq.h)."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("blocks", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+_fn = None
+
+
+def _load():
+    """The library with this module's signatures declared (once)."""
+    global _fn
+    if _fn is None:
+        lib = _lib.load()
+        i64, i32, vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+        lib.mxq_rope.argtypes = ([vp, i64, i64] * 4) + [vp, vp, i64, i32, i32, i32, i32, i32, i32, vp]
+        cache = ctypes.POINTER(_CacheStruct)
+        lib.mxq_kv_append.argtypes = [cache, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64, i32, vp]
+        for f in (lib.mxq_rope, lib.mxq_kv_append):
+            f.restype = i32
+        _fn = lib
+    return _fn
+
+
+def _call(f, dev, stream, *args):
+    """f(*args, stream) with `dev` current; raises on a status other than OK."""
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, handle)
+    if st:
+        _lib._check(_fn, st)
+
+
+def _on(who, dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{who}: {name} must be on {dev}, is on {t.device}")
+
+
+def _rows(who, name, t, dtype):
+    """Strides of a [tokens, heads, dim] tensor with a contiguous last dimension."""
+    if t.dtype != dtype or t.dim() != 3:
+        raise TypeError(f"{who}: {name} must be a 3-D {str(dtype).replace('torch.', '')} tensor [tokens, heads, dim]")
+    a, b, c = t.stride()
+    if c != 1 and t.shape[2] > 1:
+        raise ValueError(f"{who}: {name}'s last dimension must be contiguous")
+    return a, b
+
+
+def _ints(who, name, t, shape):
+    if t.dtype != _i32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{who}: {name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _device(who, name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{who}: {name} must be a device tensor")
+    return t.device
+
+
+def mxq_rope(q, k, inv_freq, positions, q_out=None, k_out=None, *, interleaved: bool = False, stream=None):
+    """q and k [tokens, heads, dim] (f16 or bf16) rotated by position; returns the rotated pair.
+
+    The first ``2 * len(inv_freq)`` values of each head turn by
+    ``positions[t] * inv_freq[i]``: neighbours as pairs if ``interleaved``, else
+    the two halves; the rest is copied.  Token and head strides are free.
+    ``q_out`` and ``k_out`` may be ``q`` and ``k``.  ``k`` may be None."""
+    who = "mxq_rope"
+    dev = _device(who, "q", q)
+    code = _HALF.get(q.dtype)
+    if code is None:
+        raise TypeError(f"{who}: q must be float16 or bfloat16")
+    n, heads, dim = q.shape if q.dim() == 3 else (0, 0, 0)
+    qs = _rows(who, "q", q, q.dtype)
+    if inv_freq.dtype != _f32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"{who}: inv_freq must be a contiguous float32 vector")
+    rot = 2 * inv_freq.shape[0]
+    if rot > dim:
+        raise ValueError(f"{who}: {rot // 2} frequencies rotate {rot} values, a head has {dim}")
+    _ints(who, "positions", positions, (n,))
+    _on(who, dev, k=k, inv_freq=inv_freq, positions=positions, q_out=q_out, k_out=k_out)
+    if q_out is None:
+        q_out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"{who}: q_out must have q's shape")
+    qo = _rows(who, "q_out", q_out, q.dtype)
+    kv_heads, ks, ko, kp, kop = 0, (0, 0), (0, 0), None, None
+    if k is not None:
+        ks = _rows(who, "k", k, q.dtype)
+        if k.shape[0] != n or k.shape[2] != dim:
+            raise ValueError(f"{who}: k must be [{n}, kv_heads, {dim}]")
+        kv_heads = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((n, kv_heads, dim), dtype=q.dtype, device=dev)
+        elif k_out.shape != k.shape:
+            raise ValueError(f"{who}: k_out must have k's shape")
+        ko = _rows(who, "k_out", k_out, q.dtype)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError(f"{who}: k_out without k")
+    _call(_load().mxq_rope, dev, stream, q.data_ptr(), *qs, kp, *ks, q_out.data_ptr(), *qo, kop, *ko,
+          inv_freq.data_ptr(), positions.data_ptr(), n, heads, kv_heads, dim, rot, 1 if interleaved else 0, code)
+    return q_out, k_out
+
+
+class KvCache:
+    """A paged key/value cache held in 8 bits; a code c stands for c * scale.
+
+    ``k`` int8 [blocks, kv_heads, block, dim], ``v`` int8 [blocks, kv_heads, dim, block],
+    ``k_scale`` and ``v_scale`` float32 [blocks, kv_heads], contiguous, on one device;
+    block 16, 32, 64 or 128, dim 64 or 128.  A sequence's tokens ``j * block ..`` are in
+    the page ``table[s, j]`` of the table that the calls take."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "_struct")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dtype != torch.int8 or k.dim() != 4 or v.dtype != torch.int8 or v.dim() != 4:
+            raise TypeError("KvCache: k and v must be 4-D int8 tensors")
+        blocks, kv_heads, block, dim = k.shape
+        if tuple(v.shape) != (blocks, kv_heads, dim, block):
+            raise ValueError(f"KvCache: v must be [blocks, kv_heads, dim, block] = {[blocks, kv_heads, dim, block]}")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype != _f32 or tuple(t.shape) != (blocks, kv_heads):
+                raise ValueError(f"KvCache: {name} must be float32 {[blocks, kv_heads]}")
+        dev = _device("KvCache", "k", k)
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.device != dev or not t.is_contiguous():
+                raise ValueError(f"KvCache: {name} must be contiguous and on {dev}")
+        if block not in (16, 32, 64, 128) or dim not in (64, 128):
+            raise ValueError(f"KvCache: block must be 16, 32, 64 or 128 and dim 64 or 128, got {block} and {dim}")
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, dev
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), blocks,
+                                    kv_heads, block, dim)
+
+    @classmethod
+    def empty(cls, blocks: int, kv_heads: int, block: int, dim: int, device="cuda"):
+        """A cache of zero codes and scales."""
+        return cls(torch.zeros((blocks, kv_heads, block, dim), dtype=torch.int8, device=device),
+                   torch.zeros((blocks, kv_heads, dim, block), dtype=torch.int8, device=device),
+                   torch.zeros((blocks, kv_heads), dtype=_f32, device=device),
+                   torch.zeros((blocks, kv_heads), dtype=_f32, device=device))
+
+    @property
+    def blocks(self):
+        return self._struct.blocks
+
+    @property
+    def kv_heads(self):
+        return self._struct.kv_heads
+
+    @property
+    def block(self):
+        return self._struct.block
+
+    @property
+    def dim(self):
+        return self._struct.dim
+
+
+def _paging(who, dev, table, lens, starts, tokens):
+    """(seqs, table row stride, width, starts pointer) of checked paging tensors."""
+    if table.dtype != _i32 or table.dim() != 2:
+        raise TypeError(f"{who}: table must be a 2-D int32 tensor [sequences, pages]")
+    seqs, width = table.shape
+    row, one = table.stride()
+    if (one != 1 and width > 1) or (row < width and seqs > 1):
+        raise ValueError(f"{who}: table's rows must be contiguous")
+    _ints(who, "lens", lens, (seqs,))
+    if starts is None:
+        if tokens != seqs:
+            raise ValueError(f"{who}: {tokens} tokens for {seqs} sequences need starts")
+    else:
+        _ints(who, "starts", starts, (seqs + 1,))
+    _on(who, dev, table=table, lens=lens, starts=starts)
+    return seqs, row, width, None if starts is None else starts.data_ptr()
+
+
+def mxq_kv_append(cache, k, v, table, lens, starts=None, *, stream=None):
+    """New keys and values [tokens, kv_heads, dim] (f16 or bf16) quantized into ``cache``, in place; returns it.
+
+    Sequence s has ``lens[s]`` tokens with its new ones, the rows
+    ``starts[s]:starts[s + 1]`` of k and v, or row s alone without ``starts``.
+    The scheme, and what becomes of tokens without a page, is in include/mxq.h."""
+    who = "mxq_kv_append"
+    dev = cache.device
+    code = _HALF.get(k.dtype)
+    if code is None:
+        raise TypeError(f"{who}: k must be float16 or bfloat16")
+    ks, vs = _rows(who, "k", k, k.dtype), _rows(who, "v", v, k.dtype)
+    n = k.shape[0]
+    st = cache._struct
+    if k.shape != v.shape or k.shape[1] != st.kv_heads or k.shape[2] != st.dim:
+        raise ValueError(f"{who}: k and v must be [tokens, {st.kv_heads}, {st.dim}]")
+    _on(who, dev, k=k, v=v)
+    seqs, row, width, sp = _paging(who, dev, table, lens, starts, n)
+    _call(_load().mxq_kv_append, dev, stream, st, k.data_ptr(), *ks, v.data_ptr(), *vs, table.data_ptr(), row, width,
+          lens.data_ptr(), sp, n, seqs, code)
+    return cache

@@ -12,6 +12,7 @@
 
 #include "../../include/mxq.h"
 #include "mxq_internal.h"
+#include "serve_internal.h"
 
 namespace {
 
@@ -280,6 +281,12 @@ mxq_status run_matmul(const char* who, const void* x, const uint32_t* w, const v
 }  // namespace
 
 namespace mxq {
+
+void clear_error() { g_last_error.clear(); }
+
+mxq_status report(mxq_status s, const std::string& msg) { return fail(s, msg); }
+
+mxq_status report_hip(const char* who, hipError_t e) { return hip_fail(who, e); }
 
 hipError_t device_info(DeviceInfo* out) {
   int dev = 0;

@@ -1,0 +1,151 @@
+// Rotary positions: each pair (a, b) of a head turns by the angle
+// position * inv_freq[i] into (a cos - b sin, b cos + a sin).  Pairs are
+// neighbours (interleaved) or lie rot / 2 apart (halves); dim - rot values
+// behind them pass through.
+//
+// The angle of a far position needs more than 32 bits (131071 rad leaves
+// 2^-7 rad of resolution in f32): position * inv_freq / 2 pi is taken in f64,
+// its whole turns removed there, and the rest, within half a turn, goes to f32.
+//
+// Bound: HBM, q and k read once and written once.  One workgroup holds one
+// token, computes its rot / 2 cosines and sines once into LDS (every head
+// shares them), and walks the heads 16 bytes a lane.
+#include "mxq_device.h"
+#include "serve_internal.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kMaxRot = 256;
+constexpr double kInvTwoPi = 0.15915494309189533577;
+
+template <bool BF16>
+__device__ __forceinline__ void widen8(u4 v, float (&f)[8]) {
+  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = sb_to_f32<BF16>(static_cast<uint16_t>(d[i]));
+    f[2 * i + 1] = sb_to_f32<BF16>(static_cast<uint16_t>(d[i] >> 16));
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ u4 narrow8(const float (&f)[8]) {
+  uint32_t d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    d[i] = static_cast<uint32_t>(f32_to_act_bits<BF16>(f[2 * i])) |
+           (static_cast<uint32_t>(f32_to_act_bits<BF16>(f[2 * i + 1])) << 16);
+  return u4{d[0], d[1], d[2], d[3]};
+}
+
+// Cosine and sine of a whole angle, for this token's pairs.
+__device__ __forceinline__ void fill_turns(const float* inv_freq, int pos, int half, float* cs, float* sn) {
+  for (int i = threadIdx.x; i < half; i += blockDim.x) {
+    const double turns = static_cast<double>(pos) * static_cast<double>(inv_freq[i]) * kInvTwoPi;
+    const float rest = static_cast<float>(turns - __builtin_rint(turns));
+    float s, c;
+    sincospif(2.0f * rest, &s, &c);
+    cs[i] = c;
+    sn[i] = s;
+  }
+  __syncthreads();
+}
+
+}  // namespace
+
+// 16-byte rows: dim and rot multiples of 8 (halves: rot of 16).  Units of a
+// head: interleaved, dim / 8 chunks; halves, rot / 16 chunks of the first half
+// with their partners, then the (dim - rot) / 8 chunks behind.
+template <bool BF16, bool INTER>
+__global__ __launch_bounds__(256) void rope_wide_kernel(RopeArgs a) {
+  __shared__ float cs[kMaxRot / 2], sn[kMaxRot / 2];
+  const int64_t t = blockIdx.x;
+  const int half = a.rot / 2;
+  fill_turns(a.inv_freq, a.positions[t], half, cs, sn);
+  const int turned = INTER ? a.rot / 8 : a.rot / 16;
+  const int units = turned + (a.dim - a.rot) / 8;
+  const int first = a.side[0].heads * units, all = first + a.side[1].heads * units;
+  for (int u = threadIdx.x; u < all; u += blockDim.x) {
+    const RopeSide& s = a.side[u < first ? 0 : 1];
+    const int v = u < first ? u : u - first;
+    const int head = v / units, c = v - head * units;
+    const uint16_t* in = s.in + t * s.in_token + head * s.in_head;
+    uint16_t* out = s.out + t * s.out_token + head * s.out_head;
+    if (c >= turned) {
+      const int at = a.rot + (c - turned) * 8;
+      *reinterpret_cast<u4*>(out + at) = *reinterpret_cast<const u4*>(in + at);
+    } else if constexpr (INTER) {
+      float x[8], y[8];
+      widen8<BF16>(*reinterpret_cast<const u4*>(in + c * 8), x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float co = cs[c * 4 + i], si = sn[c * 4 + i];
+        y[2 * i] = x[2 * i] * co - x[2 * i + 1] * si;
+        y[2 * i + 1] = x[2 * i + 1] * co + x[2 * i] * si;
+      }
+      *reinterpret_cast<u4*>(out + c * 8) = narrow8<BF16>(y);
+    } else {
+      float x[8], z[8], y[8], w[8];
+      widen8<BF16>(*reinterpret_cast<const u4*>(in + c * 8), x);
+      widen8<BF16>(*reinterpret_cast<const u4*>(in + half + c * 8), z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float co = cs[c * 8 + i], si = sn[c * 8 + i];
+        y[i] = x[i] * co - z[i] * si;
+        w[i] = z[i] * co + x[i] * si;
+      }
+      *reinterpret_cast<u4*>(out + c * 8) = narrow8<BF16>(y);
+      *reinterpret_cast<u4*>(out + half + c * 8) = narrow8<BF16>(w);
+    }
+  }
+}
+
+// Any strides, alignments and even rot: one pair, or one value behind them, a lane.
+template <bool BF16>
+__global__ __launch_bounds__(256) void rope_narrow_kernel(RopeArgs a) {
+  __shared__ float cs[kMaxRot / 2], sn[kMaxRot / 2];
+  const int64_t t = blockIdx.x;
+  const int half = a.rot / 2;
+  fill_turns(a.inv_freq, a.positions[t], half, cs, sn);
+  const int units = half + a.dim - a.rot;
+  const int first = a.side[0].heads * units, all = first + a.side[1].heads * units;
+  for (int u = threadIdx.x; u < all; u += blockDim.x) {
+    const RopeSide& s = a.side[u < first ? 0 : 1];
+    const int v = u < first ? u : u - first;
+    const int head = v / units, c = v - head * units;
+    const uint16_t* in = s.in + t * s.in_token + head * s.in_head;
+    uint16_t* out = s.out + t * s.out_token + head * s.out_head;
+    if (c >= half) {
+      out[a.rot + c - half] = in[a.rot + c - half];
+    } else {
+      const int i = a.interleaved ? 2 * c : c, j = a.interleaved ? 2 * c + 1 : half + c;
+      const float x = sb_to_f32<BF16>(in[i]), y = sb_to_f32<BF16>(in[j]);
+      out[i] = f32_to_act_bits<BF16>(x * cs[c] - y * sn[c]);
+      out[j] = f32_to_act_bits<BF16>(y * cs[c] + x * sn[c]);
+    }
+  }
+}
+
+hipError_t launch_rope(const RopeArgs& a) {
+  bool wide = a.dim % 8 == 0 && a.rot % (a.interleaved ? 8 : 16) == 0;
+  for (const RopeSide& s : a.side)
+    if (s.heads > 0)
+      wide = wide && ((reinterpret_cast<uintptr_t>(s.in) | reinterpret_cast<uintptr_t>(s.out)) & 15) == 0 &&
+             ((s.in_token | s.in_head | s.out_token | s.out_head) & 7) == 0;
+  const dim3 grid(static_cast<unsigned>(a.tokens)), block(256);
+  if (wide && a.interleaved) {
+    if (a.bf16) hipLaunchKernelGGL((rope_wide_kernel<true, true>), grid, block, 0, a.stream, a);
+    else hipLaunchKernelGGL((rope_wide_kernel<false, true>), grid, block, 0, a.stream, a);
+  } else if (wide) {
+    if (a.bf16) hipLaunchKernelGGL((rope_wide_kernel<true, false>), grid, block, 0, a.stream, a);
+    else hipLaunchKernelGGL((rope_wide_kernel<false, false>), grid, block, 0, a.stream, a);
+  } else {
+    if (a.bf16) hipLaunchKernelGGL((rope_narrow_kernel<true>), grid, block, 0, a.stream, a);
+    else hipLaunchKernelGGL((rope_narrow_kernel<false>), grid, block, 0, a.stream, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mxq

@@ -257,6 +257,77 @@ mxq_status mxq_linear_a8(const void* x, const uint32_t* w, const void* scales, c
                          int group_size, mxq_dtype sb_dtype, void* stream);
 
 /*
+ * mxq_rope -- rotary positions on q and k.
+ *
+ * Pair i < rot / 2 of a head turns by angle positions[t] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * (a, b) = (x[2i], x[2i+1]) if `interleaved`, else (x[i], x[rot/2 + i]); the
+ * dim - rot values behind the rotated part are copied.  Long-context scaling
+ * of the frequencies is part of inv_freq, the caller's own.  The angle is
+ * taken in f64 and reduced there, the rotation in f32, rounded once to the
+ * storage type.
+ *   q      f16|bf16, element (t, h, d) at t * q_token + h * q_head + d; k the same
+ *   q_out, k_out  the same type with strides of their own; may be q and k
+ *          themselves (same strides), must not overlap them otherwise
+ *   inv_freq f32 [rot / 2], positions i32 [tokens]
+ * heads or kv_heads may be 0 (its pointers may then be null).  rot is even,
+ * 0 <= rot <= dim <= 256.  All pointers 2-byte (arrays 4-byte) aligned; rows
+ * that are 16-byte aligned with dim and rot multiples of 16 run on wider
+ * accesses.  tokens == 0 is a no-op.
+ */
+mxq_status mxq_rope(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                    int64_t k_head, void* q_out, int64_t q_out_token, int64_t q_out_head, void* k_out,
+                    int64_t k_out_token, int64_t k_out_head, const float* inv_freq,
+                    const int32_t* positions, int64_t tokens, int heads, int kv_heads, int dim, int rot,
+                    int interleaved, mxq_dtype dtype, void* stream);
+
+/*
+ * A paged key/value cache held in 8 bits (device pointers, the caller's
+ * memory).  A page holds `block` tokens of every kv head; a code c stands for
+ * c * scale, one scale for each (page, kv head), never negative.
+ *   k       i8  [blocks, kv_heads, block, dim]
+ *   v       i8  [blocks, kv_heads, dim, block]   (tokens innermost)
+ *   k_scale, v_scale  f32 [blocks, kv_heads]
+ * block in {16, 32, 64, 128}, dim in {64, 128}; k and v 16-byte, scales
+ * 4-byte aligned.  A sequence's tokens j * block .. are in page table[s][j].
+ */
+typedef struct mxq_kv_cache {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t blocks;
+  int32_t kv_heads;
+  int32_t block;
+  int32_t dim;
+} mxq_kv_cache;
+
+/*
+ * mxq_kv_append -- quantize new keys and values into the cache.
+ *
+ * Sequence s has lens[s] tokens with its new ones, which are its last; its new
+ * rows of k and v are starts[s] .. starts[s + 1] (starts: i32 [seqs + 1], from
+ * 0 to `tokens`, not descending), or row s alone where starts is null (then
+ * tokens == seqs).  For each page that gets new tokens, and each head:
+ *   fresh = max |x| / 127 over its new tokens,
+ *   scale = max(old scale, fresh) where the page holds older tokens of the
+ *           sequence, else fresh,
+ *   new codes = clamp(rint(x * (1 / scale)), -127, 127); 0 if scale is 0,
+ *   older codes = rint(code * (old scale / scale)), unchanged if that is 1,
+ * quotients correctly rounded to f32, products in f32, ties to even.  Other
+ * codes of the page stay as they are.  k and v must be finite.  Pages that get
+ * new tokens must not be shared by two sequences of one call.  New tokens
+ * without a place (a table entry outside 0 .. blocks - 1, a position beyond
+ * `width` pages, or more of them than lens[s]) are dropped.
+ *   k, v    f16|bf16, element (t, h, d) at t * k_token + h * k_head + d
+ *   table   i32, row s at s * table_stride, `width` entries; width * block < 2^31
+ */
+mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_token, int64_t k_head,
+                         const void* v, int64_t v_token, int64_t v_head, const int32_t* table,
+                         int64_t table_stride, int64_t width, const int32_t* lens, const int32_t* starts,
+                         int64_t tokens, int64_t seqs, mxq_dtype dtype, void* stream);
+
+/*
  * mxq_dequant -- standalone dequantization: out[n, k] = q * s + b.
  *
  * The reconstruction mlxcel #574 ("What is already in-tree") requires to be
