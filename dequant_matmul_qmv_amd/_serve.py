@@ -42,7 +42,9 @@ def _load():
         lib.mxq_rope.argtypes = ([vp, i64, i64] * 4) + [vp, vp, i64, i32, i32, i32, i32, i32, i32, vp]
         cache = ctypes.POINTER(_CacheStruct)
         lib.mxq_kv_append.argtypes = [cache, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64, i32, vp]
-        for f in (lib.mxq_rope, lib.mxq_kv_append):
+        lib.mxq_attention.argtypes = [vp, i64, i64, cache, vp, i64, i64, vp, vp, i64, i64, i32, i64, ctypes.c_float, vp,
+                                      vp, i32, vp]
+        for f in (lib.mxq_rope, lib.mxq_kv_append, lib.mxq_attention):
             f.restype = i32
         _fn = lib
     return _fn
@@ -228,3 +230,34 @@ def mxq_kv_append(cache, k, v, table, lens, starts=None, *, stream=None):
     _call(_load().mxq_kv_append, dev, stream, st, k.data_ptr(), *ks, v.data_ptr(), *vs, table.data_ptr(), row, width,
           lens.data_ptr(), sp, n, seqs, code)
     return cache
+
+
+def mxq_attention(q, cache, table, lens, starts=None, out=None, *, window: int = 0, scale: float | None = None,
+                  return_lse: bool = False, stream=None):
+    """Causal attention of q [tokens, heads, dim] (f16 or bf16) over ``cache``, which holds the new tokens already.
+
+    Sequences and their rows as in ``mxq_kv_append``.  ``window`` > 0: the last
+    that many keys of each token; ``scale``: 1 / sqrt(dim) if None.  Returns out
+    [tokens, heads, dim] in q's type, or (out, lse) with the log-sums float32
+    [tokens, heads].  A row without keys gives 0 and -inf."""
+    who = "mxq_attention"
+    dev = cache.device
+    code = _HALF.get(q.dtype)
+    if code is None:
+        raise TypeError(f"{who}: q must be float16 or bfloat16")
+    qs = _rows(who, "q", q, q.dtype)
+    n, heads, dim = q.shape
+    st = cache._struct
+    if dim != st.dim:
+        raise ValueError(f"{who}: q's heads have {dim} values, the cache's {st.dim}")
+    _on(who, dev, q=q)
+    seqs, row, width, sp = _paging(who, dev, table, lens, starts, n)
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"{who}: out must be a contiguous tensor of q's shape and type on {dev}")
+    lse = torch.empty((n, heads), dtype=_f32, device=dev) if return_lse else None
+    _call(_load().mxq_attention, dev, stream, q.data_ptr(), *qs, st, table.data_ptr(), row, width, lens.data_ptr(), sp,
+          n, seqs, heads, window, dim ** -0.5 if scale is None else scale, out.data_ptr(),
+          None if lse is None else lse.data_ptr(), code)
+    return (out, lse) if return_lse else out

@@ -1,0 +1,526 @@
+// Attention of a few new tokens a sequence over the 8-bit paged cache: the
+// serving step's form (one token), and short drafts.
+//
+//   x = (q . kcode) * kscale * scale,  p = exp(x - max x),
+//   out = sum p * vscale * vcode / sum p
+//
+// with a key seen by a row if it is not past the row's position, inside the
+// window, and its page exists; a row that sees none gives 0 and a log-sum of
+// -inf.
+//
+// Bound: HBM, the cache read once (2 * keys * kv heads * dim bytes).  So the
+// key axis is split over workgroups: every wave finds its part by a scan over
+// the sequences' lengths, which only the GPU knows, and all parts are near
+// equal whatever the lengths are.  The four waves of a workgroup take its
+// 64-key chunks in turn and join their results in LDS; where a sequence has
+// several parts, a second kernel joins those.
+//
+// Both products run on the matrix cores with the codes as exact f16, straight
+// from registers.  S^T = K Q^T leaves each lane 16 keys of one query row, and
+// with the keys of a chunk dealt out so that those 16 are neighbours, they are
+// the operand of O^T = V^T P^T as they stand: no exchange, no LDS, 16-byte
+// loads of k and of v (whose tokens are innermost).  The 16 rows are the query
+// heads that share a kv head, times the new tokens.
+//
+// Rounding: q and codes are exact, sums, maxima and weights f32; P is f16
+// (2^-11 relative; the weights are summed before that rounding), held as 2^14
+// times its value: normal down to 2^-28 of the row's largest.  A chunk that has
+// smaller ones (rare: 19 below the largest score) multiplies them apart, in
+// steps of 2^24.  v's scales differ by page: P carries vscale / the
+// largest vscale so far, at most 1, and that largest one multiplies the sums.
+#include <climits>
+
+#include "attend_device.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kFewThreads = 256, kFewWaves = 4;
+constexpr int kChunk = 64;      // keys a wave takes at a time
+constexpr int kMinChunks = 4;   // at least one chunk for each wave of a workgroup
+constexpr float kTiny = 1e-30f;
+
+// One sequence's share of the few-row work.
+struct Share {
+  int c0, chunks;  // first 64-key chunk, and how many
+  int groups;      // groups of 16 * MT rows
+};
+template <int MT>
+__device__ __forceinline__ Share share_of(const AttendArgs& a, int s) {
+  Share r{};
+  if (s >= a.seqs) return r;
+  const SeqSpan q = seq_span(a, s);
+  const int64_t rows = static_cast<int64_t>(q.n) * a.group;
+  if (rows > a.few_rows) return r;
+  r.groups = static_cast<int>((rows + 16 * MT - 1) / (16 * MT));
+  const int hi = min(max(q.len, 0), a.width * a.pool.block);
+  const int lo = a.window > 0 ? max(0, q.len - q.n - a.window + 1) : 0;
+  r.c0 = lo / kChunk;
+  r.chunks = max(0, (hi + kChunk - 1) / kChunk - r.c0);
+  return r;
+}
+
+struct Part {
+  bool any;
+  int seq, base, nth;   // base: the sequence's first slot; nth: the slot within it
+  int step, splits;     // chunks of a part, parts of the sequence
+  Share share;
+};
+
+// Where slot `slot` lies, or (slot < 0) sequence `seq`.  Run by whole waves.
+template <int MT>
+__device__ Part find_part(const AttendArgs& a, int slot, int seq) {
+  const int lane = threadIdx.x & 63, hk = a.pool.kv_heads;
+  long long total = 0;
+  Share mine{};
+  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+    mine = share_of<MT>(a, s0 + lane);
+    total += static_cast<long long>(mine.chunks) * mine.groups * hk;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) total += __shfl_xor(total, d);
+  const long long even = (total + a.target - 1) / a.target;
+  Part p{};
+  p.step = static_cast<int>(max(even, static_cast<long long>(kMinChunks)));
+  int before = 0;
+  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+    if (a.seqs > 64) mine = share_of<MT>(a, s0 + lane);
+    const int splits = max(1, (mine.chunks + p.step - 1) / p.step);
+    const int count = mine.groups * splits * hk;
+    int sum = count;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    const unsigned long long hit = slot >= 0 ? __ballot(before + sum > slot) : (seq < s0 + 64 ? 1ull << (seq - s0) : 0);
+    if (hit != 0) {
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
+      p.any = true;
+      p.seq = s0 + src;
+      p.base = before + __shfl(sum, src) - __shfl(count, src);
+      p.nth = slot - p.base;
+      p.splits = __shfl(splits, src);
+      p.share.c0 = __shfl(mine.c0, src);
+      p.share.chunks = __shfl(mine.chunks, src);
+      p.share.groups = __shfl(mine.groups, src);
+      return p;
+    }
+    before += __shfl(sum, 63);
+  }
+  return p;
+}
+
+template <int DIM>
+struct Raw {
+  u4 k[4 * (DIM / 64)];
+  u4 v[DIM / 16];
+  float ks, vs;
+  bool ok;
+};
+
+struct Pages {
+  int k, v;   // pages of the lane's k rows and of its v tokens; -1: none
+};
+
+}  // namespace
+
+template <int DIM, int MT, bool BF16>
+__global__ __launch_bounds__(kFewThreads, MT * DIM > 256 ? 1 : 2) void attend_few_kernel(AttendArgs a) {
+  constexpr int U = DIM / 64, DB = DIM / 16, kRows = 16 * MT;
+  __shared__ float join[kFewWaves][16][DIM + 4];
+  __shared__ float join_m[kFewWaves][16], join_l[kFewWaves][16];
+  const Part part = find_part<MT>(a, blockIdx.x, -1);
+  if (!part.any) return;
+  const int hk = a.pool.kv_heads, block = a.pool.block;
+  const int head = part.nth % hk, rest = part.nth / hk, rg = rest % part.share.groups, split = rest / part.share.groups;
+  const SeqSpan sp = seq_span(a, part.seq);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rho = lane & 15, h = lane >> 4;
+  const int row0 = rg * kRows, rows = min(kRows, sp.n * a.group - row0);
+  const int pos0 = sp.len - sp.n;
+  const int limit = min(max(sp.len, 0), a.width * block);
+
+  // query rows of this lane (one of 16 for each mt), their fragments and key ranges
+  u4 qf[MT][2 * U];
+  float factor[MT];
+  int from[MT], upto[MT];
+  int all_from = 0, all_upto = INT_MAX;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int i = row0 + mt * 16 + rho;
+    const bool real = i < sp.n * a.group;
+    const int tok = real ? i / a.group : 0, hq = head * a.group + (real ? i - tok * a.group : 0);
+    const uint16_t* q = a.q + static_cast<int64_t>(sp.t0 + tok) * a.q_token + static_cast<int64_t>(hq) * a.q_head;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) qf[mt][2 * u + f] = *reinterpret_cast<const u4*>(q + u * 64 + h * 16 + f * 8);
+    float inverse = 1.0f;
+    if constexpr (BF16) {
+      float top = 0.0f, fac;
+#pragma unroll
+      for (int f = 0; f < 2 * U; ++f) top = fmaxf(top, absmax8_bf16(qf[mt][f]));
+      top = max_xor16(max_xor32(top));
+      row_factor(top, fac, inverse);
+#pragma unroll
+      for (int f = 0; f < 2 * U; ++f) qf[mt][f] = bf16_to_scaled_f16(qf[mt][f], fac);
+    }
+    factor[mt] = a.scale2 * inverse;
+    const int pos = pos0 + tok;
+    upto[mt] = min(pos + 1, limit);  // rows past the last repeat the first; they are not stored
+    from[mt] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    if (real) {
+      all_from = max(all_from, from[mt]);
+      all_upto = min(all_upto, upto[mt]);
+    }
+  }
+  // keys that every row sees: [all_from, all_upto)
+#pragma unroll
+  for (int d = 1; d < 16; d *= 2) {
+    all_from = max(all_from, __shfl_xor(all_from, d));
+    all_upto = min(all_upto, __shfl_xor(all_upto, d));
+  }
+
+  const int32_t* table = a.table + static_cast<int64_t>(part.seq) * a.table_stride;
+  const int c_begin = part.share.c0 + split * part.step;
+  const int c_end = min(c_begin + part.step, part.share.c0 + part.share.chunks);
+  const int kgroup = rho >> 2;  // the 16-key group whose k rows this lane loads
+  const uint32_t magic = kMagic;
+
+  auto pages_of = [&](int c) {
+    Pages p;
+    const int jk = (c * kChunk + kgroup * 16) / block, jv = (c * kChunk + h * 16) / block;
+    p.k = jk < a.width ? table[jk] : -1;
+    p.v = jv < a.width ? table[jv] : -1;
+    return p;
+  };
+  auto load = [&](int c, Pages p, Raw<DIM>& r) {
+    const int nb = static_cast<int>(a.pool.blocks);
+    // a page past the sequence's end may be anyone's, or never written
+    r.ok = p.v >= 0 && p.v < nb && c * kChunk + h * 16 < limit;
+    const int64_t pk = p.k >= 0 && p.k < nb ? p.k : 0, pv = r.ok ? p.v : 0;
+    const int tk = (c * kChunk + kgroup * 16) & (block - 1), tv = (c * kChunk + h * 16) & (block - 1);
+    const int8_t* kp = a.pool.k + ((pk * hk + head) * block + tk + (rho & 3)) * DIM + h * 16;
+    const int8_t* vp = a.pool.v + ((pv * hk + head) * DIM + rho) * block + tv;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int u = 0; u < U; ++u) r.k[b * U + u] = *reinterpret_cast<const u4*>(kp + b * 4 * DIM + u * 64);
+#pragma unroll
+    for (int db = 0; db < DB; ++db) r.v[db] = *reinterpret_cast<const u4*>(vp + db * 16 * block);
+    r.ks = a.pool.k_scale[pv * hk + head];
+    r.vs = r.ok ? a.pool.v_scale[pv * hk + head] : 0.0f;
+  };
+
+  f4 acc[MT][DB];
+  float m[MT], l[MT], top_vs = kTiny;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m[mt] = kNegInf;
+    l[mt] = 0.0f;
+#pragma unroll
+    for (int db = 0; db < DB; ++db) acc[mt][db] = f4{0, 0, 0, 0};
+  }
+
+  auto compute = [&](int c, const Raw<DIM>& r) {
+    f4 s[MT][4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[mt][b] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const u4 w = r.k[b * U + u];
+        const h8 k0 = as_h8(codes8_f16(w.x, w.y, magic)), k1 = as_h8(codes8_f16(w.z, w.w, magic));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          s[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, as_h8(qf[mt][2 * u]), s[mt][b], 0, 0, 0);
+          s[mt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, as_h8(qf[mt][2 * u + 1]), s[mt][b], 0, 0, 0);
+        }
+      }
+    }
+    const float was_vs = top_vs;
+    top_vs = fmaxf(top_vs, max_xor16(max_xor32(r.vs)));
+    const float share = r.vs / top_vs, shrink = was_vs / top_vs;
+    const bool whole = __all(r.ok) && c * kChunk >= all_from && (c + 1) * kChunk <= all_upto;
+    const int key0 = c * kChunk + h * 16;
+    bool low = false;
+    float ref[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const float f = r.ks * factor[mt];
+      float mx = kNegInf, mn = -kNegInf;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float x = s[mt][i >> 2][i & 3] * f;
+        if (!whole) {
+          const int key = key0 + i;
+          const bool seen = r.ok && key >= from[mt] && key < upto[mt];
+          mn = fminf(mn, seen ? x : -kNegInf);
+          x = seen ? x : kNegInf;
+        } else {
+          mn = fminf(mn, x);
+        }
+        mx = fmaxf(mx, x);
+        s[mt][i >> 2][i & 3] = x;
+      }
+      const float now = fmaxf(m[mt], max_xor16(max_xor32(mx)));
+      ref[mt] = now == kNegInf ? 0.0f : now;
+      const float alpha = __builtin_amdgcn_exp2f(m[mt] - ref[mt]);
+      m[mt] = now;
+      l[mt] *= alpha;
+      low |= __builtin_amdgcn_exp2f(mn - ref[mt] + kLift) * share < kF16Normal;
+      const float down = alpha * shrink;
+#pragma unroll
+      for (int db = 0; db < DB; ++db) acc[mt][db] *= down;
+    }
+    const bool any_low = __any(low);
+    u4 pf[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float sum = 0.0f;
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float p0 = __builtin_amdgcn_exp2f(s[mt][i >> 2][i & 3] - ref[mt] + kLift);
+        float p1 = __builtin_amdgcn_exp2f(s[mt][i >> 2][(i & 3) + 1] - ref[mt] + kLift);
+        sum += p0 + p1;
+        p0 *= share;
+        p1 *= share;
+        if (any_low) {  // kept for the second product
+          s[mt][i >> 2][i & 3] = p0;
+          s[mt][i >> 2][(i & 3) + 1] = p1;
+          p0 = p0 < kF16Normal ? 0.0f : p0;
+          p1 = p1 < kF16Normal ? 0.0f : p1;
+        }
+        const h2 pk = {static_cast<_Float16>(p0), static_cast<_Float16>(p1)};
+        w[i / 2] = as_u32(pk);
+      }
+      l[mt] += sum;
+      pf[mt][0] = u4{w[0], w[1], w[2], w[3]};
+      pf[mt][1] = u4{w[4], w[5], w[6], w[7]};
+    }
+#pragma unroll
+    for (int db = 0; db < DB; ++db) {
+      const u4 w = r.v[db];
+      const h8 v0 = as_h8(codes8_f16(w.x, w.y, magic)), v1 = as_h8(codes8_f16(w.z, w.w, magic));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        acc[mt][db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, as_h8(pf[mt][0]), acc[mt][db], 0, 0, 0);
+        acc[mt][db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, as_h8(pf[mt][1]), acc[mt][db], 0, 0, 0);
+      }
+    }
+    // values below f16's normal range: products of their own, 2^24, 2^48, ..
+    // times larger, until none is left (an f32 weight ends at 2^-126)
+    float floor = kF16Normal, lift = kLowLift;
+    for (bool more = any_low; more; floor *= 1.0f / kLowLift, lift *= kLowLift) {
+      bool left = false;
+      const float next = floor * (1.0f / kLowLift);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float p0 = s[mt][i >> 2][i & 3], p1 = s[mt][i >> 2][(i & 3) + 1];
+          left |= (p0 > 0.0f && p0 < next) || (p1 > 0.0f && p1 < next);
+          const h2 pk = {static_cast<_Float16>(p0 < floor && p0 >= next ? p0 * lift : 0.0f),
+                         static_cast<_Float16>(p1 < floor && p1 >= next ? p1 * lift : 0.0f)};
+          w[i / 2] = as_u32(pk);
+        }
+        pf[mt][0] = u4{w[0], w[1], w[2], w[3]};
+        pf[mt][1] = u4{w[4], w[5], w[6], w[7]};
+      }
+      more = __any(left);
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        const u4 w = r.v[db];
+        const h8 v0 = as_h8(codes8_f16(w.x, w.y, magic)), v1 = as_h8(codes8_f16(w.z, w.w, magic));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          f4 t = f4{0, 0, 0, 0};
+          t = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, as_h8(pf[mt][0]), t, 0, 0, 0);
+          t = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, as_h8(pf[mt][1]), t, 0, 0, 0);
+          acc[mt][db] += t * (1.0f / lift);
+        }
+      }
+    }
+  };
+
+  int c = c_begin + wave;
+  if (c < c_end) {
+    Raw<DIM> cur, next;
+    Pages ahead = pages_of(c);
+    load(c, ahead, cur);
+    ahead = pages_of(c + kFewWaves);   // past the end: -1 or a page that is not used
+    for (; c < c_end; c += kFewWaves) {
+      const bool more = c + kFewWaves < c_end;
+      if (more) {
+        load(c + kFewWaves, ahead, next);
+        ahead = pages_of(c + 2 * kFewWaves);
+      }
+      compute(c, cur);
+      if (more) cur = next;
+    }
+  }
+
+  // join the waves, 16 rows at a time
+  const bool alone = part.splits == 1;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const float weight = add_xor16(add_xor32(l[mt]));
+    if (h == 0) {
+      join_m[wave][rho] = m[mt];
+      join_l[wave][rho] = weight;
+    }
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+      *reinterpret_cast<f4*>(&join[wave][rho][db * 16 + h * 4]) = acc[mt][db] * top_vs;
+    __syncthreads();
+    for (int u = threadIdx.x; u < 16 * (DIM / 4); u += kFewThreads) {
+      const int row = u / (DIM / 4), d = (u - row * (DIM / 4)) * 4, i = mt * 16 + row;
+      if (i < rows) {
+        float top = join_m[0][row];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) top = fmaxf(top, join_m[w][row]);
+        const float ref = top == kNegInf ? 0.0f : top;
+        f4 y = f4{0, 0, 0, 0};
+        float total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) {
+          const float e = __builtin_amdgcn_exp2f(join_m[w][row] - ref);
+          y += *reinterpret_cast<const f4*>(&join[w][row][d]) * e;
+          total += join_l[w][row] * e;
+        }
+        if (alone) {
+          const int tok = (row0 + i) / a.group, hq = head * a.group + (row0 + i) - tok * a.group;
+          const int64_t at = static_cast<int64_t>(sp.t0 + tok) * a.heads + hq;
+          const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+          uint16_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e] * inv);
+          *reinterpret_cast<uint2*>(a.out + at * DIM + d) =
+              uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
+                    static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
+          if (a.lse && d == 0) a.lse[at] = log_sum(ref, total);
+        } else {
+          const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + i;
+          *reinterpret_cast<f4*>(a.part + at * DIM + d) = y;
+          if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = float2{top, total};
+        }
+      }
+    }
+    if (mt + 1 < MT) __syncthreads();
+  }
+}
+
+// One workgroup for each (token, query head): the parts of its row, 4 values a
+// lane, the parts dealt over the workgroup's groups of DIM / 4 lanes.
+template <int DIM, int MT, bool BF16>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
+  constexpr int kLanes = DIM / 4, kTeams = 256 / kLanes, kRows = 16 * MT;
+  __shared__ float sums[kTeams][DIM];
+  __shared__ float team_m[kTeams], team_l[kTeams];
+  const int tok = blockIdx.x, hq = blockIdx.y;
+  int seq = tok;
+  if (a.starts != nullptr) {   // the last sequence that starts at or before the token
+    int lo = 0, hi = a.seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.starts[mid] <= tok) lo = mid; else hi = mid;
+    }
+    seq = lo;
+    const SeqSpan q = seq_span(a, seq);
+    if (tok < q.t0 || tok >= q.t0 + q.n || static_cast<int64_t>(q.n) * a.group > a.few_rows) return;
+  }
+  const Part part = find_part<MT>(a, -1, seq);
+  if (part.splits == 1) return;
+  const SeqSpan sp = seq_span(a, seq);
+  const int hk = a.pool.kv_heads, head = hq / a.group;
+  const int i = (tok - sp.t0) * a.group + hq - head * a.group, rg = i / kRows, row = i - rg * kRows;
+  const int team = threadIdx.x / kLanes, d = (threadIdx.x - team * kLanes) * 4;
+  float top = kNegInf, total = 0.0f;
+  f4 y = f4{0, 0, 0, 0};
+  for (int s = team; s < part.splits; s += kTeams) {
+    const int64_t at = (part.base + (static_cast<int64_t>(s) * part.share.groups + rg) * hk + head) * kRows + row;
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+    const f4 v = *reinterpret_cast<const f4*>(a.part + at * DIM + d);
+    const float now = fmaxf(top, ml.x), ref = now == kNegInf ? 0.0f : now;
+    const float e0 = __builtin_amdgcn_exp2f(top - ref), e1 = __builtin_amdgcn_exp2f(ml.x - ref);
+    y = y * e0 + v * e1;
+    total = total * e0 + ml.y * e1;
+    top = now;
+  }
+  *reinterpret_cast<f4*>(&sums[team][d]) = y;
+  if (d == 0) {
+    team_m[team] = top;
+    team_l[team] = total;
+  }
+  __syncthreads();
+  if (threadIdx.x >= kLanes) return;
+  top = team_m[0];
+#pragma unroll
+  for (int t = 1; t < kTeams; ++t) top = fmaxf(top, team_m[t]);
+  const float ref = top == kNegInf ? 0.0f : top;
+  y = f4{0, 0, 0, 0};
+  total = 0.0f;
+#pragma unroll
+  for (int t = 0; t < kTeams; ++t) {
+    const float e = __builtin_amdgcn_exp2f(team_m[t] - ref);
+    y += *reinterpret_cast<const f4*>(&sums[t][d]) * e;
+    total += team_l[t] * e;
+  }
+  const int64_t at = static_cast<int64_t>(tok) * a.heads + hq;
+  const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+  uint16_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e] * inv);
+  *reinterpret_cast<uint2*>(a.out + at * DIM + d) = uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
+                                                          static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
+  if (a.lse && d == 0) a.lse[at] = log_sum(ref, total);
+}
+
+namespace {
+
+template <int DIM, int MT>
+hipError_t launch_mt(const AttendArgs& a, unsigned slots, bool joined) {
+  if (a.bf16) hipLaunchKernelGGL((attend_few_kernel<DIM, MT, true>), dim3(slots), dim3(kFewThreads), 0, a.stream, a);
+  else hipLaunchKernelGGL((attend_few_kernel<DIM, MT, false>), dim3(slots), dim3(kFewThreads), 0, a.stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !joined) return e;
+  const dim3 grid(static_cast<unsigned>(a.tokens), static_cast<unsigned>(a.heads));
+  if (a.bf16) hipLaunchKernelGGL((attend_join_kernel<DIM, MT, true>), grid, dim3(256), 0, a.stream, a);
+  else hipLaunchKernelGGL((attend_join_kernel<DIM, MT, false>), grid, dim3(256), 0, a.stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_few(const AttendArgs& a, int mt, unsigned slots, bool joined) {
+  if (a.pool.dim == 64) return mt == 1 ? launch_mt<64, 1>(a, slots, joined) : mt == 2 ? launch_mt<64, 2>(a, slots, joined) : launch_mt<64, 4>(a, slots, joined);
+  return mt == 1 ? launch_mt<128, 1>(a, slots, joined) : mt == 2 ? launch_mt<128, 2>(a, slots, joined) : launch_mt<128, 4>(a, slots, joined);
+}
+
+}  // namespace
+
+hipError_t launch_attend(const AttendArgs& given, const DeviceInfo& dev) {
+  AttendArgs a = given;
+  if (a.pool.blocks == 0) a.width = 0;  // no page exists: every row is empty
+  a.few_rows = INT_MAX;
+  a.target = dev.num_cu * 4;
+  const int64_t most = a.starts == nullptr ? a.group : static_cast<int64_t>(a.tokens) * a.group;
+  const int mt = most <= 16 ? 1 : most <= 32 ? 2 : 4;
+  // slots: at most `target` full parts, and one more for each (sequence, group of rows, kv head)
+  const int64_t rows = static_cast<int64_t>(a.tokens) * a.group, per = 16 * mt;
+  const int64_t ends = (rows / per + a.seqs) * a.pool.kv_heads;
+  const int64_t slots = ends + a.target;
+  if (slots > INT32_MAX) return hipErrorInvalidValue;
+  const bool joined = static_cast<int64_t>(a.width) * a.pool.block > kMinChunks * kChunk;
+  if (!joined) return launch_few(a, mt, static_cast<unsigned>(ends), false);
+  const size_t sums = static_cast<size_t>(slots) * per * a.pool.dim * 4, bytes = sums + static_cast<size_t>(slots) * per * 8;
+  return with_split_workspace(dev, a.stream, bytes, [&](float* ws) {
+    a.part = ws;
+    a.part_ml = ws + sums / 4;
+    return launch_few(a, mt, static_cast<unsigned>(slots), true);
+  });
+}
+
+}  // namespace mxq

@@ -124,4 +124,50 @@ mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_tok
   return finish("mxq_kv_append", mxq::launch_kv_append(a));
 }
 
+mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const mxq_kv_cache* cache,
+                         const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
+                         const int32_t* starts, int64_t tokens, int64_t seqs, int heads, int64_t window,
+                         float scale, void* out, float* lse, mxq_dtype dtype, void* stream) {
+  mxq::clear_error();
+  mxq::AttendArgs a{};
+  mxq_status st = check_pool("mxq_attention", cache, &a.pool);
+  if (st != MXQ_OK) return st;
+  if (!half_type(dtype)) return report(MXQ_ERR_UNSUPPORTED, "mxq_attention: q must be MXQ_F16 or MXQ_BF16");
+  if (heads < 0 || window < 0) return report(MXQ_ERR_INVALID_ARG, "mxq_attention: heads and window must be >= 0");
+  if (heads > 65535) return report(MXQ_ERR_UNSUPPORTED, "mxq_attention: heads must be below 2^16");
+  if (heads > 0 && (a.pool.kv_heads == 0 || heads % a.pool.kv_heads != 0))
+    return report(MXQ_ERR_UNSUPPORTED, "mxq_attention: heads must be a multiple of the cache's kv_heads");
+  if (heads == 0) return MXQ_OK;
+  if (!(scale - scale == 0.0f)) return report(MXQ_ERR_INVALID_ARG, "mxq_attention: scale must be finite");
+  st = check_paging("mxq_attention", a.pool, table, table_stride, width, lens, starts, tokens, seqs);
+  if (st != MXQ_OK) return st;
+  if (tokens == 0 || seqs == 0) return MXQ_OK;
+  if (tokens * heads > INT32_MAX) return report(MXQ_ERR_UNSUPPORTED, "mxq_attention: tokens * heads must be below 2^31");
+  if (!q || !out) return report(MXQ_ERR_INVALID_ARG, "mxq_attention: null pointer");
+  if (!aligned(q, 16) || ((q_token | q_head) & 7) != 0 || !aligned(out, 8) || !aligned(lse, 4))
+    return report(MXQ_ERR_MISALIGNED,
+                  "mxq_attention: rows of q must be 16-byte, out 8-byte and lse 4-byte aligned");
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.width = static_cast<int>(width);
+  a.lens = lens;
+  a.starts = starts;
+  a.tokens = static_cast<int>(tokens);
+  a.seqs = static_cast<int>(seqs);
+  a.heads = heads;
+  a.group = heads / a.pool.kv_heads;
+  a.window = static_cast<int>(window > INT32_MAX ? 0 : window);
+  a.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  a.bf16 = dtype == MXQ_BF16;
+  a.stream = static_cast<hipStream_t>(stream);
+  mxq::DeviceInfo dev;
+  const hipError_t e = mxq::device_info(&dev);
+  return finish("mxq_attention", e != hipSuccess ? e : mxq::launch_attend(a, dev));
+}
+
 }  // extern "C"

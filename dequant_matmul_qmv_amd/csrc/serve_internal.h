@@ -15,6 +15,31 @@ void clear_error();
 mxq_status report(mxq_status s, const std::string& msg);
 mxq_status report_hip(const char* who, hipError_t e);
 
+// Runs `enqueue(workspace)` with `bytes` of device memory that stay the
+// stream's own until what it enqueues is done: the split workspace cache
+// (workspace.cpp), or, on a stream being captured, memory of the graph.
+// hipErrorOutOfMemory, with nothing enqueued, where none can be had.
+template <typename F>
+hipError_t with_split_workspace(const DeviceInfo& dev, hipStream_t stream, size_t bytes, F enqueue) {
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &cap) != hipSuccess) {
+    (void)hipGetLastError();
+    cap = hipStreamCaptureStatusNone;
+  }
+  if (cap == hipStreamCaptureStatusNone) {
+    std::lock_guard<std::mutex> lk(split_workspace_mutex());
+    float* ws = split_workspace_locked(dev.device, stream, bytes);
+    return ws == nullptr ? hipErrorOutOfMemory : enqueue(ws);
+  }
+  void* ws = nullptr;
+  if (hipMallocAsync(&ws, bytes, stream) != hipSuccess) {
+    (void)hipGetLastError();
+    return hipErrorOutOfMemory;
+  }
+  const hipError_t e = enqueue(static_cast<float*>(ws)), f = hipFreeAsync(ws, stream);
+  return e != hipSuccess ? e : f;
+}
+
 // q and k views: [tokens, heads, dim] with element strides for tokens and
 // heads, the last dimension contiguous.  Null with 0 heads: absent.
 struct RopeSide {
@@ -60,5 +85,31 @@ struct KvAppendArgs {
   hipStream_t stream;
 };
 hipError_t launch_kv_append(const KvAppendArgs& a);
+
+// Attention of new tokens over the cache.  Partial results of a key range, one
+// slot a workgroup: rows of dim f32 sums, then their maxima and weights.
+struct AttendArgs {
+  KvPool pool;
+  const uint16_t* q;
+  int64_t q_token, q_head;
+  uint16_t* out;          // [tokens, heads, dim]
+  float* lse;             // [tokens, heads] or null
+  const int32_t* table;
+  int64_t table_stride;
+  int width;
+  const int32_t* lens;
+  const int32_t* starts;  // null: one token for each sequence
+  int tokens, seqs, heads, group;  // group: query heads of one kv head
+  int window;             // 0: none
+  float scale2;           // softmax scale times log2(e)
+  bool bf16;
+  hipStream_t stream;
+  // set by the launcher
+  float* part;            // sums [slots, rows, dim]
+  float* part_ml;         // (maximum, weight) [slots, rows, 2]
+  int target;             // workgroups the work is split for
+  int few_rows;           // most rows (new tokens times group) of a sequence that the few-row kernel takes
+};
+hipError_t launch_attend(const AttendArgs& a, const DeviceInfo& dev);
 
 }  // namespace mxq

@@ -328,6 +328,32 @@ mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_tok
                          int64_t tokens, int64_t seqs, mxq_dtype dtype, void* stream);
 
 /*
+ * mxq_attention -- causal attention of new tokens over the 8-bit cache (which
+ * holds them already: mxq_kv_append comes first).
+ *
+ *   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[t, h] . k_j),
+ * over the keys j of t's sequence with j <= pos(t), j > pos(t) - window where
+ * window > 0, and an existing page (a table entry in 0 .. blocks - 1); query
+ * head h reads kv head h / (heads / kv_heads).  pos(t) is lens[s] minus the
+ * number of the sequence's new tokens from t on.  A row without keys gives 0.
+ * Sequences, their rows and their table as for mxq_kv_append.
+ *   q    f16|bf16, element (t, h, d) at t * q_token + h * q_head + d, rows
+ *        16-byte aligned (strides multiples of 8)
+ *   out  the same type [tokens, heads, dim], 8-byte aligned
+ *   lse  f32 [tokens, heads] or null: log sum_j p_j (-inf for a row without keys)
+ * Rows of q and out that no sequence covers are neither read nor written.
+ * Products of q and codes are exact, sums, maxima and weights f32, the
+ * probabilities f16 relative to their row's largest (a bf16 q's smallest values
+ * are rounded at 2^-25 of its row's largest).  Results are the same bits from
+ * run to run.  Partial results of a split key axis go to the split workspace
+ * (see above); MXQ_ERR_HIP if that cannot be had.
+ */
+mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const mxq_kv_cache* cache,
+                         const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
+                         const int32_t* starts, int64_t tokens, int64_t seqs, int heads, int64_t window,
+                         float scale, void* out, float* lse, mxq_dtype dtype, void* stream);
+
+/*
  * mxq_dequant -- standalone dequantization: out[n, k] = q * s + b.
  *
  * The reconstruction mlxcel #574 ("What is already in-tree") requires to be

@@ -78,3 +78,46 @@ def append_ref(pool, k, v, table, lens, new, block):
                     scales[page, h] = now
         at += n
     return kc, vc, ks, vs
+
+
+def attention_ref(q, pool, table, lens, new, window, scale):
+    """(out, lse, error scale of out, of lse) of the definition in float64, row by row."""
+    kc, vc, ks, vs = (t.double().numpy() for t in pool)
+    n, heads, dim = q.shape
+    blocks, hk, block, _ = kc.shape
+    group = heads // hk
+    qd = q.double().numpy()
+    out, lse = np.zeros((n, heads, dim)), np.full((n, heads), -np.inf)
+    off, loff = np.zeros((n, heads, dim)), np.zeros((n, heads))
+    at = 0
+    for s, (length, nn) in enumerate(zip(lens, new)):
+        pages = [int(table[s, j]) if j < table.shape[1] else -1 for j in range(-(-length // block))]
+        there = np.array([0 <= p < blocks for p in pages], bool)
+        ids = np.where(there, pages, 0).astype(int) if pages else np.zeros(0, int)
+        seen_page = np.repeat(there, block)[:length]
+        for h in range(hk):
+            k = (kc[ids, h] * ks[ids, h][:, None, None]).reshape(-1, dim)[:length]
+            v = (vc[ids, h] * vs[ids, h][:, None, None]).transpose(0, 2, 1).reshape(-1, dim)[:length]
+            for i in range(nn):
+                pos = length - nn + i
+                j = np.arange(length)
+                see = seen_page & (j <= pos) & ((j > pos - window) if window else True)
+                if not see.any():
+                    continue
+                for g in range(group):
+                    row = qd[at + i, h * group + g]
+                    x = scale * (k[see] @ row)
+                    top = x.max()
+                    p = np.exp(x - top)
+                    l = p.sum()
+                    o = (at + i, h * group + g)
+                    out[o] = p @ v[see] / l
+                    lse[o] = top + np.log(l)
+                    # f32: sums of dim products, the scores' roundings, exp2; q's own 2^-25 for bf16
+                    a = abs(scale) * np.abs(k[see] * row).sum(1).max()
+                    aq = abs(scale) * np.abs(row).max() * np.abs(k[see]).sum(1).max()
+                    d = 2 * ((dim + 8) * 2.0 ** -24 * a + 2.0 ** -24 * aq + 2.0 ** -18)
+                    off[o] = (2.0 ** -11 + 2 * d) * (p @ np.abs(v[see])) / l
+                    loff[o] = d + 2.0 ** -22 * (abs(lse[o]) + 20)
+        at += nn
+    return out, lse, off, loff
