@@ -8,7 +8,7 @@ launch), ``mxq_qmm`` (prefill), ``mxq_linear`` (either, plus an output bias),
 ``mxq_dequant`` (bit-exact standalone dequant) and ``mxq_pack`` (host packer),
 the serving operators around the projections, ``mxq_rope`` (rotary positions),
 ``KvCache`` and ``mxq_kv_append`` (an 8-bit paged key/value cache),
-``mxq_attention`` (over that cache),
+``mxq_attention`` (over that cache), ``mxq_sample`` (the next token from logits),
 plus diagnostics (``mxq_describe``, ``mxq_describe_grouped``) and the split
 workspace controls (``mxq_release_workspaces``, ``mxq_workspace_bytes``).
 """
@@ -41,7 +41,7 @@ from ._lib import (  # noqa: F401
 )
 
 # the serving operators, bound on first use: their module needs torch, which the rest imports inside its calls
-_SERVE = ("KvCache", "mxq_attention", "mxq_kv_append", "mxq_rope")
+_SERVE = ("KvCache", "mxq_attention", "mxq_kv_append", "mxq_rope", "mxq_sample")
 
 
 def __getattr__(name):

@@ -15,9 +15,10 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import MXQ_BF16, MXQ_F16
+from ._lib import MXQ_BF16, MXQ_F16, MXQ_F32
 
 _HALF = {torch.float16: MXQ_F16, torch.bfloat16: MXQ_BF16}
+_LOGITS = {torch.float16: MXQ_F16, torch.bfloat16: MXQ_BF16, torch.float32: MXQ_F32}
 _i32 = torch.int32
 _f32 = torch.float32
 
@@ -28,6 +29,14 @@ class _CacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("blocks", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
                 ("block", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class _SamplingStruct(ctypes.Structure):
+    """ctypes mirror of ``mxq_sampling`` (include/mxq.h)."""
+
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
 
 
 _fn = None
@@ -44,7 +53,8 @@ def _load():
         lib.mxq_kv_append.argtypes = [cache, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64, i32, vp]
         lib.mxq_attention.argtypes = [vp, i64, i64, cache, vp, i64, i64, vp, vp, i64, i64, i32, i64, ctypes.c_float, vp,
                                       vp, i32, vp]
-        for f in (lib.mxq_rope, lib.mxq_kv_append, lib.mxq_attention):
+        lib.mxq_sample.argtypes = [vp, i64, i64, i64, i32, vp, ctypes.POINTER(_SamplingStruct), vp, vp, vp]
+        for f in (lib.mxq_rope, lib.mxq_kv_append, lib.mxq_attention, lib.mxq_sample):
             f.restype = i32
         _fn = lib
     return _fn
@@ -261,3 +271,48 @@ def mxq_attention(q, cache, table, lens, starts=None, out=None, *, window: int =
           n, seqs, heads, window, dim ** -0.5 if scale is None else scale, out.data_ptr(),
           None if lse is None else lse.data_ptr(), code)
     return (out, lse) if return_lse else out
+
+
+def _setting(who, name, value, rows, dtype, dev):
+    """(pointer, value for all) of a setting given as a tensor of one value a row, or as a number."""
+    if isinstance(value, torch.Tensor):
+        if value.dtype != dtype or tuple(value.shape) != (rows,) or not value.is_contiguous() or value.device != dev:
+            raise ValueError(f"{who}: {name} must be a number or a contiguous "
+                             f"{str(dtype).replace('torch.', '')} tensor [{rows}] on {dev}")
+        return value.data_ptr(), 0
+    return None, value
+
+
+def mxq_sample(logits, u, tokens=None, probs=None, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+    """One token for each row of ``logits`` [rows, vocab] (f16, bf16 or f32), drawn by the uniform numbers ``u`` [rows].
+
+    ``temperature`` (<= 0: the largest logit), ``top_k`` (<= 0: off), ``top_p`` (>= 1: off) and ``min_p`` (<= 0: off)
+    are numbers, or tensors of one value a row (float32; top_k int32).  Returns (tokens int32, probs float32), each
+    token's probability being that among the kept ones.  The rule, ties included, is in include/mxq.h."""
+    who = "mxq_sample"
+    dev = _device(who, "logits", logits)
+    code = _LOGITS.get(logits.dtype)
+    if code is None or logits.dim() != 2:
+        raise TypeError(f"{who}: logits must be a 2-D float16, bfloat16 or float32 tensor [rows, vocab]")
+    rows, vocab = logits.shape
+    row, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError(f"{who}: logits' rows must be contiguous")
+    if u.dtype != _f32 or tuple(u.shape) != (rows,) or not u.is_contiguous() or u.device != dev:
+        raise ValueError(f"{who}: u must be a contiguous float32 tensor [{rows}] on {dev}")
+    t, t_all = _setting(who, "temperature", temperature, rows, _f32, dev)
+    k, k_all = _setting(who, "top_k", top_k, rows, _i32, dev)
+    p, p_all = _setting(who, "top_p", top_p, rows, _f32, dev)
+    m, m_all = _setting(who, "min_p", min_p, rows, _f32, dev)
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=_i32, device=dev)
+    else:
+        _ints(who, "tokens", tokens, (rows,))
+    if probs is None:
+        probs = torch.empty(rows, dtype=_f32, device=dev)
+    elif probs.dtype != _f32 or tuple(probs.shape) != (rows,) or not probs.is_contiguous():
+        raise ValueError(f"{who}: probs must be a contiguous float32 tensor [{rows}]")
+    _on(who, dev, tokens=tokens, probs=probs)
+    _call(_load().mxq_sample, dev, stream, logits.data_ptr(), row, rows, vocab, code, u.data_ptr(),
+          _SamplingStruct(t, k, p, m, t_all, k_all, p_all, m_all), tokens.data_ptr(), probs.data_ptr())
+    return tokens, probs

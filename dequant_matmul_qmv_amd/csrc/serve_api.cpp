@@ -170,4 +170,42 @@ mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const m
   return finish("mxq_attention", e != hipSuccess ? e : mxq::launch_attend(a, dev));
 }
 
+mxq_status mxq_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab, mxq_dtype dtype,
+                      const float* u, const mxq_sampling* settings, int32_t* tokens, float* probs, void* stream) {
+  mxq::clear_error();
+  if (rows < 0 || vocab < 0) return report(MXQ_ERR_INVALID_ARG, "mxq_sample: rows and vocab must be >= 0");
+  if (dtype != MXQ_F16 && dtype != MXQ_BF16 && dtype != MXQ_F32)
+    return report(MXQ_ERR_UNSUPPORTED, "mxq_sample: logits must be MXQ_F16, MXQ_BF16 or MXQ_F32");
+  if (vocab > (1 << 20)) return report(MXQ_ERR_UNSUPPORTED, "mxq_sample: vocab must be at most 2^20");
+  if (rows > (1 << 24)) return report(MXQ_ERR_UNSUPPORTED, "mxq_sample: rows must be at most 2^24");
+  if (rows == 0) return MXQ_OK;
+  if (vocab == 0) return report(MXQ_ERR_INVALID_ARG, "mxq_sample: nothing to draw from (vocab is 0)");
+  if (!logits || !u || !settings || !tokens || !probs) return report(MXQ_ERR_INVALID_ARG, "mxq_sample: null pointer");
+  if (rows > 1 && row_stride < vocab)
+    return report(MXQ_ERR_INVALID_ARG, "mxq_sample: rows overlap (row_stride < vocab)");
+  if (!aligned(logits, dtype == MXQ_F32 ? 4 : 2) || !aligned(u, 4) || !aligned(tokens, 4) || !aligned(probs, 4) ||
+      !aligned(settings->temperature, 4) || !aligned(settings->top_k, 4) || !aligned(settings->top_p, 4) ||
+      !aligned(settings->min_p, 4))
+    return report(MXQ_ERR_MISALIGNED, "mxq_sample: a pointer is not aligned to its elements");
+  mxq::SampleArgs a{};
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.rows = static_cast<int>(rows);
+  a.vocab = static_cast<int>(vocab);
+  a.type = static_cast<int>(dtype);
+  a.u = u;
+  a.temperature = settings->temperature;
+  a.top_k = settings->top_k;
+  a.top_p = settings->top_p;
+  a.min_p = settings->min_p;
+  a.temperature_all = settings->temperature_all;
+  a.top_k_all = settings->top_k_all;
+  a.top_p_all = settings->top_p_all;
+  a.min_p_all = settings->min_p_all;
+  a.tokens = tokens;
+  a.probs = probs;
+  a.stream = static_cast<hipStream_t>(stream);
+  return finish("mxq_sample", mxq::launch_sample(a));
+}
+
 }  // extern "C"

@@ -112,4 +112,25 @@ struct AttendArgs {
 };
 hipError_t launch_attend(const AttendArgs& a, const DeviceInfo& dev);
 
+// One draw for each row of logits.  Settings: arrays of a value for each row,
+// or (null) one value for all.
+struct SampleArgs {
+  const void* logits;
+  int64_t row_stride;  // elements
+  int rows, vocab;
+  int type;            // mxq_dtype value
+  const float* u;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all;
+  int top_k_all;
+  float top_p_all, min_p_all;
+  int32_t* tokens;
+  float* probs;
+  hipStream_t stream;
+};
+hipError_t launch_sample(const SampleArgs& a);
+
 }  // namespace mxq

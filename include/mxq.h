@@ -354,6 +354,44 @@ mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const m
                          float scale, void* out, float* lse, mxq_dtype dtype, void* stream);
 
 /*
+ * The settings of mxq_sample: device arrays of one value a row, or (null) the
+ * value for all rows.
+ */
+typedef struct mxq_sampling {
+  const float* temperature;  /* <= 0 or NaN: the largest logit */
+  const int32_t* top_k;      /* <= 0: no limit */
+  const float* top_p;        /* >= 1: no limit */
+  const float* min_p;        /* <= 0: no limit */
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all;
+  float min_p_all;
+} mxq_sampling;
+
+/*
+ * mxq_sample -- one token for each row of logits.
+ *
+ * With w_i = exp((x_i - max x) / temperature) and the tokens in descending
+ * order of their logits, equals by index, a token is kept if
+ *   its place is among the first top_k,
+ *   the weight of those before it is below top_p of the weight of the top_k,
+ *   w_i >= min_p;
+ * the first token always is.  tokens[r] is the first, in index order, whose
+ * running sum of kept weights exceeds u[r] times their total, u in [0, 1)
+ * (beyond: the last kept one); probs[r] its weight over that total.  A
+ * temperature <= 0 takes the largest logit, the first of equals, at
+ * probability 1; so do top_p <= 0 or NaN and min_p > 1 or NaN.  A NaN logit
+ * counts as -inf; a row of nothing but -inf is uniform.  Weights are taken in
+ * f64 and summed exactly in steps of 2^-43: the draw does not depend on the
+ * order of summation and is the same from run to run.
+ *   logits  f16|bf16|f32, row r at r * row_stride, 1 <= vocab <= 2^20
+ *   u       f32 [rows];  tokens i32 [rows];  probs f32 [rows]
+ * `settings` is a host structure, read during the call.
+ */
+mxq_status mxq_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab, mxq_dtype dtype,
+                      const float* u, const mxq_sampling* settings, int32_t* tokens, float* probs, void* stream);
+
+/*
  * mxq_dequant -- standalone dequantization: out[n, k] = q * s + b.
  *
  * The reconstruction mlxcel #574 ("What is already in-tree") requires to be

@@ -121,3 +121,34 @@ def attention_ref(q, pool, table, lens, new, window, scale):
                     loff[o] = d + 2.0 ** -22 * (abs(lse[o]) + 20)
         at += nn
     return out, lse, off, loff
+
+
+def sample_ref(x, u, temperature, top_k, top_p, min_p):
+    """(token, probability, distance of the nearest border) of one row in float64: the tokens in descending order,
+    equals by index, cut to the kept prefix, one drawn in index order.  The distance, relative to the total, is that
+    of u's border and of top_p's and min_p's."""
+    x = x.astype(np.float64)
+    x = np.where(np.isnan(x), -np.inf, x)
+    order = np.argsort(-x, kind="stable")
+    top = x[order[0]]
+    if not temperature > 0 or not top_p > 0 or not min_p <= 1:
+        return int(order[0]), 1.0, 1.0
+    with np.errstate(invalid="ignore"):
+        w = np.where(x == top, 1.0, np.exp((x - top) / np.float64(temperature)))
+    s = w[order]
+    keep = len(s) if top_k <= 0 else min(len(s), top_k)
+    near = 1.0
+    if top_p < 1:
+        mass = np.cumsum(s[:keep])
+        at = np.float64(top_p) * mass[-1]
+        near = min(near, float(np.abs(mass - at).min() / mass[-1]))
+        keep = 1 + int((mass[:-1] < at).sum())
+    if min_p > 0:
+        near = min(near, float(np.abs(s - np.float64(min_p)).min()))
+        keep = max(1, min(keep, int((s >= np.float64(min_p)).sum())))
+    ids = np.sort(order[:keep])
+    mass = np.cumsum(w[ids])
+    at = np.float64(u) * mass[-1]
+    near = min(near, float(np.abs(mass - at).min() / mass[-1]))
+    i = min(keep - 1, int((mass <= at).sum()))
+    return int(ids[i]), float(w[ids[i]] / mass[-1]), near
