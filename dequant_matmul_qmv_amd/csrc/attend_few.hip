@@ -112,6 +112,7 @@ __device__ Part find_part(const AttendArgs& a, int slot, int seq) {
   return p;
 }
 
+// One lane's part of a chunk, as stored.
 template <int DIM>
 struct Raw {
   u4 k[4 * (DIM / 64)];
@@ -120,6 +121,13 @@ struct Raw {
   bool ok;
 };
 
+// Registers as if rewritten: what is computed from them again is not shared
+// with, or kept from, an earlier computation.
+__device__ __forceinline__ u4 anew(u4 w) {
+  asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+  return w;
+}
+
 struct Pages {
   int k, v;   // pages of the lane's k rows and of its v tokens; -1: none
 };
@@ -127,7 +135,7 @@ struct Pages {
 }  // namespace
 
 template <int DIM, int MT, bool BF16>
-__global__ __launch_bounds__(kFewThreads, MT * DIM > 256 ? 1 : 2) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_few_kernel(AttendArgs a) {
   constexpr int U = DIM / 64, DB = DIM / 16, kRows = 16 * MT;
   __shared__ float join[kFewWaves][16][DIM + 4];
   __shared__ float join_m[kFewWaves][16], join_l[kFewWaves][16];
@@ -195,22 +203,25 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM > 256 ? 1 : 2) void attend_fe
     p.v = jv < a.width ? table[jv] : -1;
     return p;
   };
-  auto load = [&](int c, Pages p, Raw<DIM>& r) {
-    const int nb = static_cast<int>(a.pool.blocks);
-    // a page past the sequence's end may be anyone's, or never written
-    r.ok = p.v >= 0 && p.v < nb && c * kChunk + h * 16 < limit;
-    const int64_t pk = p.k >= 0 && p.k < nb ? p.k : 0, pv = r.ok ? p.v : 0;
-    const int tk = (c * kChunk + kgroup * 16) & (block - 1), tv = (c * kChunk + h * 16) & (block - 1);
+  auto load_k = [&](int c, Pages p, Raw<DIM>& r) {
+    const int64_t pk = p.k >= 0 && p.k < static_cast<int>(a.pool.blocks) ? p.k : 0;
+    const int tk = (c * kChunk + kgroup * 16) & (block - 1);
     const int8_t* kp = a.pool.k + ((pk * hk + head) * block + tk + (rho & 3)) * DIM + h * 16;
-    const int8_t* vp = a.pool.v + ((pv * hk + head) * DIM + rho) * block + tv;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int u = 0; u < U; ++u) r.k[b * U + u] = *reinterpret_cast<const u4*>(kp + b * 4 * DIM + u * 64);
-#pragma unroll
-    for (int db = 0; db < DB; ++db) r.v[db] = *reinterpret_cast<const u4*>(vp + db * 16 * block);
+  };
+  auto load_v = [&](int c, Pages p, Raw<DIM>& r) {
+    // a page past the sequence's end may be anyone's, or never written
+    r.ok = p.v >= 0 && p.v < static_cast<int>(a.pool.blocks) && c * kChunk + h * 16 < limit;
+    const int64_t pv = r.ok ? p.v : 0;
+    const int tv = (c * kChunk + h * 16) & (block - 1);
+    const int8_t* vp = a.pool.v + ((pv * hk + head) * DIM + rho) * block + tv;
     r.ks = a.pool.k_scale[pv * hk + head];
     r.vs = r.ok ? a.pool.v_scale[pv * hk + head] : 0.0f;
+#pragma unroll
+    for (int db = 0; db < DB; ++db) r.v[db] = *reinterpret_cast<const u4*>(vp + db * 16 * block);
   };
 
   f4 acc[MT][DB];
@@ -223,7 +234,10 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM > 256 ? 1 : 2) void attend_fe
     for (int db = 0; db < DB; ++db) acc[mt][db] = f4{0, 0, 0, 0};
   }
 
-  auto compute = [&](int c, const Raw<DIM>& r) {
+  // one chunk: as soon as k's registers are free they take the next chunk's
+  // rows, and v's do after the second product
+  auto step = [&](int c, Raw<DIM>& r, Pages& ahead) {
+    const bool more_chunks = c + kFewWaves < c_end;
     f4 s[MT][4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -240,6 +254,7 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM > 256 ? 1 : 2) void attend_fe
         }
       }
     }
+    if (more_chunks) load_k(c + kFewWaves, ahead, r);
     const float was_vs = top_vs;
     top_vs = fmaxf(top_vs, max_xor16(max_xor32(r.vs)));
     const float share = r.vs / top_vs, shrink = was_vs / top_vs;
@@ -334,7 +349,7 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM > 256 ? 1 : 2) void attend_fe
       more = __any(left);
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
-        const u4 w = r.v[db];
+        const u4 w = anew(r.v[db]);
         const h8 v0 = as_h8(codes8_f16(w.x, w.y, magic)), v1 = as_h8(codes8_f16(w.z, w.w, magic));
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -345,23 +360,20 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM > 256 ? 1 : 2) void attend_fe
         }
       }
     }
+    if (more_chunks) {
+      load_v(c + kFewWaves, ahead, r);
+      ahead = pages_of(c + 2 * kFewWaves);
+    }
   };
 
   int c = c_begin + wave;
   if (c < c_end) {
-    Raw<DIM> cur, next;
+    Raw<DIM> raw;
     Pages ahead = pages_of(c);
-    load(c, ahead, cur);
-    ahead = pages_of(c + kFewWaves);   // past the end: -1 or a page that is not used
-    for (; c < c_end; c += kFewWaves) {
-      const bool more = c + kFewWaves < c_end;
-      if (more) {
-        load(c + kFewWaves, ahead, next);
-        ahead = pages_of(c + 2 * kFewWaves);
-      }
-      compute(c, cur);
-      if (more) cur = next;
-    }
+    load_k(c, ahead, raw);
+    load_v(c, ahead, raw);
+    ahead = pages_of(c + kFewWaves);   // past the end: -1, or a page that is not used
+    for (; c < c_end; c += kFewWaves) step(c, raw, ahead);
   }
 
   // join the waves, 16 rows at a time
@@ -495,32 +507,59 @@ hipError_t launch_mt(const AttendArgs& a, unsigned slots, bool joined) {
 }
 
 hipError_t launch_few(const AttendArgs& a, int mt, unsigned slots, bool joined) {
-  if (a.pool.dim == 64) return mt == 1 ? launch_mt<64, 1>(a, slots, joined) : mt == 2 ? launch_mt<64, 2>(a, slots, joined) : launch_mt<64, 4>(a, slots, joined);
-  return mt == 1 ? launch_mt<128, 1>(a, slots, joined) : mt == 2 ? launch_mt<128, 2>(a, slots, joined) : launch_mt<128, 4>(a, slots, joined);
+  if (slots == 0) return hipSuccess;
+  if (a.pool.dim == 64) return mt == 1 ? launch_mt<64, 1>(a, slots, joined) : launch_mt<64, 2>(a, slots, joined);
+  return mt == 1 ? launch_mt<128, 1>(a, slots, joined) : launch_mt<128, 2>(a, slots, joined);
 }
+
+// Sequences of up to this many rows take the few-row kernel.
+constexpr int kFewRows = 64;
 
 }  // namespace
 
 hipError_t launch_attend(const AttendArgs& given, const DeviceInfo& dev) {
   AttendArgs a = given;
   if (a.pool.blocks == 0) a.width = 0;  // no page exists: every row is empty
-  a.few_rows = INT_MAX;
+  const int64_t all_rows = static_cast<int64_t>(a.tokens) * a.group, hk = a.pool.kv_heads;
+  // How many new tokens a sequence has is known on the GPU alone.  One kernel
+  // runs where that cannot matter; else both, each with its own sequences.
+  const bool few = a.starts == nullptr || a.seqs > 1 || all_rows <= kFewRows;
+  const bool many = a.starts != nullptr && all_rows > kFewRows;
+  a.few_rows = !many ? INT_MAX : few ? kFewRows : 0;
   a.target = dev.num_cu * 4;
-  const int64_t most = a.starts == nullptr ? a.group : static_cast<int64_t>(a.tokens) * a.group;
-  const int mt = most <= 16 ? 1 : most <= 32 ? 2 : 4;
+
+  const int64_t most = a.starts == nullptr ? a.group : all_rows < kFewRows ? all_rows : kFewRows;
+  const int mt = most <= 16 ? 1 : 2;
   // slots: at most `target` full parts, and one more for each (sequence, group of rows, kv head)
-  const int64_t rows = static_cast<int64_t>(a.tokens) * a.group, per = 16 * mt;
-  const int64_t ends = (rows / per + a.seqs) * a.pool.kv_heads;
-  const int64_t slots = ends + a.target;
+  int64_t few_total = all_rows;
+  if (many && few_total > static_cast<int64_t>(a.seqs) * kFewRows) few_total = static_cast<int64_t>(a.seqs) * kFewRows;
+  const int64_t per = 16 * mt, ends = few ? (few_total / per + a.seqs) * hk : 0;
+  const bool joined = few && static_cast<int64_t>(a.width) * a.pool.block > kMinChunks * kChunk;
+  const int64_t slots = ends + (joined ? a.target : 0);
   if (slots > INT32_MAX) return hipErrorInvalidValue;
-  const bool joined = static_cast<int64_t>(a.width) * a.pool.block > kMinChunks * kChunk;
-  if (!joined) return launch_few(a, mt, static_cast<unsigned>(ends), false);
-  const size_t sums = static_cast<size_t>(slots) * per * a.pool.dim * 4, bytes = sums + static_cast<size_t>(slots) * per * 8;
-  return with_split_workspace(dev, a.stream, bytes, [&](float* ws) {
+  const size_t sums = joined ? static_cast<size_t>(slots) * per * a.pool.dim * 4 : 0;
+  const size_t few_bytes = joined ? sums + static_cast<size_t>(slots) * per * 8 : 0;
+
+  // the many-row kernel's key axis is split while its tiles leave compute units idle
+  a.many_splits = 1;
+  if (many) {
+    const int64_t tiles = many_tiles(a) * hk, stages = (static_cast<int64_t>(a.width) * a.pool.block + kChunk - 1) / kChunk;
+    int64_t splits = tiles > 0 ? 2 * dev.num_cu / tiles : 1;
+    if (splits > stages / 4) splits = stages / 4;
+    if (splits > 32) splits = 32;
+    if (splits > 1) a.many_splits = static_cast<int>(splits);
+  }
+  const size_t many_bytes = many ? many_part_bytes(a) : 0;
+
+  const auto enqueue = [&](float* ws) {
     a.part = ws;
     a.part_ml = ws + sums / 4;
-    return launch_few(a, mt, static_cast<unsigned>(slots), true);
-  });
+    hipError_t e = many ? launch_many(a, ws + few_bytes / 4) : hipSuccess;
+    if (e == hipSuccess && few) e = launch_few(a, mt, static_cast<unsigned>(slots), joined);
+    return e;
+  };
+  if (few_bytes + many_bytes == 0) return enqueue(nullptr);
+  return with_split_workspace(dev, a.stream, few_bytes + many_bytes, enqueue);
 }
 
 }  // namespace mxq

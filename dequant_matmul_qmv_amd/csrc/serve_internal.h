@@ -107,9 +107,17 @@ struct AttendArgs {
   // set by the launcher
   float* part;            // sums [slots, rows, dim]
   float* part_ml;         // (maximum, weight) [slots, rows, 2]
-  int target;             // workgroups the work is split for
+  int target;             // workgroups the few-row work is split for
   int few_rows;           // most rows (new tokens times group) of a sequence that the few-row kernel takes
+  float* many_part;       // the same of the many-row kernel
+  float* many_ml;
+  int many_splits;        // parts of its key axis
 };
+// The many-row kernel (attend_many.hip): its tiles at most, the bytes of its
+// partial results, its launch (with the second one that joins them).
+int64_t many_tiles(const AttendArgs& a);
+size_t many_part_bytes(const AttendArgs& a);
+hipError_t launch_many(const AttendArgs& a, float* ws);
 hipError_t launch_attend(const AttendArgs& a, const DeviceInfo& dev);
 
 // One draw for each row of logits.  Settings: arrays of a value for each row,
