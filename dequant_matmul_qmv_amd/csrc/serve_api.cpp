@@ -205,7 +205,9 @@ mxq_status mxq_sample(const void* logits, int64_t row_stride, int64_t rows, int6
   a.tokens = tokens;
   a.probs = probs;
   a.stream = static_cast<hipStream_t>(stream);
-  return finish("mxq_sample", mxq::launch_sample(a));
+  mxq::DeviceInfo dev;
+  const hipError_t e = mxq::device_info(&dev);
+  return finish("mxq_sample", e != hipSuccess ? e : mxq::launch_sample(a, dev));
 }
 
 }  // extern "C"

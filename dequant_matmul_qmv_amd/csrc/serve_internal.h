@@ -138,7 +138,12 @@ struct SampleArgs {
   int32_t* tokens;
   float* probs;
   hipStream_t stream;
+  // set by the launcher
+  uint32_t* cells;     // largest key of each 64 tokens [rows, cell_count]
+  double* pieces;      // weight of each 512 tokens [rows, piece_count]
+  int cell_count, piece_count;
+  bool wide;           // rows are 16-byte aligned
 };
-hipError_t launch_sample(const SampleArgs& a);
+hipError_t launch_sample(const SampleArgs& a, const DeviceInfo& dev);
 
 }  // namespace mxq
