@@ -60,13 +60,17 @@ def _load():
     return _fn
 
 
+# The current stream's handle without the Stream object around it (1.7 us of a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
+
+
 def _call(f, dev, stream, *args):
     """f(*args, stream) with `dev` current; raises on a status other than OK."""
-    if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    else:
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    index = dev.index
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
         st = f(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -75,7 +79,8 @@ def _call(f, dev, stream, *args):
         _lib._check(_fn, st)
 
 
-def _on(who, dev, **tensors):
+def _elsewhere(who, dev, **tensors):
+    """Names the tensor that is not on `dev`."""
     for name, t in tensors.items():
         if t is not None and t.device != dev:
             raise ValueError(f"{who}: {name} must be on {dev}, is on {t.device}")
@@ -92,7 +97,7 @@ def _rows(who, name, t, dtype):
 
 
 def _ints(who, name, t, shape):
-    if t.dtype != _i32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != _i32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{who}: {name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
@@ -122,9 +127,12 @@ def mxq_rope(q, k, inv_freq, positions, q_out=None, k_out=None, *, interleaved: 
     if rot > dim:
         raise ValueError(f"{who}: {rot // 2} frequencies rotate {rot} values, a head has {dim}")
     _ints(who, "positions", positions, (n,))
-    _on(who, dev, k=k, inv_freq=inv_freq, positions=positions, q_out=q_out, k_out=k_out)
+    if inv_freq.device != dev or positions.device != dev:
+        _elsewhere(who, dev, inv_freq=inv_freq, positions=positions)
+    if k is not None and k.device != dev or q_out is not None or k_out is not None:
+        _elsewhere(who, dev, k=k, q_out=q_out, k_out=k_out)
     if q_out is None:
-        q_out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+        q_out = q.new_empty(q.shape)
     elif q_out.shape != q.shape:
         raise ValueError(f"{who}: q_out must have q's shape")
     qo = _rows(who, "q_out", q_out, q.dtype)
@@ -135,7 +143,7 @@ def mxq_rope(q, k, inv_freq, positions, q_out=None, k_out=None, *, interleaved: 
             raise ValueError(f"{who}: k must be [{n}, kv_heads, {dim}]")
         kv_heads = k.shape[1]
         if k_out is None:
-            k_out = torch.empty((n, kv_heads, dim), dtype=q.dtype, device=dev)
+            k_out = k.new_empty(k.shape)
         elif k_out.shape != k.shape:
             raise ValueError(f"{who}: k_out must have k's shape")
         ko = _rows(who, "k_out", k_out, q.dtype)
@@ -161,10 +169,10 @@ class KvCache:
         if k.dtype != torch.int8 or k.dim() != 4 or v.dtype != torch.int8 or v.dim() != 4:
             raise TypeError("KvCache: k and v must be 4-D int8 tensors")
         blocks, kv_heads, block, dim = k.shape
-        if tuple(v.shape) != (blocks, kv_heads, dim, block):
+        if v.shape != (blocks, kv_heads, dim, block):
             raise ValueError(f"KvCache: v must be [blocks, kv_heads, dim, block] = {[blocks, kv_heads, dim, block]}")
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t.dtype != _f32 or tuple(t.shape) != (blocks, kv_heads):
+            if t.dtype != _f32 or t.shape != (blocks, kv_heads):
                 raise ValueError(f"KvCache: {name} must be float32 {[blocks, kv_heads]}")
         dev = _device("KvCache", "k", k)
         for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
@@ -215,7 +223,8 @@ def _paging(who, dev, table, lens, starts, tokens):
             raise ValueError(f"{who}: {tokens} tokens for {seqs} sequences need starts")
     else:
         _ints(who, "starts", starts, (seqs + 1,))
-    _on(who, dev, table=table, lens=lens, starts=starts)
+    if table.device != dev or lens.device != dev or (starts is not None and starts.device != dev):
+        _elsewhere(who, dev, table=table, lens=lens, starts=starts)
     return seqs, row, width, None if starts is None else starts.data_ptr()
 
 
@@ -235,7 +244,8 @@ def mxq_kv_append(cache, k, v, table, lens, starts=None, *, stream=None):
     st = cache._struct
     if k.shape != v.shape or k.shape[1] != st.kv_heads or k.shape[2] != st.dim:
         raise ValueError(f"{who}: k and v must be [tokens, {st.kv_heads}, {st.dim}]")
-    _on(who, dev, k=k, v=v)
+    if k.device != dev or v.device != dev:
+        _elsewhere(who, dev, k=k, v=v)
     seqs, row, width, sp = _paging(who, dev, table, lens, starts, n)
     _call(_load().mxq_kv_append, dev, stream, st, k.data_ptr(), *ks, v.data_ptr(), *vs, table.data_ptr(), row, width,
           lens.data_ptr(), sp, n, seqs, code)
@@ -260,10 +270,11 @@ def mxq_attention(q, cache, table, lens, starts=None, out=None, *, window: int =
     st = cache._struct
     if dim != st.dim:
         raise ValueError(f"{who}: q's heads have {dim} values, the cache's {st.dim}")
-    _on(who, dev, q=q)
+    if q.device != dev:
+        _elsewhere(who, dev, q=q)
     seqs, row, width, sp = _paging(who, dev, table, lens, starts, n)
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=q.dtype, device=dev)
+        out = q.new_empty(q.shape)
     elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"{who}: out must be a contiguous tensor of q's shape and type on {dev}")
     lse = torch.empty((n, heads), dtype=_f32, device=dev) if return_lse else None
@@ -276,7 +287,7 @@ def mxq_attention(q, cache, table, lens, starts=None, out=None, *, window: int =
 def _setting(who, name, value, rows, dtype, dev):
     """(pointer, value for all) of a setting given as a tensor of one value a row, or as a number."""
     if isinstance(value, torch.Tensor):
-        if value.dtype != dtype or tuple(value.shape) != (rows,) or not value.is_contiguous() or value.device != dev:
+        if value.dtype != dtype or value.shape != (rows,) or not value.is_contiguous() or value.device != dev:
             raise ValueError(f"{who}: {name} must be a number or a contiguous "
                              f"{str(dtype).replace('torch.', '')} tensor [{rows}] on {dev}")
         return value.data_ptr(), 0
@@ -298,7 +309,7 @@ def mxq_sample(logits, u, tokens=None, probs=None, *, temperature=1.0, top_k=0, 
     row, one = logits.stride()
     if one != 1 and vocab > 1:
         raise ValueError(f"{who}: logits' rows must be contiguous")
-    if u.dtype != _f32 or tuple(u.shape) != (rows,) or not u.is_contiguous() or u.device != dev:
+    if u.dtype != _f32 or u.shape != (rows,) or not u.is_contiguous() or u.device != dev:
         raise ValueError(f"{who}: u must be a contiguous float32 tensor [{rows}] on {dev}")
     t, t_all = _setting(who, "temperature", temperature, rows, _f32, dev)
     k, k_all = _setting(who, "top_k", top_k, rows, _i32, dev)
@@ -310,9 +321,10 @@ def mxq_sample(logits, u, tokens=None, probs=None, *, temperature=1.0, top_k=0, 
         _ints(who, "tokens", tokens, (rows,))
     if probs is None:
         probs = torch.empty(rows, dtype=_f32, device=dev)
-    elif probs.dtype != _f32 or tuple(probs.shape) != (rows,) or not probs.is_contiguous():
+    elif probs.dtype != _f32 or probs.shape != (rows,) or not probs.is_contiguous():
         raise ValueError(f"{who}: probs must be a contiguous float32 tensor [{rows}]")
-    _on(who, dev, tokens=tokens, probs=probs)
+    if tokens.device != dev or probs.device != dev:
+        _elsewhere(who, dev, tokens=tokens, probs=probs)
     _call(_load().mxq_sample, dev, stream, logits.data_ptr(), row, rows, vocab, code, u.data_ptr(),
           _SamplingStruct(t, k, p, m, t_all, k_all, p_all, m_all), tokens.data_ptr(), probs.data_ptr())
     return tokens, probs

@@ -433,21 +433,13 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   constexpr int kLanes = DIM / 4, kTeams = 256 / kLanes, kRows = 16 * MT;
   __shared__ float sums[kTeams][DIM];
   __shared__ float team_m[kTeams], team_l[kTeams];
-  const int tok = blockIdx.x, hq = blockIdx.y;
-  int seq = tok;
-  if (a.starts != nullptr) {   // the last sequence that starts at or before the token
-    int lo = 0, hi = a.seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.starts[mid] <= tok) lo = mid; else hi = mid;
-    }
-    seq = lo;
-    const SeqSpan q = seq_span(a, seq);
-    if (tok < q.t0 || tok >= q.t0 + q.n || static_cast<int64_t>(q.n) * a.group > a.few_rows) return;
-  }
+  // one token a sequence, or up to `join_new`
+  const int hq = blockIdx.y, seq = blockIdx.x / a.join_new, nth = blockIdx.x - seq * a.join_new;
+  const SeqSpan sp = seq_span(a, seq);
+  if (nth >= sp.n || static_cast<int64_t>(sp.n) * a.group > a.few_rows) return;
+  const int tok = sp.t0 + nth;
   const Part part = find_part<MT>(a, -1, seq);
   if (part.splits == 1) return;
-  const SeqSpan sp = seq_span(a, seq);
   const int hk = a.pool.kv_heads, head = hq / a.group;
   const int i = (tok - sp.t0) * a.group + hq - head * a.group, rg = i / kRows, row = i - rg * kRows;
   const int team = threadIdx.x / kLanes, d = (threadIdx.x - team * kLanes) * 4;
@@ -500,7 +492,7 @@ hipError_t launch_mt(const AttendArgs& a, unsigned slots, bool joined) {
   else hipLaunchKernelGGL((attend_few_kernel<DIM, MT, false>), dim3(slots), dim3(kFewThreads), 0, a.stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !joined) return e;
-  const dim3 grid(static_cast<unsigned>(a.tokens), static_cast<unsigned>(a.heads));
+  const dim3 grid(static_cast<unsigned>(a.seqs) * static_cast<unsigned>(a.join_new), static_cast<unsigned>(a.heads));
   if (a.bf16) hipLaunchKernelGGL((attend_join_kernel<DIM, MT, true>), grid, dim3(256), 0, a.stream, a);
   else hipLaunchKernelGGL((attend_join_kernel<DIM, MT, false>), grid, dim3(256), 0, a.stream, a);
   return hipGetLastError();
@@ -527,6 +519,8 @@ hipError_t launch_attend(const AttendArgs& given, const DeviceInfo& dev) {
   const bool many = a.starts != nullptr && all_rows > kFewRows;
   a.few_rows = !many ? INT_MAX : few ? kFewRows : 0;
   a.target = dev.num_cu * 4;
+  // the most new tokens of a sequence that the few-row kernel takes
+  a.join_new = a.starts == nullptr ? 1 : many ? (kFewRows / a.group > 0 ? kFewRows / a.group : 1) : a.tokens;
 
   const int64_t most = a.starts == nullptr ? a.group : all_rows < kFewRows ? all_rows : kFewRows;
   const int mt = most <= 16 ? 1 : 2;

@@ -342,10 +342,13 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     return base + incl - count;
   };
 
-  // the end of the prefix, digit by digit (8 bits), of `m` elements: key(i), mass(i); by count, or by weight of
+  u64 outer_mass = 0;  // of the ties that the outer end keeps
+  auto row_key = [&](int i) { return key_of(load_logit<T>(x, i)); };
+  // the end of the prefix, digit by digit (8 bits), of the list's `m` tokens or the row's; by count, or by weight of
   // those up to `end`.  `above`: what is larger than all of them
-  auto find_end = [&](int m, auto key, auto mass, bool by_mass, End end, double want, u64 above) {
+  auto find_end = [&](bool listing, int m, bool by_mass, End end, double want, u64 above) {
     uint32_t prefix = 0, mask = 0;
+#pragma clang loop unroll(disable)
     for (int shift = 24; shift >= 0; shift -= 8) {
       __syncthreads();
       if (tid < 256) {
@@ -353,25 +356,26 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
         sh.digit_count[tid] = 0;
       }
       __syncthreads();
+#pragma clang loop unroll(disable)
       for (int i = tid; i < m; i += kDrawThreads) {
-        const uint32_t ky = key(i);
+        const uint32_t ky = listing ? sh.list.key[i] : row_key(i);
         if ((ky & mask) != prefix || ky < end.key) continue;
         const uint32_t d = (ky >> shift) & 255u;
         atomicAdd(&sh.digit_count[d], 1u);
-        if (by_mass && ky > end.key) atomicAdd(&sh.digit_mass[d], mass(i));
+        if (by_mass && ky > end.key) atomicAdd(&sh.digit_mass[d], listing ? sh.list.mass[i] : w.fixed(ky));
       }
       __syncthreads();
       if (wave == 0) {  // four digits a lane, the largest first
         u64 here[4], sum = 0;
         uint32_t some = 0;
+        const uint32_t end_digit = (end.key & mask) == prefix && end.key != 0 ? (end.key >> shift) & 255u : 256u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t d = 255u - (lane * 4 + j);
           const uint32_t cnt = sh.digit_count[d];
           here[j] = by_mass ? sh.digit_mass[d] : cnt;
           // the ties at the outer end belong to the digit that holds it
-          if (by_mass && end.key != 0 && cnt != 0 && (end.key & (mask | (255u << shift))) == (prefix | (d << shift)))
-            here[j] += end.ties * w.fixed(end.key);
+          if (by_mass && cnt != 0 && d == end_digit) here[j] += outer_mass;
           some |= cnt != 0 ? 1u << j : 0;
           sum += here[j];
         }
@@ -412,10 +416,6 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     if (by_mass && prefix == end.key) e.ties = min(e.ties, end.ties);
     return e;
   };
-  auto row_key = [&](int i) { return key_of(load_logit<T>(x, i)); };
-  auto row_mass = [&](int i) { return w.fixed(row_key(i)); };
-  auto list_key = [&](int i) { return sh.list.key[i]; };
-  auto list_mass = [&](int i) { return sh.list.mass[i]; };
 
   // bins by value: equal widths from the largest down; the last one holds all that is further
   const float top_x = value_of(top);
@@ -487,7 +487,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   // the tokens of `from` and up, in index order, from cells that reach `from`; false where they are too many
   int listed = 0;
   auto gather_cells = [&](uint32_t from) {
-    uint32_t hits = 0, all = 0, count = 0;
+    uint32_t hits = 0, all = 0;
     for (int c = c0; c < c1; ++c) hits += cells[c] >= from;
     uint32_t at = place(hits, all);
     if (all > kList) return false;
@@ -498,82 +498,81 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     const int h0 = min(wave * each, static_cast<int>(all)), h1 = min(h0 + each, static_cast<int>(all));
     // cells of this wave: at most kList / 16, two a lane
     const int my0 = h0 + lane < h1 ? sh.list.id[h0 + lane] : 0, my1 = h0 + 64 + lane < h1 ? sh.list.id[h0 + 64 + lane] : 0;
-    for (int j = h0; j < h1; j += 4) {
-      uint32_t k4[4];
+    // once to count, once to write
+    at = 0;
+#pragma clang loop unroll(disable)
+    for (int round = 0; round < 2; ++round) {
+      for (int j = h0; j < h1; j += 4) {
+        uint32_t k4[4];
+        int i4[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int o = min(j + e, h1 - 1) - h0, c = o < 64 ? __shfl(my0, o) : __shfl(my1, o - 64), i = c * kCell + lane;
-        k4[e] = j + e < h1 && i < n ? row_key(i) : 0;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) count += __popcll(__ballot(k4[e] >= from));
-    }
-    at = place(lane == 0 ? count : 0, all);  // barriers: every wave has its cells
-    if (all > kList) return false;
-    at = __shfl(static_cast<int>(at), 0);
-    for (int j = h0; j < h1; j += 4) {
-      uint32_t k4[4];
-      int i4[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int o = min(j + e, h1 - 1) - h0, c = o < 64 ? __shfl(my0, o) : __shfl(my1, o - 64);
-        i4[e] = c * kCell + lane;
-        k4[e] = j + e < h1 && i4[e] < n ? row_key(i4[e]) : 0;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const u64 hit = __ballot(k4[e] >= from);
-        if (k4[e] >= from) {
-          const uint32_t to = at + __popcll(hit & ((1ull << lane) - 1));
-          sh.list.key[to] = k4[e];
-          sh.list.id[to] = i4[e];
+        for (int e = 0; e < 4; ++e) {
+          const int o = min(j + e, h1 - 1) - h0, c = o < 64 ? __shfl(my0, o) : __shfl(my1, o - 64);
+          i4[e] = c * kCell + lane;
+          k4[e] = j + e < h1 && i4[e] < n ? row_key(i4[e]) : 0;
         }
-        at += __popcll(hit);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const u64 hit = __ballot(k4[e] >= from);
+          if (round == 1 && k4[e] >= from) {
+            const uint32_t to = at + __popcll(hit & ((1ull << lane) - 1));
+            sh.list.key[to] = k4[e];
+            sh.list.id[to] = i4[e];
+            sh.list.mass[to] = w.fixed(k4[e]);
+          }
+          at += __popcll(hit);
+        }
+      }
+      if (round == 0) {
+        at = place(lane == 0 ? at : 0, all);  // its barriers: every wave has its cells
+        if (all > kList) return false;
+        at = __shfl(static_cast<int>(at), 0);
       }
     }
     listed = static_cast<int>(all);
     __syncthreads();
-    for (int i = tid; i < listed; i += kDrawThreads) sh.list.mass[i] = w.fixed(sh.list.key[i]);
-    __syncthreads();
     return true;
   };
 
-  // Sums of list weights up to an end.
-  auto list_sum = [&](End end) {
-    u64 s = 0;
-    for (int i = tid; i < listed; i += kDrawThreads)
-      if (sh.list.key[i] > end.key) s += sh.list.mass[i];
-    s = wave_sum(s);
-    __syncthreads();
-    if (lane == 0) sh.wave_mass[wave] = s;
-    __syncthreads();
-    s = 0;
-    for (int i = 0; i < kDrawWaves; ++i) s += sh.wave_mass[i];
-    return s + (end.key != 0 ? end.ties * w.fixed(end.key) : 0);
-  };
-
-  const End none{0, 0xFFFFFFFFu};
-  End end = none;
   bool small = low != 0 && gather_cells(low);
-  if (small) {
-    if (limit_k && rule.k < listed) end = find_end(listed, list_key, list_mass, false, none, static_cast<double>(rule.k), 0);
-    if (rule.p < 1.0f) {
-      const u64 held = list_sum(end);
-      double want = static_cast<double>(rule.p) * static_cast<double>(held);
-      if (!limit_k) want = static_cast<double>(rule.p) * total * kFix;
+  const float fine = static_cast<float>(kBins) / fminf(fmaxf(40.0f * rule.t, 1e-30f), 1e30f);
+  End end{0, 0xFFFFFFFFu};
+  // by count, then by weight; a list that turns out too short leaves the second round to the row
+#pragma clang loop unroll(disable)
+  for (int round = 0; round < 2; ++round) {
+    const bool by_mass = round != 0;
+    if (by_mass ? !(rule.p < 1.0f) : !limit_k || (small && rule.k >= listed)) continue;
+    double want = static_cast<double>(rule.k);
+    outer_mass = by_mass && end.key != 0 ? end.ties * w.fixed(end.key) : 0;
+    bool listing = small, done = false;
+    if (by_mass) {
+      u64 s = 0;
+      if (small || limit_k) {  // the weight up to the outer end
+        const int m = small ? listed : n;
+#pragma clang loop unroll(disable)
+        for (int i = tid; i < m; i += kDrawThreads) {
+          const uint32_t key = small ? sh.list.key[i] : row_key(i);
+          if (key > end.key) s += small ? sh.list.mass[i] : w.fixed(key);
+        }
+        s = wave_sum(s);
+        __syncthreads();
+        if (lane == 0) sh.wave_mass[wave] = s;
+        __syncthreads();
+        s = outer_mass;
+        for (int i = 0; i < kDrawWaves; ++i) s += sh.wave_mass[i];
+      }
+      want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(s) : total * kFix);
       // without top_k the list is a guess: it has to hold the whole prefix, or all that min_p leaves of it
-      const bool holds = limit_k || static_cast<double>(held) >= want;
-      if (holds) end = find_end(listed, list_key, list_mass, true, end, want, 0);
-      else if (!floor) small = false;
+      if (small && !limit_k && !(static_cast<double>(s) >= want)) {
+        if (floor) done = true;
+        else small = listing = false;
+      }
     }
-  }
-
-  if (!small) {
-    // the row itself: the prefix's end is looked for among the tokens of one bin
-    listed = 0;
-    end = none;
-    const float scale = static_cast<float>(kBins) / fminf(fmaxf(40.0f * rule.t, 1e-30f), 1e30f);
-    auto row_end = [&](bool by_mass, End outer, double want) {
+    if (done) continue;
+    int m = small ? listed : n;
+    u64 above = 0;
+    if (!small && finite) {
+      // the row: the tokens of the bin in which the prefix ends become the list
       __syncthreads();
       for (int i = tid; i < kBins; i += kDrawThreads) {
         sh.bins.mass[i] = 0;
@@ -581,63 +580,46 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
       }
       __syncthreads();
       int bin = -1;
-      u64 above = 0;
       uint32_t inside = 0;
-      if (finite) {
+#pragma clang loop unroll(disable)
+      for (int pass = 0; pass < 2; ++pass) {
+#pragma clang loop unroll(disable)
         for (int i = tid * 8; i < n; i += kDrawThreads * 8) {
           uint32_t key[8];
           load_keys8<T>(x, i, n, a.wide, key);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            if (key[e] == 0 || key[e] < outer.key) continue;
-            const int b = bin_of(key[e], scale);
-            atomicAdd(&sh.bins.count[b], 1u);
-            if (by_mass && key[e] > outer.key) atomicAdd(&sh.bins.mass[b], w.fixed(key[e]));
+            const int b = bin_of(key[e], fine);
+            if (key[e] == 0 || key[e] < end.key || (pass == 1 && b != bin)) continue;
+            const u64 mass = by_mass ? w.fixed(key[e]) : 0;
+            if (pass == 0) {
+              atomicAdd(&sh.bins.count[b], 1u);
+              if (by_mass && key[e] > end.key) atomicAdd(&sh.bins.mass[b], mass);
+            } else {  // in any order: only their keys and weights count here
+              const uint32_t to = atomicAdd(&sh.found, 1u);
+              sh.list.key[to] = key[e];
+              sh.list.mass[to] = mass;
+            }
           }
         }
         __syncthreads();
-        if (by_mass && outer.key != 0 && tid == 0) sh.bins.mass[bin_of(outer.key, scale)] += outer.ties * w.fixed(outer.key);
-        __syncthreads();
-        bin = reach(by_mass, want, above, inside);
-      }
-      if (bin < 0 || inside > kList) return find_end(n, row_key, row_mass, by_mass, outer, want, 0);
-      // the bin's tokens become the list (in any order: only their keys count here)
-      if (tid == 0) sh.found = 0;
-      __syncthreads();
-      for (int i = tid * 8; i < n; i += kDrawThreads * 8) {
-        uint32_t key[8];
-        load_keys8<T>(x, i, n, a.wide, key);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (key[e] != 0 && key[e] >= outer.key && bin_of(key[e], scale) == bin) {
-            const uint32_t to = atomicAdd(&sh.found, 1u);
-            sh.list.key[to] = key[e];
-            sh.list.mass[to] = by_mass ? w.fixed(key[e]) : 0;
+        if (pass == 0) {
+          if (tid == 0 && outer_mass != 0) sh.bins.mass[bin_of(end.key, fine)] += outer_mass;
+          __syncthreads();
+          bin = reach(by_mass, want, above, inside);
+          if (bin < 0 || inside > kList) {
+            above = 0;
+            break;
           }
-      }
-      __syncthreads();
-      const int m = static_cast<int>(sh.found);
-      return find_end(m, list_key, list_mass, by_mass, outer, want, above);
-    };
-    if (limit_k) end = row_end(false, none, static_cast<double>(rule.k));
-    if (rule.p < 1.0f) {
-      double want = static_cast<double>(rule.p) * total * kFix;
-      if (limit_k) {
-        u64 s = 0;
-        for (int i = tid; i < n; i += kDrawThreads) {
-          const uint32_t key = row_key(i);
-          if (key > end.key) s += w.fixed(key);
+          if (tid == 0) sh.found = 0;
+          __syncthreads();
+        } else {
+          listing = true;
+          m = static_cast<int>(sh.found);
         }
-        s = wave_sum(s);
-        __syncthreads();
-        if (lane == 0) sh.wave_mass[wave] = s;
-        __syncthreads();
-        s = end.ties * w.fixed(end.key);
-        for (int i = 0; i < kDrawWaves; ++i) s += sh.wave_mass[i];
-        want = static_cast<double>(rule.p) * static_cast<double>(s);
       }
-      end = row_end(true, end, want);
     }
+    end = find_end(listing, m, by_mass, end, want, above);
     __syncthreads();
   }
 
@@ -671,44 +653,14 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
       }
     }
   };
-  u64 sum = 0;
-  uint32_t ties = 0;
-  for (int at = from; at < upto; at += kPiece) {
-    u64 mass[8];
-    uint32_t eq;
-    eight(at, mass, eq);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum += mass[e];
-    ties += __popc(eq);
-  }
-  sum = wave_sum(sum);
-  ties = wave_sum(ties);
-  __syncthreads();
-  if (lane == 0) {
-    sh.wave_mass[wave] = sum;
-    sh.wave_count[wave] = ties;
-  }
-  __syncthreads();
-  u64 mass_before = 0, mass_all = 0;
-  uint32_t eq_before = 0, eq_all = 0;
-  for (int i = 0; i < kDrawWaves; ++i) {
-    if (i == wave) {
-      mass_before = mass_all;
-      eq_before = eq_all;
-    }
-    mass_all += sh.wave_mass[i];
-    eq_all += sh.wave_count[i];
-  }
   auto with_ties = [&](u64 v, uint32_t eq) { return v + min(eq, end.ties) * end_mass; };
-  const u64 all = with_ties(mass_all, eq_all);
-  const double want = static_cast<double>(a.u[row]) * static_cast<double>(all);
-  const u64 start = with_ties(mass_before, eq_before), stop = with_ties(mass_before + sum, eq_before + ties);
-  // the wave whose tokens cross the border; the last with weight where u * total reaches the total
-  const bool last = static_cast<double>(all) <= want && stop == all && start < all;
-  if ((static_cast<double>(start) <= want && static_cast<double>(stop) > want) || last) {
-    const double edge = last ? static_cast<double>(all) * (1.0 - 1e-15) : want;
-    u64 run = mass_before;
-    uint32_t run_eq = eq_before;
+  u64 run = 0, all = 0;
+  uint32_t run_eq = 0;
+  double edge = 0.0;
+  // once to add this wave's tokens, once, in the wave that the border falls in, to find the token
+#pragma clang loop unroll(disable)
+  for (int round = 0; round < 2; ++round) {
+#pragma clang loop unroll(disable)
     for (int at = from; at < upto; at += kPiece) {
       u64 mass[8];
       uint32_t eq;
@@ -717,6 +669,11 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
 #pragma unroll
       for (int e = 0; e < 8; ++e) own += mass[e];
       const uint32_t cnt = __popc(eq);
+      if (round == 0) {
+        run += own;
+        run_eq += cnt;
+        continue;
+      }
       const u64 pre = wave_scan(own, lane);
       const uint32_t pre_eq = wave_scan(cnt, lane);
       const u64 hit = __ballot(static_cast<double>(with_ties(run + pre, run_eq + pre_eq)) > edge);
@@ -724,23 +681,48 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
         if (lane == __ffsll(hit) - 1) {
           u64 c = run + pre - own;
           uint32_t ce = run_eq + pre_eq - cnt;
-          bool done = false;
+          int pick = -1;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             c += mass[e];
             ce += (eq >> e) & 1u;
-            if (!done && static_cast<double>(with_ties(c, ce)) > edge) {
-              done = true;
-              const int i = at + lane * 8 + e;
-              a.tokens[row] = small ? sh.list.id[i] : i;
-              a.probs[row] = static_cast<float>(w.weight(small ? sh.list.key[i] : row_key(i)) * kFix / static_cast<double>(all));
-            }
+            if (pick < 0 && static_cast<double>(with_ties(c, ce)) > edge) pick = e;
           }
+          const int i = at + lane * 8 + max(pick, 0);
+          a.tokens[row] = small ? sh.list.id[i] : i;
+          a.probs[row] = static_cast<float>(w.weight(small ? sh.list.key[i] : row_key(i)) * kFix / static_cast<double>(all));
         }
         break;
       }
       run += __shfl(pre, 63);
       run_eq += __shfl(pre_eq, 63);
+    }
+    if (round == 0) {
+      const u64 sum = wave_sum(run);
+      const uint32_t ties = wave_sum(run_eq);
+      __syncthreads();
+      if (lane == 0) {
+        sh.wave_mass[wave] = sum;
+        sh.wave_count[wave] = ties;
+      }
+      __syncthreads();
+      u64 mass_all = 0;
+      uint32_t eq_all = 0;
+      for (int i = 0; i < kDrawWaves; ++i) {
+        if (i == wave) {
+          run = mass_all;
+          run_eq = eq_all;
+        }
+        mass_all += sh.wave_mass[i];
+        eq_all += sh.wave_count[i];
+      }
+      all = with_ties(mass_all, eq_all);
+      const double target = static_cast<double>(a.u[row]) * static_cast<double>(all);
+      const u64 start = with_ties(run, run_eq), stop = with_ties(run + sum, run_eq + ties);
+      // the wave whose tokens cross the border; the last with weight where u * total reaches the total
+      const bool last = static_cast<double>(all) <= target && stop == all && start < all;
+      if (!last && !(static_cast<double>(start) <= target && static_cast<double>(stop) > target)) return;
+      edge = last ? static_cast<double>(all) * (1.0 - 1e-15) : target;
     }
   }
 }
