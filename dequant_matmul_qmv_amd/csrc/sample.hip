@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kDrawThreads = 1024, kDrawWaves = 16;
 constexpr int kCell = 64, kPiece = 512, kStatTokens = 2048;  // tokens of a cell, a piece, a stats workgroup
-constexpr int kList = 2048, kBins = 2048;
+constexpr int kList = 2048, kShort = 256, kBins = 2048;
 constexpr double kFix = 8796093022208.0;  // 2^43
 typedef unsigned long long u64;
 
@@ -76,6 +76,30 @@ __device__ __forceinline__ void load_keys8(const void* row, int i, int n, bool w
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) key[e] = i + e < n ? key_of(load_logit<T>(row, i + e)) : 0;
+  }
+}
+
+// The same four times, all loads before their first use where every lane's are wide.
+template <int T>
+__device__ __forceinline__ void load_keys32(const void* row, const int (&i)[4], int n, bool wide, uint32_t (&key)[4][8]) {
+  bool inside = wide;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) inside = inside && (i[e] + 8 <= n || i[e] >= n);
+  if (__all(inside)) {
+    int at[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) at[e] = i[e] + 8 <= n ? i[e] : 0;
+    if (n >= 8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) load_keys8<T>(row, at[e], 0x7FFFFFFF, true, key[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) key[e][k] = i[e] + 8 <= n ? key[e][k] : 0;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) load_keys8<T>(row, i[e], n, wide, key[e]);
   }
 }
 
@@ -491,50 +515,123 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     for (int c = c0; c < c1; ++c) hits += cells[c] >= from;
     uint32_t at = place(hits, all);
     if (all > kList) return false;
+    int* hit_cells = reinterpret_cast<int*>(sh.list.mass);  // the weights come last
     for (int c = c0; c < c1; ++c)
-      if (cells[c] >= from) sh.list.id[at++] = c;  // cells first; tokens take their place below
+      if (cells[c] >= from) hit_cells[at++] = c;
     __syncthreads();
-    const int each = (static_cast<int>(all) + kDrawWaves - 1) / kDrawWaves;
-    const int h0 = min(wave * each, static_cast<int>(all)), h1 = min(h0 + each, static_cast<int>(all));
-    // cells of this wave: at most kList / 16, two a lane
-    const int my0 = h0 + lane < h1 ? sh.list.id[h0 + lane] : 0, my1 = h0 + 64 + lane < h1 ? sh.list.id[h0 + 64 + lane] : 0;
+    // a step of a wave: 8 cells, 8 tokens a lane
+    const int steps = (static_cast<int>(all) + 7) / 8, each = (steps + kDrawWaves - 1) / kDrawWaves;
+    const int h0 = min(wave * each * 8, static_cast<int>(all)), h1 = min(h0 + each * 8, static_cast<int>(all));
     // once to count, once to write
     at = 0;
+    uint32_t own = 0;
 #pragma clang loop unroll(disable)
     for (int round = 0; round < 2; ++round) {
-      for (int j = h0; j < h1; j += 4) {
-        uint32_t k4[4];
-        int i4[4];
+#pragma clang loop unroll(disable)
+      for (int j = h0; j < h1; j += 32) {
+        uint32_t key[4][8];
+        int first[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int o = min(j + e, h1 - 1) - h0, c = o < 64 ? __shfl(my0, o) : __shfl(my1, o - 64);
-          i4[e] = c * kCell + lane;
-          k4[e] = j + e < h1 && i4[e] < n ? row_key(i4[e]) : 0;
+          const int c = j + e * 8 + (lane >> 3);
+          first[e] = c < h1 ? hit_cells[c] * kCell + (lane & 7) * 8 : n;
         }
+        load_keys32<T>(x, first, n, a.wide, key);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const u64 hit = __ballot(k4[e] >= from);
-          if (round == 1 && k4[e] >= from) {
-            const uint32_t to = at + __popcll(hit & ((1ull << lane) - 1));
-            sh.list.key[to] = k4[e];
-            sh.list.id[to] = i4[e];
-            sh.list.mass[to] = w.fixed(k4[e]);
+          uint32_t count = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) count += key[e][i] >= from;
+          if (round == 0) {
+            own += count;
+            continue;
           }
-          at += __popcll(hit);
+          const uint32_t incl = wave_scan(count, lane);
+          uint32_t to = at + incl - count;
+          at += __shfl(incl, 63);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (key[e][i] >= from) {
+              sh.list.key[to] = key[e][i];
+              sh.list.id[to] = first[e] + i;
+              ++to;
+            }
         }
       }
       if (round == 0) {
-        at = place(lane == 0 ? at : 0, all);  // its barriers: every wave has its cells
+        own = wave_sum(own);
+        at = place(lane == 0 ? own : 0, all);  // its barriers: every wave has its cells
         if (all > kList) return false;
-        at = __shfl(static_cast<int>(at), 0);
+        at = __shfl(at, 0);
       }
     }
+    __syncthreads();
+    for (int i = tid; i < static_cast<int>(all); i += kDrawThreads) sh.list.mass[i] = w.fixed(sh.list.key[i]);
     listed = static_cast<int>(all);
     __syncthreads();
     return true;
   };
 
   bool small = low != 0 && gather_cells(low);
+  const double least = floor ? static_cast<double>(rule.min_p) * kFix : 0.0;  // of a kept token's integer weight
+  if (small && listed <= kShort) {
+    // a short list: each token's place, and the weight before it, from a look at all others
+    uint32_t key = 0, rank = 0;
+    u64 mass = 0, ahead = 0;
+    if (tid < listed) {
+      key = sh.list.key[tid];
+      mass = sh.list.mass[tid];
+      for (int j = 0; j < listed; ++j) {
+        const uint32_t other = sh.list.key[j];
+        const bool earlier = other > key || (other == key && j < tid);
+        rank += earlier;
+        ahead += earlier ? sh.list.mass[j] : 0;
+      }
+    }
+    const bool within = tid < listed && rank < static_cast<uint32_t>(rule.k);
+    u64 held = 0;
+    if (wave < kShort / 64) held = wave_sum(within ? mass : 0);
+    if (lane == 0) sh.wave_mass[wave] = held;
+    __syncthreads();
+    held = 0;
+    for (int i = 0; i < kShort / 64; ++i) held += sh.wave_mass[i];
+    const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total * kFix);
+    // without top_k the list is a guess: it has to hold the whole prefix, or all that min_p leaves of it
+    if (rule.p >= 1.0f || limit_k || floor || static_cast<double>(held) >= want) {
+      const bool kept = within && (rank == 0 || ((rule.p >= 1.0f || static_cast<double>(ahead) < want) &&
+                                                 static_cast<double>(mass) >= least));
+      if (tid < kShort) sh.digit_mass[tid] = kept ? mass : 0;
+      __syncthreads();
+      if (wave != 0) return;
+      constexpr int kEach = kShort / 64;
+      u64 m[kEach], sum = 0;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        m[e] = sh.digit_mass[lane * kEach + e];
+        sum += m[e];
+      }
+      const u64 incl = wave_scan(sum, lane), all = __shfl(incl, 63);
+      const double target = static_cast<double>(a.u[row]) * static_cast<double>(all);
+      const u64 hit = __ballot(static_cast<double>(incl) > target), some = __ballot(sum != 0);
+      // u * total may reach the total: the last token with weight then
+      const int src = hit != 0 ? __ffsll(hit) - 1 : 63 - __clzll(some | 1);
+      if (lane == src) {
+        u64 run = incl - sum;
+        int pick = -1, last = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          run += m[e];
+          if (m[e] != 0) last = e;
+          if (pick < 0 && hit != 0 && static_cast<double>(run) > target) pick = e;
+        }
+        if (pick < 0) pick = last;
+        const int i = lane * kEach + pick;
+        a.tokens[row] = sh.list.id[i];
+        a.probs[row] = static_cast<float>(w.weight(sh.list.key[i]) * kFix / static_cast<double>(all));
+      }
+      return;
+    }
+  }
   const float fine = static_cast<float>(kBins) / fminf(fmaxf(40.0f * rule.t, 1e-30f), 1e30f);
   End end{0, 0xFFFFFFFFu};
   // by count, then by weight; a list that turns out too short leaves the second round to the row
@@ -624,8 +721,8 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   }
 
   // min_p: an end whose weight is below it keeps no ties, others are looked at one by one
-  if (floor && end.key != 0 && w.weight(end.key) < static_cast<double>(rule.min_p)) end.ties = 0;
   const u64 end_mass = end.key != 0 ? w.fixed(end.key) : 0;
+  if (floor && end.key != 0 && static_cast<double>(end_mass) < least) end.ties = 0;
 
   // The draw, in index order: kept weight and ties wave by wave, then within
   // the wave that the border falls in.
@@ -639,18 +736,17 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     if (small) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) key[e] = i + e < upto ? sh.list.key[i + e] : 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mass[e] = i + e < upto ? sh.list.mass[i + e] : 0;
     } else {
       load_keys8<T>(x, i, upto, a.wide, key);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mass[e] = w.fixed(key[e]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      mass[e] = 0;
-      if (key[e] > end.key) {
-        const double v = w.weight(key[e]);
-        if (!floor || v >= static_cast<double>(rule.min_p)) mass[e] = static_cast<u64>(__builtin_rint(v * kFix));
-      } else if (key[e] == end.key && key[e] != 0) {
-        eq |= 1u << e;
-      }
+      if (key[e] == end.key && key[e] != 0) eq |= 1u << e;
+      if (key[e] <= end.key || static_cast<double>(mass[e]) < least) mass[e] = 0;
     }
   };
   auto with_ties = [&](u64 v, uint32_t eq) { return v + min(eq, end.ties) * end_mass; };
