@@ -10,22 +10,33 @@
 // Which token a border falls on is a whole number, so weights are taken in f64.
 // Where threads add in no fixed order they add integers of 2^-43: such sums are
 // the same in any order, and a border is off by 2^-44 a token of a total that is
-// at least 1.  Other sums are f64 in a fixed order.
+// at least 1.  Other sums are f64 in a fixed order.  A token below 2^-44 of the
+// largest has the integer 0: it can neither be drawn nor move a border, and is
+// left out everywhere.
+//
+// The descending order is that of one number a token, its word: the logit as an
+// ordered 32-bit key, then the index, the lower the larger.  Words differ, so a
+// prefix is held as its last word, and "kept" is word >= end and weight >= min_p.
 //
 // Bound: one read of the logits, and one f64 exponential for each of them (16
-// operations) where the whole row's weight is asked for.  Two kernels:
+// operations) where the whole row's weight is asked for.  Four kernels:
 //   stats   many workgroups a row: the largest value of each cell of 64 tokens;
 //           where no top-k limits the row, also the weight of each piece of 512,
 //           relative to the piece's own largest
 //   draw    one workgroup a row.  Without limits it adds the pieces, finds the
 //           one that u falls in and looks at its tokens alone.  With limits the
 //           cells give a bound that no kept token is below (the k-th largest
-//           cell bounds the k-th largest token), and only cells that reach it are
-//           read again: a list of at most 2048 tokens, in LDS, in index order.
-//           Rows whose kept tokens are more than that are binned by value, and
-//           the bin in which the prefix ends becomes the list.
-// A prefix is held as (key, ties): the value at its end, as an ordered 32-bit
-// key, and how many of the tokens equal to it belong to it, the first by index.
+//           cell bounds the k-th largest token), and only cells that reach it
+//           are read again, into a list of at most 2048 tokens in LDS.  Rows
+//           whose kept tokens are more than that are left to the last two
+//   bins    many workgroups a row: counts and weights of 2048 bins by value
+//   wide    many workgroups a row: the bins say in which of them the prefix
+//           ends; their tokens go to a list, those before them into the kept
+//           weight of their piece.  The row's last workgroup finds the end in
+//           the list and draws.  Where a bin has more tokens than a list (many
+//           equal logits) it searches the row itself
+#include <cfloat>
+
 #include "mxq_device.h"
 #include "serve_internal.h"
 
@@ -33,11 +44,14 @@ namespace mxq {
 
 namespace {
 
+typedef unsigned long long u64;
 constexpr int kDrawThreads = 1024, kDrawWaves = 16;
 constexpr int kCell = 64, kPiece = 512, kStatTokens = 2048;  // tokens of a cell, a piece, a stats workgroup
-constexpr int kList = 2048, kShort = 256, kBins = 2048;
+constexpr int kList = 2048, kShort = 256, kBins = 2048, kMaxPieces = 2048;
+constexpr int kGuess = 192;      // cells that a list for top_p alone is taken from
+constexpr int kMostRows = 1024;  // rows of one launch: 70 KB of workspace each
 constexpr double kFix = 8796093022208.0;  // 2^43
-typedef unsigned long long u64;
+constexpr float kDeepest = 30.6f;         // 44 ln 2: a token this many temperatures below the largest has no weight
 
 enum { kF16In = 0, kBF16In = 1, kF32In = 2 };
 
@@ -79,30 +93,6 @@ __device__ __forceinline__ void load_keys8(const void* row, int i, int n, bool w
   }
 }
 
-// The same four times, all loads before their first use where every lane's are wide.
-template <int T>
-__device__ __forceinline__ void load_keys32(const void* row, const int (&i)[4], int n, bool wide, uint32_t (&key)[4][8]) {
-  bool inside = wide;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) inside = inside && (i[e] + 8 <= n || i[e] >= n);
-  if (__all(inside)) {
-    int at[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) at[e] = i[e] + 8 <= n ? i[e] : 0;
-    if (n >= 8) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) load_keys8<T>(row, at[e], 0x7FFFFFFF, true, key[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) key[e][k] = i[e] + 8 <= n ? key[e][k] : 0;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) load_keys8<T>(row, i[e], n, wide, key[e]);
-  }
-}
-
 // 2^z for z <= 0: whole part by the exponent, the rest, within a half, by the
 // series of exp(r ln 2) to r^11 (6e-15).
 __device__ __forceinline__ double exp2_neg(double z) {
@@ -130,7 +120,13 @@ struct Weigh {
   __device__ __forceinline__ double weight(uint32_t key) const {
     return key == top ? 1.0 : exp2_neg((static_cast<double>(value_of(key)) - top_value) * per);
   }
-  __device__ __forceinline__ u64 fixed(uint32_t key) const { return static_cast<u64>(__builtin_rint(weight(key) * kFix)); }
+  // more than 2^-44; key 0 is no token
+  __device__ __forceinline__ bool exists(uint32_t key) const {
+    return key != 0 && (key == top || (static_cast<double>(value_of(key)) - top_value) * per > -44.0);
+  }
+  __device__ __forceinline__ u64 fixed(uint32_t key) const {
+    return exists(key) ? static_cast<u64>(__builtin_rint(weight(key) * kFix)) : 0;
+  }
 };
 __device__ __forceinline__ Weigh weigher(uint32_t top, float temperature) {
   return Weigh{top, static_cast<double>(value_of(top)), 1.44269504088896340736 / static_cast<double>(temperature)};
@@ -168,6 +164,10 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
   for (int d = 32; d > 0; d /= 2) x = max(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), d)));
   return x;
 }
+// How many of the lanes below this one are in `who`.
+__device__ __forceinline__ int lanes_below(u64 who) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(who >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(who), 0));
+}
 // Inclusive sums over the lanes, in their order.
 template <typename V>
 __device__ __forceinline__ V wave_scan(V x, int lane) {
@@ -183,32 +183,388 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int row, int 
   return static_cast<const char*>(a.logits) + static_cast<int64_t>(row) * a.row_stride * size;
 }
 
-struct End {
-  uint32_t key;
-  uint32_t ties;
+// A token's place in the descending order: its key, equals by index.
+__device__ __forceinline__ u64 word_of(uint32_t key, int i) { return (static_cast<u64>(key) << 20) | (0xFFFFFu - static_cast<uint32_t>(i)); }
+__device__ __forceinline__ uint32_t key_in(u64 word) { return static_cast<uint32_t>(word >> 20); }
+__device__ __forceinline__ int index_in(u64 word) { return static_cast<int>(0xFFFFFu - (static_cast<uint32_t>(word) & 0xFFFFFu)); }
+
+// A row's state: drawn, or what the last two kernels have to do.
+enum { kDone = 0, kSums = 1, kBinned = 2, kSearch = 3 };  // sums alone; a prefix that ends in a bin; a search in the row
+
+// Bins by value: equal widths from the largest down; the last one holds all that is further.
+struct Bins {
+  float top, scale;
+  __device__ __forceinline__ int of(uint32_t key) const {
+    const float d = (top - value_of(key)) * scale;
+    return d < static_cast<float>(kBins - 1) ? static_cast<int>(d) : kBins - 1;
+  }
 };
 
 struct Shared {
+  u64 word[kList];  // the list
   union {
-    struct {  // the list, in index order
-      uint32_t key[kList];
-      int id[kList];
-      u64 mass[kList];
-    } list;
-    struct {  // bins by value
-      u64 mass[kBins];
-      uint32_t count[kBins];
-    } bins;
+    struct {
+      union {
+        u64 mass[kList];
+        int hit[kList];  // cells to be read, before the list has weights
+      };
+      union {
+        u64 piece[kMaxPieces];  // kept weight
+        struct {
+          uint32_t count[256];
+          u64 mass[256];
+        } digit;
+        struct {
+          uint32_t rank[4][kShort];
+          u64 ahead[4][kShort];
+        } pairs;
+        uint32_t bin[kBins];
+      };
+    };
+    uint32_t some[kDrawWaves][kPiece];  // keys of a wave's piece
   };
-  u64 digit_mass[256];
-  uint32_t digit_count[256];
-  u64 wave_mass[kDrawWaves];
-  double wave_sum[kDrawWaves];
+  u64 wave_mass[kDrawWaves], wave_bits[kDrawWaves];
   uint32_t wave_count[kDrawWaves], red[kDrawWaves];
-  uint32_t prefix, found;
-  u64 above;
+  double wave_sum[kDrawWaves];
+  u64 above, end, other;
   double at;
+  uint32_t found, hits, listed;
 };
+static_assert(kMaxPieces * kPiece == 1 << 20 && kMaxPieces == 2 * kDrawThreads && kBins == 2 * kDrawThreads, "two a thread");
+
+// Sum over the workgroup, the same in every thread.
+__device__ __forceinline__ u64 block_sum(Shared& sh, u64 x) {
+  x = wave_sum(x);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh.wave_mass[threadIdx.x >> 6] = x;
+  __syncthreads();
+  u64 s = 0;
+  for (int i = 0; i < kDrawWaves; ++i) s += sh.wave_mass[i];
+  return s;
+}
+__device__ __forceinline__ uint32_t block_max(Shared& sh, uint32_t x) {
+  x = wave_max(x);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh.red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return wave_max(sh.red[threadIdx.x & (kDrawWaves - 1)]);
+}
+
+// The word at which the count (or weight) of the larger ones and its own
+// reaches `want`, or 0, digit by digit (8 bits) from the first in which the
+// words differ.  get(i, word, mass) gives item i of `m`, or false; `above` is
+// what is larger than all items.
+template <typename Get>
+__device__ __forceinline__ u64 select_word(Shared& sh, Get get, int m, bool by_mass, double want, u64 above) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  u64 some = 0, any = ~0ull;  // bits set in one of the words, in all of them
+#pragma clang loop unroll(disable)
+  for (int i = tid; i < m; i += kDrawThreads) {
+    u64 word, mass;
+    if (!get(i, false, word, mass)) continue;
+    some |= word;
+    any &= word;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) {
+    some |= __shfl_xor(some, d);
+    any &= __shfl_xor(any, d);
+  }
+  __syncthreads();
+  if (lane == 0) {
+    sh.wave_mass[wave] = some;
+    sh.wave_bits[wave] = any;
+  }
+  __syncthreads();
+  for (int i = 0; i < kDrawWaves; ++i) {
+    some |= sh.wave_mass[i];
+    any &= sh.wave_bits[i];
+  }
+  if (some == 0) return 0;
+  const u64 differ = some & ~any;
+  int shift = differ != 0 ? (63 - __clzll(differ)) / 8 * 8 : 0;
+  u64 mask = ~0ull << shift << 8, prefix = some & any & mask;
+#pragma clang loop unroll(disable)
+  for (; shift >= 0; shift -= 8) {
+    __syncthreads();
+    if (tid < 256) {
+      sh.digit.mass[tid] = 0;
+      sh.digit.count[tid] = 0;
+    }
+    if (tid == 0) sh.found = 0;
+    __syncthreads();
+#pragma clang loop unroll(disable)
+    for (int i = tid; i < m; i += kDrawThreads) {
+      u64 word, mass;
+      if (!get(i, by_mass, word, mass) || (word & mask) != prefix) continue;
+      const uint32_t d = static_cast<uint32_t>(word >> shift) & 255u;
+      atomicAdd(&sh.digit.count[d], 1u);
+      if (by_mass) atomicAdd(&sh.digit.mass[d], mass);
+    }
+    __syncthreads();
+    if (wave == 0) {  // four digits a lane, the largest first
+      u64 here[4], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t d = 255u - (lane * 4 + j);
+        here[j] = by_mass ? sh.digit.mass[d] : sh.digit.count[d];
+        sum += here[j];
+      }
+      u64 run = above + wave_scan(sum, lane) - sum;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (static_cast<double>(run) < want && static_cast<double>(run + here[j]) >= want) {
+          const uint32_t d = 255u - (lane * 4 + j);
+          sh.found = d + 1;
+          sh.above = run;
+          sh.hits = sh.digit.count[d];
+        }
+        run += here[j];
+      }
+    }
+    __syncthreads();
+    if (sh.found == 0) return 0;  // all of them, and less than `want`
+    prefix |= static_cast<u64>(sh.found - 1) << shift;
+    above = sh.above;
+    mask |= 255ull << shift;
+    if (sh.hits == 1 && shift > 0) {  // it alone
+      for (int i = tid; i < m; i += kDrawThreads) {
+        u64 word, mass;
+        if (get(i, false, word, mass) && (word & mask) == prefix) sh.end = word;
+      }
+      __syncthreads();
+      return sh.end;
+    }
+  }
+  return prefix;
+}
+
+// Of a wave's 8 keys a lane those that `which` holds for, put side by side into
+// its `to` in any order; how many they are.
+template <typename Which>
+__device__ __forceinline__ int compact(const uint32_t (&key)[8], uint32_t* to, Which which) {
+  int held = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool in = which(key[e]);
+    const u64 who = __ballot(in);
+    if (in) to[held + lanes_below(who)] = key[e];
+    held += __popcll(who);
+  }
+  // the wave's stores before its loads
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return held;
+}
+
+// The draw among tokens with word >= end and weight >= least: `listed` tokens
+// are looked at in the list, the kept weight of all others is in sh.piece.
+template <int T>
+__device__ __forceinline__ void draw_kept(const SampleArgs& a, Shared& sh, int row, const void* x, const Weigh& w, u64 end,
+                                          double least, int listed) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __syncthreads();
+  for (int i = tid; i < listed; i += kDrawThreads)
+    if (sh.word[i] >= end && static_cast<double>(sh.mass[i]) >= least) atomicAdd(&sh.piece[index_in(sh.word[i]) / kPiece], sh.mass[i]);
+  __syncthreads();
+  // two pieces a thread, in index order
+  const int p = 2 * tid;
+  const u64 m0 = p < a.piece_count ? sh.piece[p] : 0, m1 = p + 1 < a.piece_count ? sh.piece[p + 1] : 0;
+  const u64 incl = wave_scan(m0 + m1, lane);
+  if (lane == 63) sh.wave_mass[wave] = incl;
+  __syncthreads();
+  u64 base = 0, all = 0;
+  for (int i = 0; i < kDrawWaves; ++i) {
+    if (i == wave) base = all;
+    all += sh.wave_mass[i];
+  }
+  const double target = static_cast<double>(a.u[row]) * static_cast<double>(all);
+  const bool past = !(static_cast<double>(all) > target);  // u of 1 and up: the last token with weight
+  const auto over = [&](u64 sum) { return past ? sum >= all : static_cast<double>(sum) > target; };
+  const u64 stop = base + incl, start = stop - m0 - m1;
+  if (!over(start) && over(stop)) {
+    const bool second = !over(start + m0);
+    sh.found = p + (second ? 1 : 0);
+    sh.above = second ? start + m0 : start;
+  }
+  __syncthreads();
+  // a token a thread
+  const int i = static_cast<int>(sh.found) * kPiece + tid;
+  uint32_t key = 0;
+  u64 mass = 0;
+  if (tid < kPiece && i < a.vocab) {
+    key = key_of(load_logit<T>(x, i));
+    if (word_of(key, i) >= end) mass = w.fixed(key);
+    if (static_cast<double>(mass) < least) mass = 0;
+  }
+  const u64 sum = wave_scan(mass, lane);
+  if (lane == 63) sh.wave_mass[wave] = sum;  // every thread is past its last use
+  __syncthreads();
+  u64 before = sh.above + sum - mass;
+  for (int j = 0; j < wave; ++j) before += sh.wave_mass[j];
+  if (mass != 0 && !over(before) && over(before + mass)) {
+    a.tokens[row] = i;
+    a.probs[row] = static_cast<float>(w.weight(key) * kFix / static_cast<double>(all));
+  }
+}
+
+// Where the prefix ends, by the bins: the one in which the top_k end, and what
+// is before it (kBins: all that is there); top_p of their weight, between that
+// without and with this bin, ends in the bins from `first` to `last`.
+struct Where {
+  int k_bin, first, last;
+  u64 k_count, k_mass, first_mass;
+};
+__device__ __forceinline__ Where locate(const SampleArgs& a, Shared& sh, int row, const Rule& rule, const SamplePlan& plan) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool limit_k = rule.k < a.vocab, limit_p = rule.p < 1.0f;
+  const double p = static_cast<double>(rule.p);
+  Where at{kBins, kBins, kBins, 0, 0, 0};
+  if (plan.state == kBinned) {
+    const u64* bin_mass = a.bin_mass + static_cast<int64_t>(row) * kBins;
+    const uint32_t* bin_count = a.bin_count + static_cast<int64_t>(row) * kBins;
+    const uint32_t c0 = bin_count[2 * tid], c1 = bin_count[2 * tid + 1];
+    const u64 m0 = bin_mass[2 * tid], m1 = bin_mass[2 * tid + 1];
+    const uint32_t count = wave_scan(c0 + c1, lane);
+    const u64 mass = wave_scan(m0 + m1, lane);
+    if (lane == 63) {
+      sh.wave_count[wave] = count;
+      sh.wave_mass[wave] = mass;
+    }
+    if (tid == 0) sh.found = sh.hits = sh.listed = kBins;
+    __syncthreads();
+    uint32_t count_base = 0;
+    u64 mass_base = 0, all = 0;
+    for (int i = 0; i < kDrawWaves; ++i) {
+      if (i < wave) count_base += sh.wave_count[i];
+      if (i == wave) mass_base = all;
+      all += sh.wave_mass[i];
+    }
+    const uint32_t count_stop = count_base + count, count_start = count_stop - c0 - c1, k = static_cast<uint32_t>(rule.k);
+    const u64 mass_stop = mass_base + mass, mass_start = mass_stop - m0 - m1;
+    if (limit_k && count_start < k && count_stop >= k) {
+      const bool second = count_start + c0 < k;
+      sh.found = 2 * tid + (second ? 1 : 0);
+      sh.end = second ? count_start + c0 : count_start;
+      sh.above = second ? mass_start + m0 : mass_start;
+      sh.other = second ? m1 : m0;
+    }
+    __syncthreads();
+    at.k_bin = static_cast<int>(sh.found);
+    if (at.k_bin < kBins) {
+      at.k_count = sh.end;
+      at.k_mass = sh.above;
+    } else {
+      at.k_mass = all;
+    }
+    const double least_want = p * (limit_k ? static_cast<double>(at.k_mass) : plan.total);
+    const double most_want = limit_k ? p * static_cast<double>(at.k_mass + (at.k_bin < kBins ? sh.other : 0)) : least_want;
+    __syncthreads();
+    if (limit_p) {
+      const auto crosses = [&](double want, u64 from, u64 upto) { return static_cast<double>(from) < want && static_cast<double>(upto) >= want; };
+      if (crosses(least_want, mass_start, mass_start + m0)) {
+        sh.hits = 2 * tid;
+        sh.above = mass_start;
+      } else if (crosses(least_want, mass_start + m0, mass_stop)) {
+        sh.hits = 2 * tid + 1;
+        sh.above = mass_start + m0;
+      }
+      if (crosses(most_want, mass_start, mass_start + m0)) sh.listed = 2 * tid;
+      else if (crosses(most_want, mass_start + m0, mass_stop)) sh.listed = 2 * tid + 1;
+      __syncthreads();
+      at.first = static_cast<int>(sh.hits);
+      at.last = static_cast<int>(sh.listed);
+      // not reached: min_p leaves less than top_p does, all that is there is kept; or top_k ends in the first bin
+      if (at.first < kBins) at.first_mass = sh.above;
+      else if (!(least_want > 0.0)) at.first = 0;
+    } else {
+      at.first = at.last = at.k_bin;
+    }
+    __syncthreads();
+  }
+  return at;
+}
+
+// The end of the prefix from the list, or token by token where that is not the
+// whole of its bins, and the draw.
+template <int T>
+__device__ __forceinline__ void finish_row(const SampleArgs& a, Shared& sh, int row, const void* x, const Rule& rule, const Weigh& w,
+                                           const Bins& bins, const SamplePlan& plan, const Where& where) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.vocab;
+  const bool limit_k = rule.k < n, limit_p = rule.p < 1.0f;
+  const double p = static_cast<double>(rule.p);
+  const double least = rule.min_p > 0.0f ? static_cast<double>(rule.min_p) * kFix : 0.0;
+  const u64* list = a.list + static_cast<int64_t>(row) * kList;
+  const u64* kept = a.kept + static_cast<int64_t>(row) * a.piece_count;
+  u64 k_mass = where.k_mass;
+  if (tid == 0) sh.listed = plan.state == kSearch ? kList + 1 : __hip_atomic_load(&a.plans[row].listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  int listed = static_cast<int>(sh.listed);
+  u64 end = 0;
+  if (listed <= kList) {
+    for (int i = tid; i < listed; i += kDrawThreads) {
+      const u64 word = list[i];
+      sh.word[i] = word;
+      sh.mass[i] = w.fixed(key_in(word));
+    }
+    __syncthreads();
+    if (where.k_bin < kBins) {
+      const auto item = [&](int i, bool, u64& word, u64& mass) {
+        word = sh.word[i];
+        mass = 0;
+        return bins.of(key_in(word)) == where.k_bin;
+      };
+      end = select_word(sh, item, listed, false, rule.k, where.k_count);
+      u64 held = 0;
+      for (int i = tid; i < listed; i += kDrawThreads)
+        held += sh.word[i] >= end && bins.of(key_in(sh.word[i])) == where.k_bin ? sh.mass[i] : 0;
+      k_mass += block_sum(sh, held);
+    }
+    if (limit_p && plan.state == kBinned) {
+      const auto item = [&](int i, bool, u64& word, u64& mass) {
+        word = sh.word[i];
+        mass = sh.mass[i];
+        return word >= end && bins.of(key_in(word)) <= where.last;
+      };
+      end = max(end, select_word(sh, item, listed, true, p * (limit_k ? static_cast<double>(k_mass) : plan.total), where.first_mass));
+    }
+    __syncthreads();
+    for (int q = tid; q < a.piece_count; q += kDrawThreads) sh.piece[q] = kept[q];
+  } else {
+    // the row itself, token by token
+    u64 from = 0;
+    const auto item = [&](int i, bool weight, u64& word, u64& mass) {
+      const uint32_t key = key_of(load_logit<T>(x, i));
+      word = word_of(key, i);
+      if (key < plan.low || word < from) return false;
+      mass = weight ? w.fixed(key) : 0;
+      return true;
+    };
+    listed = 0;
+    if (limit_k) end = from = select_word(sh, item, n, false, rule.k, 0);
+    if (limit_p) {
+      double whole = plan.total;
+      if (limit_k) {
+        u64 held = 0, word, mass;
+        for (int i = tid; i < n; i += kDrawThreads) held += item(i, true, word, mass) ? mass : 0;
+        whole = static_cast<double>(block_sum(sh, held));
+      }
+      end = max(end, select_word(sh, item, n, true, p * whole, 0));
+    }
+    __syncthreads();
+    for (int q = wave; q < a.piece_count; q += kDrawWaves) {
+      u64 sum = 0;
+      for (int i = q * kPiece + lane; i < min((q + 1) * kPiece, n); i += 64) {
+        const uint32_t key = key_of(load_logit<T>(x, i));
+        const u64 m = word_of(key, i) >= end ? w.fixed(key) : 0;
+        sum += static_cast<double>(m) >= least ? m : 0;
+      }
+      sum = wave_sum(sum);
+      if (lane == 0) sh.piece[q] = sum;
+    }
+  }
+  draw_kept<T>(a, sh, row, x, w, end, least, listed);
+}
 
 }  // namespace
 
@@ -245,21 +601,19 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   const uint32_t* cells = a.cells + static_cast<int64_t>(row) * a.cell_count;
   const double* pieces = a.pieces + static_cast<int64_t>(row) * a.piece_count;
   const Rule rule = rule_of(a, row);
-  // cells and pieces of a thread: neighbours, so that threads are in index order
-  const int cells_each = (a.cell_count + kDrawThreads - 1) / kDrawThreads;
-  const int c0 = min(tid * cells_each, a.cell_count), c1 = min(c0 + cells_each, a.cell_count);
 
   uint32_t top = 0;
-  for (int c = c0; c < c1; ++c) top = max(top, cells[c]);
-  top = wave_max(top);
-  if (lane == 0) sh.red[wave] = top;
-  if (tid == 0) sh.found = 0x7FFFFFFF;
-  __syncthreads();
-  top = wave_max(sh.red[lane & (kDrawWaves - 1)]);
+  for (int c = tid; c < a.cell_count; c += kDrawThreads) top = max(top, cells[c]);
+  if (tid == 0) {
+    sh.found = 0x7FFFFFFF;
+    sh.hits = sh.listed = 0;
+    if (a.plans) a.plans[row].state = kDone;
+  }
+  top = block_max(sh, top);
   const Weigh w = weigher(top, rule.one ? 1.0f : rule.t);
 
   if (rule.one) {
-    for (int c = c0; c < c1; ++c)
+    for (int c = tid; c < a.cell_count; c += kDrawThreads)
       if (cells[c] == top) {
         atomicMin(&sh.found, static_cast<uint32_t>(c));
         break;
@@ -351,487 +705,345 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     return;
   }
 
-  // exclusive place of this thread's `count` among all threads', in order
-  auto place = [&](uint32_t count, uint32_t& all) {
-    const uint32_t incl = wave_scan(count, lane);
-    __syncthreads();
-    if (lane == 63) sh.wave_count[wave] = incl;
-    __syncthreads();
-    uint32_t base = 0;
-    all = 0;
-    for (int i = 0; i < kDrawWaves; ++i) {
-      if (i == wave) base = all;
-      all += sh.wave_count[i];
-    }
-    return base + incl - count;
-  };
-
-  u64 outer_mass = 0;  // of the ties that the outer end keeps
-  auto row_key = [&](int i) { return key_of(load_logit<T>(x, i)); };
-  // the end of the prefix, digit by digit (8 bits), of the list's `m` tokens or the row's; by count, or by weight of
-  // those up to `end`.  `above`: what is larger than all of them
-  auto find_end = [&](bool listing, int m, bool by_mass, End end, double want, u64 above) {
-    uint32_t prefix = 0, mask = 0;
-#pragma clang loop unroll(disable)
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      __syncthreads();
-      if (tid < 256) {
-        sh.digit_mass[tid] = 0;
-        sh.digit_count[tid] = 0;
-      }
-      __syncthreads();
-#pragma clang loop unroll(disable)
-      for (int i = tid; i < m; i += kDrawThreads) {
-        const uint32_t ky = listing ? sh.list.key[i] : row_key(i);
-        if ((ky & mask) != prefix || ky < end.key) continue;
-        const uint32_t d = (ky >> shift) & 255u;
-        atomicAdd(&sh.digit_count[d], 1u);
-        if (by_mass && ky > end.key) atomicAdd(&sh.digit_mass[d], listing ? sh.list.mass[i] : w.fixed(ky));
-      }
-      __syncthreads();
-      if (wave == 0) {  // four digits a lane, the largest first
-        u64 here[4], sum = 0;
-        uint32_t some = 0;
-        const uint32_t end_digit = (end.key & mask) == prefix && end.key != 0 ? (end.key >> shift) & 255u : 256u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t d = 255u - (lane * 4 + j);
-          const uint32_t cnt = sh.digit_count[d];
-          here[j] = by_mass ? sh.digit_mass[d] : cnt;
-          // the ties at the outer end belong to the digit that holds it
-          if (by_mass && cnt != 0 && d == end_digit) here[j] += outer_mass;
-          some |= cnt != 0 ? 1u << j : 0;
-          sum += here[j];
-        }
-        u64 run = above + wave_scan(sum, lane) - sum;
-        int pick = -1, last = -1;
-        u64 pick_run = 0, last_run = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if ((some >> j) & 1u) {
-            last = j;
-            last_run = run;
-            if (pick < 0 && static_cast<double>(run + here[j]) >= want) {
-              pick = j;
-              pick_run = run;
-            }
-          }
-          run += here[j];
-        }
-        const u64 hit = __ballot(pick >= 0), any = __ballot(last >= 0);
-        // rounding of `want` may leave the sums short of it: the smallest that is there then
-        const int src = hit != 0 ? __ffsll(hit) - 1 : 63 - __clzll(any | 1);
-        if (lane == src) {
-          const int j = hit != 0 ? pick : max(last, 0);
-          sh.prefix = prefix | ((255u - (lane * 4 + j)) << shift);
-          sh.above = hit != 0 ? pick_run : last_run;
-        }
-      }
-      __syncthreads();
-      prefix = sh.prefix;
-      above = sh.above;
-      mask |= 255u << shift;
-    }
-    End e{prefix, 1};
-    const double each = by_mass ? static_cast<double>(w.fixed(prefix)) : 1.0;
-    double ties = each > 0.0 ? ceil((want - static_cast<double>(above)) / each) : 1.0;
-    ties = fmin(fmax(ties, 1.0), 4294967295.0);
-    e.ties = static_cast<uint32_t>(ties);
-    if (by_mass && prefix == end.key) e.ties = min(e.ties, end.ties);
-    return e;
-  };
-
-  // bins by value: equal widths from the largest down; the last one holds all that is further
+  // A bound that no token with weight is below, then one that no kept token is
+  // below: a token is to be listed if its key reaches `low`.
   const float top_x = value_of(top);
-  auto bin_of = [&](uint32_t key, float scale) {
-    const float d = (top_x - value_of(key)) * scale;
-    return d < static_cast<float>(kBins - 1) ? static_cast<int>(d) : kBins - 1;
+  const bool finite = top_x - top_x == 0.0f, limit_k = rule.k < n, limit_p = rule.p < 1.0f, floor = rule.min_p > 0.0f;
+  // x >= top - t d, with a margin for its rounding
+  auto key_below = [&](double d) {
+    const double edge = w.top_value - static_cast<double>(rule.t) * d;
+    const double less = edge - 1e-6 * (fabs(edge) + fabs(w.top_value));
+    return min(key_of(less > -3.4028e38 ? static_cast<float>(less) : -FLT_MAX), top);
   };
-  // the first bin at which `want` is reached, and what lies before it; -1: none.  Two bins a thread.
-  auto reach = [&](bool by_mass, double want, u64& above, uint32_t& inside) {
-    const u64 b0 = by_mass ? sh.bins.mass[2 * tid] : sh.bins.count[2 * tid];
-    const u64 b1 = by_mass ? sh.bins.mass[2 * tid + 1] : sh.bins.count[2 * tid + 1];
-    const u64 incl = wave_scan(b0 + b1, lane);
-    if (lane == 63) sh.wave_mass[wave] = incl;
+  uint32_t low = finite ? key_below(kDeepest) : top;
+  // The cells that hold weight, the furthest of them
+  uint32_t far = top;
+  for (int c = tid; c < a.cell_count; c += kDrawThreads)
+    if (cells[c] >= low) far = min(far, cells[c]);
+  far = ~block_max(sh, ~far);
+  const float spread = 2.0f * (top_x - value_of(far)), reach = kDeepest * rule.t;
+  const float width = fminf(fmaxf(spread > 0.0f && spread < reach ? spread : reach, 1e-30f), 1e30f);
+  const Bins bins{top_x, static_cast<float>(kBins) / width};
+  // top_p alone: a list of what is likely; it is no use where it does not hold the whole prefix
+  const bool guessed = limit_p && !limit_k && !floor && n > kList;
+  // tokens of less than (1 - p) / n of the total: all of them together are less than what top_p leaves out
+  if (guessed && finite) low = max(low, key_below(log(static_cast<double>(n) / ((1.0 - static_cast<double>(rule.p)) * total))));
+  const uint32_t start = low;
+  const int guess = limit_k ? rule.k : guessed ? min(kGuess, a.cell_count / 2) : 0;
+  if (finite && n > kList && guess > 0 && guess <= a.cell_count && guess <= kList) {
+    // the guess-th largest cell, to within a bin: at least that many tokens reach its smallest member
+    for (int i = tid; i < kBins; i += kDrawThreads) sh.bin[i] = 0;
+    __syncthreads();
+    for (int c = tid; c < a.cell_count; c += kDrawThreads)
+      if (cells[c] >= low) atomicAdd(&sh.bin[bins.of(cells[c])], 1u);
     if (tid == 0) sh.found = 0;
     __syncthreads();
-    u64 base = 0;
-    for (int i = 0; i < wave; ++i) base += sh.wave_mass[i];
-    const u64 start = base + incl - b0 - b1;
-    if (static_cast<double>(start) < want && static_cast<double>(start + b0 + b1) >= want) {
-      const bool second = static_cast<double>(start + b0) < want;
-      sh.found = 2 * tid + (second ? 1 : 0) + 1;
-      sh.above = start + (second ? b0 : 0);
-    }
+    const uint32_t b0 = sh.bin[2 * tid], b1 = sh.bin[2 * tid + 1], incl = wave_scan(b0 + b1, lane);
+    if (lane == 63) sh.wave_count[wave] = incl;
     __syncthreads();
-    above = sh.above;
+    uint32_t stop = incl;
+    for (int i = 0; i < wave; ++i) stop += sh.wave_count[i];
+    const uint32_t want = static_cast<uint32_t>(guess);
+    if (stop >= want && stop - b0 - b1 < want) sh.found = 2 * tid + (stop - b1 < want ? 1 : 0) + 1;
+    __syncthreads();
     const int bin = static_cast<int>(sh.found) - 1;
-    inside = bin >= 0 ? sh.bins.count[bin] : 0;
-    __syncthreads();
-    return bin;
-  };
-  const bool finite = top_x - top_x == 0.0f;
-
-  // A bound that no kept token is below.
-  uint32_t low = 0;
-  const bool limit_k = rule.k < n;
-  const int guess = limit_k ? rule.k : rule.p < 1.0f && !(rule.min_p > 0.0f) ? min(1024, a.cell_count / 2) : 0;
-  if (guess > 0 && guess <= a.cell_count && guess <= kList && finite) {
-    // the guess-th largest cell, to within a bin: at least that many tokens reach its smallest member
-    const float scale = static_cast<float>(kBins) / fminf(fmaxf(40.0f * rule.t, 1e-30f), 1e30f);
-    for (int i = tid; i < kBins; i += kDrawThreads) sh.bins.count[i] = 0;
-    __syncthreads();
-    for (int c = c0; c < c1; ++c) atomicAdd(&sh.bins.count[bin_of(cells[c], scale)], 1u);
-    __syncthreads();
-    u64 above;
-    uint32_t inside;
-    const int bin = reach(false, static_cast<double>(guess), above, inside);
-    if (bin >= 0 && bin < kBins - 1) {
-      uint32_t least = 0xFFFFFFFFu;
-      for (int c = c0; c < c1; ++c)
-        if (bin_of(cells[c], scale) <= bin) least = min(least, cells[c]);
-      least = ~wave_max(~least);
-      if (lane == 0) sh.red[wave] = least;
-      __syncthreads();
-      low = ~wave_max(~sh.red[lane & (kDrawWaves - 1)]);
-      __syncthreads();
+    if (bin >= 0) {
+      uint32_t least = top;
+      for (int c = tid; c < a.cell_count; c += kDrawThreads)
+        if (cells[c] >= low && bins.of(cells[c]) <= bin) least = min(least, cells[c]);
+      low = ~block_max(sh, ~least);
     }
   }
-  const bool floor = rule.min_p > 0.0f;
+  // for the row's own kernels; a guess is none
+  uint32_t bound = guessed ? start : low;
   // top_p of the top_k needs the weight of all of those, also below min_p
-  if (floor && finite && !(limit_k && rule.p < 1.0f)) {
-    // w >= min_p: x >= top + t ln(min_p), with a margin for its rounding
-    const double edge = w.top_value + static_cast<double>(rule.t) * log(static_cast<double>(rule.min_p));
-    const double less = edge - 1e-6 * (fabs(edge) + fabs(w.top_value));
-    if (less > -3e38) low = max(low, key_of(static_cast<float>(less)));
+  if (floor && finite && !(limit_k && limit_p)) bound = low = max(low, key_below(-log(static_cast<double>(rule.min_p))));
+
+  // the list: tokens of `low` and up, from cells that reach it, in no order
+  for (int c0 = wave * 64; c0 < a.cell_count; c0 += kDrawThreads) {
+    const int c = c0 + lane;
+    const bool hit = c < a.cell_count && cells[c] >= low;
+    const u64 who = __ballot(hit);
+    if (who == 0) continue;
+    uint32_t at = 0;
+    if (lane == 0) at = atomicAdd(&sh.hits, static_cast<uint32_t>(__popcll(who)));
+    at = __shfl(at, 0) + lanes_below(who);
+    if (hit && at < kList) sh.hit[at] = c;
   }
-
-  if (n <= kList) low = 1;  // the whole row is a list
-
-  // the tokens of `from` and up, in index order, from cells that reach `from`; false where they are too many
-  int listed = 0;
-  auto gather_cells = [&](uint32_t from) {
-    uint32_t hits = 0, all = 0;
-    for (int c = c0; c < c1; ++c) hits += cells[c] >= from;
-    uint32_t at = place(hits, all);
-    if (all > kList) return false;
-    int* hit_cells = reinterpret_cast<int*>(sh.list.mass);  // the weights come last
-    for (int c = c0; c < c1; ++c)
-      if (cells[c] >= from) hit_cells[at++] = c;
-    __syncthreads();
-    // a step of a wave: 8 cells, 8 tokens a lane
-    const int steps = (static_cast<int>(all) + 7) / 8, each = (steps + kDrawWaves - 1) / kDrawWaves;
-    const int h0 = min(wave * each * 8, static_cast<int>(all)), h1 = min(h0 + each * 8, static_cast<int>(all));
-    // once to count, once to write
-    at = 0;
-    uint32_t own = 0;
+  __syncthreads();
+  const int hits = static_cast<int>(sh.hits);
+  bool small = hits <= kList;
+  if (small) {
+    // 8 cells a wave at a time, 8 tokens a lane, two such steps in flight
 #pragma clang loop unroll(disable)
-    for (int round = 0; round < 2; ++round) {
-#pragma clang loop unroll(disable)
-      for (int j = h0; j < h1; j += 32) {
-        uint32_t key[4][8];
-        int first[4];
+    for (int j = wave * 8; j < hits; j += 2 * kDrawWaves * 8) {
+      uint32_t key[2][8];
+      int first[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = j + e * 8 + (lane >> 3);
-          first[e] = c < h1 ? hit_cells[c] * kCell + (lane & 7) * 8 : n;
-        }
-        load_keys32<T>(x, first, n, a.wide, key);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t count = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) count += key[e][i] >= from;
-          if (round == 0) {
-            own += count;
-            continue;
-          }
-          const uint32_t incl = wave_scan(count, lane);
-          uint32_t to = at + incl - count;
-          at += __shfl(incl, 63);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (key[e][i] >= from) {
-              sh.list.key[to] = key[e][i];
-              sh.list.id[to] = first[e] + i;
-              ++to;
-            }
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int h = j + e * kDrawWaves * 8 + (lane >> 3);
+        first[e] = h < hits ? sh.hit[h] * kCell + (lane & 7) * 8 : n;
       }
-      if (round == 0) {
-        own = wave_sum(own);
-        at = place(lane == 0 ? own : 0, all);  // its barriers: every wave has its cells
-        if (all > kList) return false;
-        at = __shfl(at, 0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) load_keys8<T>(x, first[e], n, a.wide, key[e]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t count = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) count += key[e][i] >= low;
+        const uint32_t incl = wave_scan(count, lane);
+        uint32_t at = 0;
+        if (lane == 63) at = atomicAdd(&sh.listed, incl);
+        at = __shfl(at, 63) + incl - count;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (key[e][i] >= low) {
+            if (at < kList) sh.word[at] = word_of(key[e][i], first[e] + i);
+            ++at;
+          }
       }
     }
     __syncthreads();
-    for (int i = tid; i < static_cast<int>(all); i += kDrawThreads) sh.list.mass[i] = w.fixed(sh.list.key[i]);
-    listed = static_cast<int>(all);
-    __syncthreads();
-    return true;
-  };
-
-  bool small = low != 0 && gather_cells(low);
+    small = sh.listed <= kList;
+  }
+  const int listed = static_cast<int>(sh.listed);
   const double least = floor ? static_cast<double>(rule.min_p) * kFix : 0.0;  // of a kept token's integer weight
-  if (small && listed <= kShort) {
-    // a short list: each token's place, and the weight before it, from a look at all others
-    uint32_t key = 0, rank = 0;
-    u64 mass = 0, ahead = 0;
-    if (tid < listed) {
-      key = sh.list.key[tid];
-      mass = sh.list.mass[tid];
-      for (int j = 0; j < listed; ++j) {
-        const uint32_t other = sh.list.key[j];
-        const bool earlier = other > key || (other == key && j < tid);
-        rank += earlier;
-        ahead += earlier ? sh.list.mass[j] : 0;
-      }
-    }
-    const bool within = tid < listed && rank < static_cast<uint32_t>(rule.k);
-    u64 held = 0;
-    if (wave < kShort / 64) held = wave_sum(within ? mass : 0);
-    if (lane == 0) sh.wave_mass[wave] = held;
+  u64 end = 0;
+  if (small) {
+    for (int i = tid; i < listed; i += kDrawThreads) sh.mass[i] = w.fixed(key_in(sh.word[i]));
     __syncthreads();
-    held = 0;
-    for (int i = 0; i < kShort / 64; ++i) held += sh.wave_mass[i];
-    const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total * kFix);
-    // without top_k the list is a guess: it has to hold the whole prefix, or all that min_p leaves of it
-    if (rule.p >= 1.0f || limit_k || floor || static_cast<double>(held) >= want) {
-      const bool kept = within && (rank == 0 || ((rule.p >= 1.0f || static_cast<double>(ahead) < want) &&
-                                                 static_cast<double>(mass) >= least));
-      if (tid < kShort) sh.digit_mass[tid] = kept ? mass : 0;
+    u64 held = 0;  // the weight of the top_k
+    if (listed <= kShort) {
+      // each token's place, and the weight before it, from a look at all others: four threads a token
+      const int i = tid & (kShort - 1), team = tid / kShort, share = (listed + 3) / 4;
+      if (i < listed) {
+        const u64 word = sh.word[i];
+        const int j1 = min((team + 1) * share, listed);
+        uint32_t rank = 0;
+        u64 ahead = 0;
+#pragma unroll 4
+        for (int j = team * share; j < j1; ++j) {
+          const bool earlier = sh.word[j] > word;
+          rank += earlier;
+          ahead += earlier ? sh.mass[j] : 0;
+        }
+        sh.pairs.rank[team][i] = rank;
+        sh.pairs.ahead[team][i] = ahead;
+      }
+      if (tid == 0) sh.end = 0;
       __syncthreads();
-      if (wave != 0) return;
-      constexpr int kEach = kShort / 64;
-      u64 m[kEach], sum = 0;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        m[e] = sh.digit_mass[lane * kEach + e];
-        sum += m[e];
-      }
-      const u64 incl = wave_scan(sum, lane), all = __shfl(incl, 63);
-      const double target = static_cast<double>(a.u[row]) * static_cast<double>(all);
-      const u64 hit = __ballot(static_cast<double>(incl) > target), some = __ballot(sum != 0);
-      // u * total may reach the total: the last token with weight then
-      const int src = hit != 0 ? __ffsll(hit) - 1 : 63 - __clzll(some | 1);
-      if (lane == src) {
-        u64 run = incl - sum;
-        int pick = -1, last = 0;
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-          run += m[e];
-          if (m[e] != 0) last = e;
-          if (pick < 0 && hit != 0 && static_cast<double>(run) > target) pick = e;
+      uint32_t rank = 0;
+      u64 ahead = 0, word = 0, mass = 0;
+      bool within = false;
+      if (tid < listed) {
+        for (int t = 0; t < 4; ++t) {
+          rank += sh.pairs.rank[t][tid];
+          ahead += sh.pairs.ahead[t][tid];
         }
-        if (pick < 0) pick = last;
-        const int i = lane * kEach + pick;
-        a.tokens[row] = sh.list.id[i];
-        a.probs[row] = static_cast<float>(w.weight(sh.list.key[i]) * kFix / static_cast<double>(all));
+        word = sh.word[tid];
+        mass = sh.mass[tid];
+        within = rank < static_cast<uint32_t>(rule.k);
+        if (!limit_p && rank + 1 == static_cast<uint32_t>(rule.k)) sh.end = word;
       }
-      return;
-    }
-  }
-  const float fine = static_cast<float>(kBins) / fminf(fmaxf(40.0f * rule.t, 1e-30f), 1e30f);
-  End end{0, 0xFFFFFFFFu};
-  // by count, then by weight; a list that turns out too short leaves the second round to the row
-#pragma clang loop unroll(disable)
-  for (int round = 0; round < 2; ++round) {
-    const bool by_mass = round != 0;
-    if (by_mass ? !(rule.p < 1.0f) : !limit_k || (small && rule.k >= listed)) continue;
-    double want = static_cast<double>(rule.k);
-    outer_mass = by_mass && end.key != 0 ? end.ties * w.fixed(end.key) : 0;
-    bool listing = small, done = false;
-    if (by_mass) {
-      u64 s = 0;
-      if (small || limit_k) {  // the weight up to the outer end
-        const int m = small ? listed : n;
-#pragma clang loop unroll(disable)
-        for (int i = tid; i < m; i += kDrawThreads) {
-          const uint32_t key = small ? sh.list.key[i] : row_key(i);
-          if (key > end.key) s += small ? sh.list.mass[i] : w.fixed(key);
-        }
-        s = wave_sum(s);
-        __syncthreads();
-        if (lane == 0) sh.wave_mass[wave] = s;
-        __syncthreads();
-        s = outer_mass;
-        for (int i = 0; i < kDrawWaves; ++i) s += sh.wave_mass[i];
-      }
-      want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(s) : total * kFix);
-      // without top_k the list is a guess: it has to hold the whole prefix, or all that min_p leaves of it
-      if (small && !limit_k && !(static_cast<double>(s) >= want)) {
-        if (floor) done = true;
-        else small = listing = false;
-      }
-    }
-    if (done) continue;
-    int m = small ? listed : n;
-    u64 above = 0;
-    if (!small && finite) {
-      // the row: the tokens of the bin in which the prefix ends become the list
+      held = block_sum(sh, within ? mass : 0);
+      const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total * kFix);
+      if (limit_p && within && static_cast<double>(ahead) < want &&
+          (static_cast<double>(ahead + mass) >= want || rank + 1 == static_cast<uint32_t>(rule.k)))
+        sh.end = word;
       __syncthreads();
-      for (int i = tid; i < kBins; i += kDrawThreads) {
-        sh.bins.mass[i] = 0;
-        sh.bins.count[i] = 0;
-      }
-      __syncthreads();
-      int bin = -1;
-      uint32_t inside = 0;
-#pragma clang loop unroll(disable)
-      for (int pass = 0; pass < 2; ++pass) {
-#pragma clang loop unroll(disable)
-        for (int i = tid * 8; i < n; i += kDrawThreads * 8) {
-          uint32_t key[8];
-          load_keys8<T>(x, i, n, a.wide, key);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int b = bin_of(key[e], fine);
-            if (key[e] == 0 || key[e] < end.key || (pass == 1 && b != bin)) continue;
-            const u64 mass = by_mass ? w.fixed(key[e]) : 0;
-            if (pass == 0) {
-              atomicAdd(&sh.bins.count[b], 1u);
-              if (by_mass && key[e] > end.key) atomicAdd(&sh.bins.mass[b], mass);
-            } else {  // in any order: only their keys and weights count here
-              const uint32_t to = atomicAdd(&sh.found, 1u);
-              sh.list.key[to] = key[e];
-              sh.list.mass[to] = mass;
-            }
-          }
-        }
-        __syncthreads();
-        if (pass == 0) {
-          if (tid == 0 && outer_mass != 0) sh.bins.mass[bin_of(end.key, fine)] += outer_mass;
-          __syncthreads();
-          bin = reach(by_mass, want, above, inside);
-          if (bin < 0 || inside > kList) {
-            above = 0;
-            break;
-          }
-          if (tid == 0) sh.found = 0;
-          __syncthreads();
-        } else {
-          listing = true;
-          m = static_cast<int>(sh.found);
-        }
-      }
-    }
-    end = find_end(listing, m, by_mass, end, want, above);
-    __syncthreads();
-  }
-
-  // min_p: an end whose weight is below it keeps no ties, others are looked at one by one
-  const u64 end_mass = end.key != 0 ? w.fixed(end.key) : 0;
-  if (floor && end.key != 0 && static_cast<double>(end_mass) < least) end.ties = 0;
-
-  // The draw, in index order: kept weight and ties wave by wave, then within
-  // the wave that the border falls in.
-  const int m = small ? listed : n;
-  const int seg = ((m + kDrawWaves - 1) / kDrawWaves + kPiece - 1) / kPiece * kPiece;
-  const int from = min(wave * seg, m), upto = min(from + seg, m);
-  auto eight = [&](int at, u64 (&mass)[8], uint32_t& eq) {  // this lane's 8 of a step; eq: one bit a tie
-    eq = 0;
-    uint32_t key[8];
-    const int i = at + lane * 8;
-    if (small) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) key[e] = i + e < upto ? sh.list.key[i + e] : 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mass[e] = i + e < upto ? sh.list.mass[i + e] : 0;
+      end = sh.end;
+      small = !(guessed && static_cast<double>(held) < want);
     } else {
-      load_keys8<T>(x, i, upto, a.wide, key);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mass[e] = w.fixed(key[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (key[e] == end.key && key[e] != 0) eq |= 1u << e;
-      if (key[e] <= end.key || static_cast<double>(mass[e]) < least) mass[e] = 0;
-    }
-  };
-  auto with_ties = [&](u64 v, uint32_t eq) { return v + min(eq, end.ties) * end_mass; };
-  u64 run = 0, all = 0;
-  uint32_t run_eq = 0;
-  double edge = 0.0;
-  // once to add this wave's tokens, once, in the wave that the border falls in, to find the token
-#pragma clang loop unroll(disable)
-  for (int round = 0; round < 2; ++round) {
-#pragma clang loop unroll(disable)
-    for (int at = from; at < upto; at += kPiece) {
-      u64 mass[8];
-      uint32_t eq;
-      eight(at, mass, eq);
-      u64 own = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) own += mass[e];
-      const uint32_t cnt = __popc(eq);
-      if (round == 0) {
-        run += own;
-        run_eq += cnt;
-        continue;
+      const auto item = [&](int i, bool, u64& word, u64& mass) {
+        word = sh.word[i];
+        mass = sh.mass[i];
+        return true;
+      };
+      if (limit_k && rule.k < listed) end = select_word(sh, item, listed, false, rule.k, 0);
+      if (limit_p) {
+        for (int i = tid; i < listed; i += kDrawThreads) held += sh.word[i] >= end ? sh.mass[i] : 0;
+        held = block_sum(sh, held);
+        const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total * kFix);
+        small = !(guessed && static_cast<double>(held) < want);
+        if (small) end = max(end, select_word(sh, item, listed, true, want, 0));
       }
-      const u64 pre = wave_scan(own, lane);
-      const uint32_t pre_eq = wave_scan(cnt, lane);
-      const u64 hit = __ballot(static_cast<double>(with_ties(run + pre, run_eq + pre_eq)) > edge);
-      if (hit != 0) {
-        if (lane == __ffsll(hit) - 1) {
-          u64 c = run + pre - own;
-          uint32_t ce = run_eq + pre_eq - cnt;
-          int pick = -1;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            c += mass[e];
-            ce += (eq >> e) & 1u;
-            if (pick < 0 && static_cast<double>(with_ties(c, ce)) > edge) pick = e;
-          }
-          const int i = at + lane * 8 + max(pick, 0);
-          a.tokens[row] = small ? sh.list.id[i] : i;
-          a.probs[row] = static_cast<float>(w.weight(small ? sh.list.key[i] : row_key(i)) * kFix / static_cast<double>(all));
-        }
-        break;
-      }
-      run += __shfl(pre, 63);
-      run_eq += __shfl(pre_eq, 63);
-    }
-    if (round == 0) {
-      const u64 sum = wave_sum(run);
-      const uint32_t ties = wave_sum(run_eq);
-      __syncthreads();
-      if (lane == 0) {
-        sh.wave_mass[wave] = sum;
-        sh.wave_count[wave] = ties;
-      }
-      __syncthreads();
-      u64 mass_all = 0;
-      uint32_t eq_all = 0;
-      for (int i = 0; i < kDrawWaves; ++i) {
-        if (i == wave) {
-          run = mass_all;
-          run_eq = eq_all;
-        }
-        mass_all += sh.wave_mass[i];
-        eq_all += sh.wave_count[i];
-      }
-      all = with_ties(mass_all, eq_all);
-      const double target = static_cast<double>(a.u[row]) * static_cast<double>(all);
-      const u64 start = with_ties(run, run_eq), stop = with_ties(run + sum, run_eq + ties);
-      // the wave whose tokens cross the border; the last with weight where u * total reaches the total
-      const bool last = static_cast<double>(all) <= target && stop == all && start < all;
-      if (!last && !(static_cast<double>(start) <= target && static_cast<double>(stop) > target)) return;
-      edge = last ? static_cast<double>(all) * (1.0 - 1e-15) : target;
     }
   }
+  if (!small) {
+    if (tid == 0) {
+      const int state = !finite ? kSearch : limit_k || limit_p ? kBinned : kSums;
+      a.plans[row] = SamplePlan{state, top, bound, bins.scale, 0, 0, total * kFix};
+    }
+    for (int i = tid; i < kBins; i += kDrawThreads) {
+      a.bin_mass[static_cast<int64_t>(row) * kBins + i] = 0;
+      a.bin_count[static_cast<int64_t>(row) * kBins + i] = 0;
+    }
+    return;
+  }
+  __syncthreads();
+  for (int p = tid; p < a.piece_count; p += kDrawThreads) sh.piece[p] = 0;
+  draw_kept<T>(a, sh, row, x, w, end, least, listed);
+}
+
+template <int T>
+__global__ __launch_bounds__(kDrawThreads) void sample_bins_kernel(SampleArgs a) {
+  __shared__ u64 mass[kBins];
+  __shared__ uint32_t count[kBins];
+  __shared__ uint32_t some[kDrawWaves][kPiece];
+  const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const SamplePlan plan = a.plans[row];
+  if (plan.state != kBinned) return;
+  const void* x = row_of(a, row, T == kF32In ? 4 : 2);
+  const Rule rule = rule_of(a, row);
+  const Weigh w = weigher(plan.top, rule.t);
+  const Bins bins{value_of(plan.top), plan.scale};
+  const bool limit_k = rule.k < a.vocab, limit_p = rule.p < 1.0f;
+  for (int i = tid; i < kBins; i += kDrawThreads) {
+    mass[i] = 0;
+    count[i] = 0;
+  }
+  __syncthreads();
+  const int upto = min((static_cast<int>(blockIdx.x) + 1) * a.span, a.vocab);
+  for (int i = blockIdx.x * a.span + wave * kPiece; i < upto; i += kDrawWaves * kPiece) {
+    uint32_t key[8];
+    load_keys8<T>(x, i + lane * 8, a.vocab, a.wide, key);
+    // those that can be kept, side by side
+    const int held = compact(key, some[wave], [&](uint32_t k) { return k >= plan.low; });
+    for (int j = lane; j < held; j += 64) {
+      const uint32_t k = some[wave][j];
+      const int b = bins.of(k);
+      if (limit_k) atomicAdd(&count[b], 1u);
+      if (limit_p) atomicAdd(&mass[b], w.fixed(k));
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  for (int i = tid; i < kBins; i += kDrawThreads) {
+    if (mass[i] != 0) atomicAdd(&a.bin_mass[static_cast<int64_t>(row) * kBins + i], mass[i]);
+    if (count[i] != 0) atomicAdd(&a.bin_count[static_cast<int64_t>(row) * kBins + i], count[i]);
+  }
+}
+
+template <int T>
+__global__ __launch_bounds__(kDrawThreads) void sample_wide_kernel(SampleArgs a) {
+  __shared__ Shared sh;
+  const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.vocab;
+  const SamplePlan plan = a.plans[row];
+  if (plan.state == kDone || (plan.state == kSearch && (blockIdx.x != 0 || !a.joined))) return;
+  const void* x = row_of(a, row, T == kF32In ? 4 : 2);
+  const Rule rule = rule_of(a, row);
+  const Weigh w = weigher(plan.top, rule.t);
+  const Bins bins{value_of(plan.top), plan.scale};
+  const Where where = locate(a, sh, row, rule, plan);
+  if (plan.state != kSearch) {
+    const double least = rule.min_p > 0.0f ? static_cast<double>(rule.min_p) * kFix : 0.0;
+    u64* list = a.list + static_cast<int64_t>(row) * kList;
+    u64* kept = a.kept + static_cast<int64_t>(row) * a.piece_count;
+    // a piece a wave at a time
+    const int p_end = min((static_cast<int>(blockIdx.x) + 1) * (a.span / kPiece), a.piece_count);
+    if (tid == 0) sh.hits = 0;
+    __syncthreads();
+    for (int q = blockIdx.x * (a.span / kPiece) + wave; q < p_end; q += kDrawWaves) {
+      const int i = q * kPiece + lane * 8;
+      uint32_t key[8], in_list = 0, sure = 0;
+      load_keys8<T>(x, i, n, a.wide, key);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int b = bins.of(key[e]);
+        if (key[e] < plan.low) continue;
+        if (b < where.first) sure |= 1u << e;
+        else if (b <= where.last || b == where.k_bin) in_list |= 1u << e;
+      }
+      if (__ballot(in_list != 0) != 0) {
+        const uint32_t count = __popc(in_list), incl = wave_scan(count, lane);
+        uint32_t at = 0;
+        if (lane == 63) at = atomicAdd(&sh.hits, incl);
+        at = __shfl(at, 63) + incl - count;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((in_list >> e) & 1u) {
+            if (at < kList) sh.word[at] = word_of(key[e], i + e);
+            ++at;
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) key[e] = (sure >> e) & 1u ? key[e] : 0;
+      const int held = compact(key, sh.some[wave], [](uint32_t k) { return k != 0; });
+      u64 sum = 0;
+      for (int j = lane; j < held; j += 64) {
+        const u64 m = w.fixed(sh.some[wave][j]);
+        sum += static_cast<double>(m) >= least ? m : 0;
+      }
+      sum = wave_sum(sum);
+      if (lane == 0) kept[q] = sum;
+      __builtin_amdgcn_wave_barrier();
+    }
+    // this workgroup's part of the list
+    __syncthreads();
+    const uint32_t own = sh.hits;
+    if (tid == 0 && own != 0) sh.found = atomicAdd(&a.plans[row].listed, own);
+    __syncthreads();
+    for (uint32_t i = tid; i < min(own, static_cast<uint32_t>(kList)); i += kDrawThreads)
+      if (sh.found + i < kList) list[sh.found + i] = sh.word[i];
+    if (!a.joined) return;
+    // the row's last workgroup goes on, with what all have written
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      sh.found = atomicAdd(&a.plans[row].arrived, 1u);
+      __threadfence();
+    }
+    __syncthreads();
+    if (sh.found + 1 != gridDim.x) return;
+  }
+  finish_row<T>(a, sh, row, x, rule, w, bins, plan, where);
+}
+
+template <int T>
+__global__ __launch_bounds__(kDrawThreads) void sample_finish_kernel(SampleArgs a) {
+  __shared__ Shared sh;
+  const int row = blockIdx.x;
+  const SamplePlan plan = a.plans[row];
+  if (plan.state == kDone) return;
+  const Rule rule = rule_of(a, row);
+  const Weigh w = weigher(plan.top, rule.t);
+  const Bins bins{value_of(plan.top), plan.scale};
+  const Where where = locate(a, sh, row, rule, plan);
+  finish_row<T>(a, sh, row, row_of(a, row, T == kF32In ? 4 : 2), rule, w, bins, plan, where);
 }
 
 namespace {
 
+// A row's workspace.
+struct Places {
+  size_t plans, bin_mass, list, kept, pieces, bin_count, cells, all;
+};
+Places places_of(const SampleArgs& a, int64_t rows, bool wide) {
+  Places p{};
+  const auto take = [&](size_t each) {
+    const size_t at = p.all;
+    p.all += (each * static_cast<size_t>(rows) + 255) / 256 * 256;
+    return at;
+  };
+  p.pieces = take(sizeof(double) * a.piece_count);
+  p.cells = take(sizeof(uint32_t) * a.cell_count);
+  if (wide) {
+    p.plans = take(sizeof(SamplePlan));
+    p.bin_mass = take(sizeof(u64) * kBins);
+    p.bin_count = take(sizeof(uint32_t) * kBins);
+    p.list = take(sizeof(u64) * kList);
+    p.kept = take(sizeof(u64) * a.piece_count);
+  }
+  return p;
+}
+
 template <int T>
-hipError_t launch_sample_type(const SampleArgs& a) {
-  for (int r0 = 0; r0 < a.rows; r0 += 65535) {  // rows of one grid
+hipError_t launch_sample_type(const SampleArgs& a, int64_t most_rows, bool wide, int num_cu) {
+  for (int64_t r0 = 0; r0 < a.rows; r0 += most_rows) {
     SampleArgs b = a;
-    const int rows = a.rows - r0 < 65535 ? a.rows - r0 : 65535;
+    const int rows = static_cast<int>(a.rows - r0 < most_rows ? a.rows - r0 : most_rows);
     b.rows = rows;
-    b.logits = static_cast<const char*>(a.logits) + static_cast<int64_t>(r0) * a.row_stride * (T == kF32In ? 4 : 2);
+    b.logits = static_cast<const char*>(a.logits) + r0 * a.row_stride * (T == kF32In ? 4 : 2);
     b.u += r0;
     if (b.temperature) b.temperature += r0;
     if (b.top_k) b.top_k += r0;
@@ -846,6 +1058,25 @@ hipError_t launch_sample_type(const SampleArgs& a) {
     hipLaunchKernelGGL(sample_draw_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kDrawThreads), 0, a.stream, b);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (!wide) continue;
+    // a row in as many parts as give each compute unit eight workgroups, of 8 tokens a thread at least
+    int64_t spans = 8 * num_cu / rows;
+    if (spans < 1) spans = 1;
+    const int64_t least = kDrawThreads * 8, each = ((a.vocab + spans - 1) / spans + least - 1) / least * least;
+    b.span = static_cast<int>(each);
+    const dim3 grid(static_cast<unsigned>((a.vocab + each - 1) / each), static_cast<unsigned>(rows));
+    hipLaunchKernelGGL(sample_bins_kernel<T>, grid, dim3(kDrawThreads), 0, a.stream, b);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // a last workgroup has to wait for its caches' write-back: less than a launch for few of them, more for many
+    b.joined = static_cast<int64_t>(grid.x) * rows <= num_cu;
+    hipLaunchKernelGGL(sample_wide_kernel<T>, grid, dim3(kDrawThreads), 0, a.stream, b);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (b.joined) continue;
+    hipLaunchKernelGGL(sample_finish_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kDrawThreads), 0, a.stream, b);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
@@ -858,14 +1089,28 @@ hipError_t launch_sample(const SampleArgs& given, const DeviceInfo& dev) {
   a.wide = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.rows == 1 || (a.row_stride * size) % 16 == 0);
   a.cell_count = (a.vocab + kCell - 1) / kCell;
   a.piece_count = (a.vocab + kPiece - 1) / kPiece;
-  const int64_t held = a.rows < 65535 ? a.rows : 65535;
-  const size_t piece_bytes = static_cast<size_t>(held) * a.piece_count * 8, cell_bytes = static_cast<size_t>(held) * a.cell_count * 4;
-  return with_split_workspace(dev, a.stream, piece_bytes + cell_bytes, [&](float* ws) {
-    a.pieces = reinterpret_cast<double*>(ws);
-    a.cells = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ws) + piece_bytes);
-    if (a.type == kF16In) return launch_sample_type<kF16In>(a);
-    if (a.type == kBF16In) return launch_sample_type<kBF16In>(a);
-    return launch_sample_type<kF32In>(a);
+  // a row longer than a list may need the last two kernels, unless its settings are known here and ask for no prefix
+  const bool all_one = (!a.temperature && !(a.temperature_all > 0.0f)) || (!a.top_p && !(a.top_p_all > 0.0f)) ||
+                       (!a.min_p && !(a.min_p_all <= 1.0f)) || (!a.top_k && a.top_k_all == 1);
+  const bool all_open = !a.top_k && (a.top_k_all <= 0 || a.top_k_all >= a.vocab) && !a.top_p && a.top_p_all >= 1.0f && !a.min_p &&
+                        !(a.min_p_all > 0.0f);
+  const bool wide = a.vocab > kList && !all_one && !all_open;
+  const int64_t held = a.rows < kMostRows ? a.rows : kMostRows;
+  const Places at = places_of(a, held, wide);
+  return with_split_workspace(dev, a.stream, at.all, [&](float* ws) {
+    char* base = reinterpret_cast<char*>(ws);
+    a.pieces = reinterpret_cast<double*>(base + at.pieces);
+    a.cells = reinterpret_cast<uint32_t*>(base + at.cells);
+    if (wide) {
+      a.plans = reinterpret_cast<SamplePlan*>(base + at.plans);
+      a.bin_mass = reinterpret_cast<u64*>(base + at.bin_mass);
+      a.bin_count = reinterpret_cast<uint32_t*>(base + at.bin_count);
+      a.list = reinterpret_cast<u64*>(base + at.list);
+      a.kept = reinterpret_cast<u64*>(base + at.kept);
+    }
+    if (a.type == kF16In) return launch_sample_type<kF16In>(a, held, wide, dev.num_cu);
+    if (a.type == kBF16In) return launch_sample_type<kBF16In>(a, held, wide, dev.num_cu);
+    return launch_sample_type<kF32In>(a, held, wide, dev.num_cu);
   });
 }
 

@@ -121,6 +121,16 @@ size_t many_part_bytes(const AttendArgs& a);
 hipError_t launch_many(const AttendArgs& a, float* ws);
 hipError_t launch_attend(const AttendArgs& a, const DeviceInfo& dev);
 
+// What sampling's kernels leave of a row for the later ones.
+struct SamplePlan {
+  int state;
+  uint32_t top;
+  uint32_t low;  // no kept token's key is below
+  float scale;   // bins a unit of logit
+  uint32_t listed, arrived;
+  double total;  // the row's weight, in the integers' unit; without top_k
+};
+
 // One draw for each row of logits.  Settings: arrays of a value for each row,
 // or (null) one value for all.
 struct SampleArgs {
@@ -144,6 +154,14 @@ struct SampleArgs {
   double* pieces;      // weight of each 512 tokens [rows, piece_count]
   int cell_count, piece_count;
   bool wide;           // rows are 16-byte aligned
+  // of rows whose kept tokens are more than a list (null where none can be)
+  SamplePlan* plans;
+  unsigned long long* bin_mass;  // weight of each bin by value [rows, 2048]
+  uint32_t* bin_count;
+  unsigned long long* list;      // tokens of the bins in which the prefix ends [rows, 2048]
+  unsigned long long* kept;      // kept weight of each piece but for the list's [rows, piece_count]
+  int span;            // tokens of a workgroup, a multiple of 8192
+  bool joined;         // the row's last workgroup draws; else a kernel of its own
 };
 hipError_t launch_sample(const SampleArgs& a, const DeviceInfo& dev);
 
