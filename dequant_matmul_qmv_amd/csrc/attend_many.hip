@@ -19,6 +19,7 @@
 // way: p * vscale share is one fma and one exp2, the share being part of the
 // exponent.  Others (the diagonal, missing pages, weights below f16's normal
 // range, page scales far apart) take each score apart.
+#include <cfloat>
 #include <climits>
 
 #include "attend_device.h"
@@ -28,14 +29,16 @@ namespace mxq {
 namespace {
 
 constexpr int kManyThreads = 256, kManyRows = 128, kStage = 64;
-constexpr float kTinyScale = 1e-30f;
+constexpr float kTinyScale = 0x1p-100f;
+constexpr float kSlack = 1.75f;  // weights reach 2^(kLift + kSlack), below f16's largest
 
 template <int DIM>
 struct Stage {
   u4 k[kStage * DIM / 8];
   u4 v[DIM * kStage / 8];
-  float ks[4], vs[4];  // of the stage's 16-key groups; vs -1: no such page
-  float pad[56];       // a stage is a multiple of 256 bytes
+  // of the stage's 16-key groups; vs -1: no such page; with v's, its log2 and its inverse
+  float ks[4], vs[4], log_vs[4], inv_vs[4];
+  float pad[48];  // a stage is a multiple of 256 bytes
 };
 
 // Place of a 16-byte piece of a row.
@@ -110,9 +113,14 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   int seq = 0, first = 0;
   const int tile_index = unit / hk / a.many_splits;
   if (!find_tile(a, tile_index, seq, first)) return;
-  const SeqSpan sp = seq_span(a, seq);
+  seq = __builtin_amdgcn_readfirstlane(seq);
+  first = __builtin_amdgcn_readfirstlane(first);
+  SeqSpan sp = seq_span(a, seq);
+  sp.t0 = __builtin_amdgcn_readfirstlane(sp.t0);
+  sp.n = __builtin_amdgcn_readfirstlane(sp.n);
+  sp.len = __builtin_amdgcn_readfirstlane(sp.len);
   const int row0 = (tile_index - first) * kManyRows, rows = sp.n * a.group;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, h = lane >> 5;
   const int limit = min(max(sp.len, 0), a.width * block), pos0 = sp.len - sp.n;
 
   // this lane's query row; rows past the last repeat it and are not stored
@@ -163,33 +171,36 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   u4 kraw[KP], vraw[KP];
   float ks = 0.0f, vs = 0.0f;
   int pk[KP], pv;
+  const int block_log2 = 31 - __builtin_clz(block);
+  const uint32_t page_bytes = static_cast<uint32_t>(hk) * block * DIM;  // hk < 2^16, a page of a head at most 2^14
+  const int8_t* k_base = a.pool.k + static_cast<int64_t>(head) * block * DIM + kc * 16;
+  const int8_t* v_base = a.pool.v + (static_cast<int64_t>(head) * DIM + vd) * block;
+  const uint32_t nb = static_cast<uint32_t>(a.pool.blocks);
   auto pages = [&](int s) {
 #pragma unroll
     for (int j = 0; j < KP; ++j) {
-      const int at = (s * kStage + kr + j * (256 / kPer)) / block;
+      const int at = (s * kStage + kr + j * (256 / kPer)) >> block_log2;
       pk[j] = at < a.width ? table[at] : -1;
     }
-    const int at = (s * kStage + vg * 16) / block;
+    const int at = (s * kStage + vg * 16) >> block_log2;
     pv = at < a.width ? table[at] : -1;
   };
   auto fetch = [&](int s) {
-    const int nb = static_cast<int>(a.pool.blocks);
 #pragma unroll
     for (int j = 0; j < KP; ++j) {
-      const int64_t p = pk[j] >= 0 && pk[j] < nb ? pk[j] : 0;
+      const uint32_t p = static_cast<uint32_t>(pk[j]) < nb ? pk[j] : 0;
       const int t = (s * kStage + kr + j * (256 / kPer)) & (block - 1);
-      kraw[j] = *reinterpret_cast<const u4*>(a.pool.k + ((p * hk + head) * block + t) * DIM + kc * 16);
+      kraw[j] = *reinterpret_cast<const u4*>(k_base + static_cast<uint64_t>(p) * page_bytes + static_cast<uint32_t>(t * DIM));
     }
     // a page past the sequence's end may be anyone's, or never written
-    const bool ok = pv >= 0 && pv < nb && s * kStage + vg * 16 < limit;
-    const int64_t p = ok ? pv : 0;
-    const int t = (s * kStage + vg * 16) & (block - 1);
+    const bool ok = static_cast<uint32_t>(pv) < nb && s * kStage + vg * 16 < limit;
+    const uint32_t p = ok ? pv : 0;
+    const int8_t* vp = v_base + static_cast<uint64_t>(p) * page_bytes + ((s * kStage + vg * 16) & (block - 1));
 #pragma unroll
-    for (int j = 0; j < KP; ++j)
-      vraw[j] = *reinterpret_cast<const u4*>(a.pool.v + ((p * hk + head) * DIM + vd + j * 64) * block + t);
+    for (int j = 0; j < KP; ++j) vraw[j] = *reinterpret_cast<const u4*>(vp + j * 64 * block);
     if (tid < 4) {
-      ks = ok ? a.pool.k_scale[p * hk + head] : 0.0f;
-      vs = ok ? a.pool.v_scale[p * hk + head] : -1.0f;
+      ks = ok ? a.pool.k_scale[static_cast<int64_t>(p) * hk + head] : 0.0f;
+      vs = ok ? a.pool.v_scale[static_cast<int64_t>(p) * hk + head] : -1.0f;
     }
   };
   const uint32_t magic = kMagic;
@@ -205,6 +216,9 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
     if (tid < 4) {
       st.ks[tid] = ks;
       st.vs[tid] = vs;
+      // what a page without a scale (or a tiny one) holds is masked, or takes the rare way
+      st.log_vs[tid] = vs < 0.0f ? 0.0f : __builtin_amdgcn_logf(vs);  // log2
+      st.inv_vs[tid] = vs >= FLT_MIN ? __builtin_amdgcn_rcpf(vs) : 0.0f;
     }
   };
 
@@ -213,7 +227,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   for (int db = 0; db < DB; ++db)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[db][i] = 0.0f;
-  float m = kNegInf, l = 0.0f, top_vs = kTinyScale;
+  float m = kNegInf, l = 0.0f, top_vs = kTinyScale, log_top_vs = -100.0f;
 
   // LDS addresses of this lane's operands: piece ^ row, so a step along the row
   // is an xor of the whole address (rows are 128 or 256 bytes, stages multiples of them)
@@ -233,116 +247,125 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
         x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(k_piece(b, i)), as_h8(qf[i]), x[b], 0, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-    float c[4], v[4], mx = kNegInf;
-    bool ok = true;
-    const float was_vs = top_vs;
+    float c[4], v[4], mx = kNegInf, shrink = 1.0f;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       c[g] = st.ks[g] * factor;
       v[g] = st.vs[g];
-      ok = ok && v[g] >= 0.0f;
-      top_vs = fmaxf(top_vs, v[g]);
     }
-    const float inv_vs = 1.0f / top_vs, shrink = was_vs * inv_vs;
-    bool plain = ok && s * kStage >= all_from && (s + 1) * kStage <= all_upto;
-    float off[4], sh[4];
-    if (plain) {
-      float mn = -kNegInf;
+    const float largest = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    const bool grows = __any(largest > top_vs);  // the same in the whole workgroup
+    if (grows) {
+      shrink = top_vs / largest;
+      top_vs = largest;
+      log_top_vs = __builtin_amdgcn_logf(largest);
+    }
+    const bool there = __all(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])) >= 0.0f);
+    const bool masked = !(there && s * kStage >= all_from && (s + 1) * kStage <= all_upto);
+    if (masked) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) mx = fmaxf(mx, max8(x[g >> 1], (g & 1) * 8) * c[g]);
-      const float now = fmaxf(m, max_xor32(mx));
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        sh[g] = v[g] * inv_vs;
-        off[g] = __builtin_amdgcn_logf(sh[g]) + (kLift - now);  // log2
-        mn = fminf(mn, __builtin_fmaf(min8(x[g >> 1], (g & 1) * 8), c[g], off[g]));
-      }
-      plain = __all(mn >= -14.0f && now > kNegInf);  // and no NaN
-      if (plain) {
-        const float alpha = __builtin_amdgcn_exp2f(m - now), down = alpha * shrink;
-        m = now;
-        l *= alpha;
-        if (__any(down != 1.0f)) {
-#pragma unroll
-          for (int db = 0; db < DB; ++db) acc[db] *= down;
+        for (int i = 0; i < 16; ++i) {
+          const int g = 2 * b + (i >> 3), key = s * kStage + b * 32 + 8 * (i >> 2) + 4 * h + (i & 3);
+          const bool seen = v[g] >= 0.0f && key >= from && key < upto;
+          x[b][i] = seen ? x[b][i] * c[g] : kNegInf;
         }
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int g = 2 * b + j;
-            float sum = 0.0f;
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][8 * j + i], c[g], off[g]));
-              const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][8 * j + i + 1], c[g], off[g]));
-              sum += p0 + p1;
-              const h2 pk2 = {static_cast<_Float16>(p0), static_cast<_Float16>(p1)};
-              w[i / 2] = as_u32(pk2);
-            }
-            l = __builtin_fmaf(sum, 1.0f / sh[g], l);
-            const h8 pf = as_h8(u4{w[0], w[1], w[2], w[3]});
-#pragma unroll
-            for (int db = 0; db < DB; ++db)
-              acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(v_piece(db, g)), pf, acc[db], 0, 0, 0);
-          }
-        return;
-      }
+      for (int g = 0; g < 4; ++g) c[g] = 1.0f;
     }
-    // each score apart
-    mx = kNegInf;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int g = 2 * b + (i >> 3), key = s * kStage + b * 32 + 8 * (i >> 2) + 4 * h + (i & 3);
-        const bool seen = v[g] >= 0.0f && key >= from && key < upto;
-        x[b][i] = seen ? x[b][i] * c[g] : kNegInf;
-        mx = fmaxf(mx, x[b][i]);
-      }
-    const float now = fmaxf(m, max_xor32(mx)), ref = now == kNegInf ? 0.0f : now;
+    for (int g = 0; g < 4; ++g) mx = fmaxf(mx, max8(x[g >> 1], (g & 1) * 8) * c[g]);
+    float now = fmaxf(m, max_xor32(mx));
+    // the reference moves only where weights would leave f16's range: not at all for most stages
+    if (!__any(now > m + kSlack)) now = m;
+    const float ref = now == kNegInf ? 0.0f : now, lift = kLift - ref;
     const float alpha = __builtin_amdgcn_exp2f(m - ref), down = alpha * shrink;
     m = now;
-    l *= alpha;
-#pragma unroll
-    for (int db = 0; db < DB; ++db) acc[db] *= down;
+    float off[4], mn = -kNegInf;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const float share = fmaxf(v[g], 0.0f) * inv_vs;
-      float p[8];
+      off[g] = st.log_vs[g] + (lift - log_top_vs);
+      if (masked) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(x[g >> 1][(g & 1) * 8 + i] - ref + kLift);
-        l += p[i];
-        p[i] *= share;
+        for (int i = 0; i < 8; ++i) {
+          const float e = x[g >> 1][(g & 1) * 8 + i];
+          mn = fminf(mn, e == kNegInf ? -kNegInf : e + off[g]);
+        }
+      } else {
+        mn = fminf(mn, __builtin_fmaf(min8(x[g >> 1], (g & 1) * 8), c[g], off[g]));
       }
-      // the weights of [2^-14, ..), then those 2^24, 2^48, .. times smaller, until none is left
-      float ceiling = -kNegInf, floor = kF16Normal, lift = 1.0f;
-      for (bool more = true; more; ceiling = floor, floor *= 1.0f / kLowLift, lift *= kLowLift) {
-        bool left = false;
+    }
+    const bool rare = !__all(mn >= -14.0f);
+    if (__any(down != 1.0f)) {
+      l *= alpha;
+#pragma unroll
+      for (int db = 0; db < DB; ++db) acc[db] *= down;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float p[8], sum = 0.0f, weigh = top_vs * st.inv_vs[g];
+      if (rare) {
+        off[g] = lift;
+        weigh = 1.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[g >> 1][8 * (g & 1) + i], c[g], off[g]));
+        p[i + 1] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[g >> 1][8 * (g & 1) + i + 1], c[g], off[g]));
+        sum += p[i] + p[i + 1];
+      }
+      l = __builtin_fmaf(sum, weigh, l);
+      if (rare) {
+        const float share = fmaxf(v[g], 0.0f) / top_vs;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i] *= share;
+          x[g >> 1][8 * (g & 1) + i] = p[i];
+          p[i] = p[i] < kF16Normal ? 0.0f : p[i];  // a NaN stays
+        }
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const h2 pk2 = {static_cast<_Float16>(p[i]), static_cast<_Float16>(p[i + 1])};
+        w[i / 2] = as_u32(pk2);
+      }
+      const h8 pf = as_h8(u4{w[0], w[1], w[2], w[3]});
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+        acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(v_piece(db, g)), pf, acc[db], 0, 0, 0);
+    }
+    if (!rare) return;
+    // the weights of [2^-38, 2^-14), then those 2^24 times smaller, .., until none is left
+    float ceiling = kF16Normal, times = kLowLift;
+#pragma clang loop unroll(disable)
+    for (bool more = true; more; ceiling *= 1.0f / kLowLift, times *= kLowLift) {
+      const float floor = ceiling * (1.0f / kLowLift);
+      bool left = false;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          left = left || (p[i] > 0.0f && p[i] < floor) || (p[i + 1] > 0.0f && p[i + 1] < floor);
-          // a NaN belongs to the first round
-          const bool in0 = lift == 1.0f ? !(p[i] < floor) : p[i] < ceiling && p[i] >= floor;
-          const bool in1 = lift == 1.0f ? !(p[i + 1] < floor) : p[i + 1] < ceiling && p[i + 1] >= floor;
-          const h2 pk2 = {static_cast<_Float16>(in0 ? p[i] * lift : 0.0f), static_cast<_Float16>(in1 ? p[i + 1] * lift : 0.0f)};
+          const float p0 = x[g >> 1][(g & 1) * 8 + i], p1 = x[g >> 1][(g & 1) * 8 + i + 1];
+          left |= (p0 > 0.0f && p0 < floor) || (p1 > 0.0f && p1 < floor);
+          const h2 pk2 = {static_cast<_Float16>(p0 < ceiling && p0 >= floor ? p0 * times : 0.0f),
+                          static_cast<_Float16>(p1 < ceiling && p1 >= floor ? p1 * times : 0.0f)};
           w[i / 2] = as_u32(pk2);
         }
         const h8 pf = as_h8(u4{w[0], w[1], w[2], w[3]});
-        more = __any(left);
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
           f16x t;
 #pragma unroll
           for (int i = 0; i < 16; ++i) t[i] = 0.0f;
           t = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(again(v_piece(db, g))), pf, t, 0, 0, 0);
-          acc[db] += t * (1.0f / lift);
+          acc[db] += t * (1.0f / times);
           __builtin_amdgcn_sched_barrier(0);  // one product's registers at a time
         }
       }
+      more = __any(left);
     }
   };
 
