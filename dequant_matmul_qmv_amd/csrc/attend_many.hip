@@ -316,6 +316,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
         sum += p[i] + p[i + 1];
       }
       l = __builtin_fmaf(sum, weigh, l);
+      asm volatile("" : "+v"(l));  // added here, not where 32 weights would have to be kept for it
       if (rare) {
         const float share = fmaxf(v[g], 0.0f) / top_vs;
 #pragma unroll
