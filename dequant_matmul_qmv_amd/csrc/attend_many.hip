@@ -153,7 +153,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   // the wave's rows are in order: its first and last hold the narrowest and widest ranges
   const int last_row = min(row0 + wave * 32 + 31, rows - 1), first_row = min(row0 + wave * 32, rows - 1);
   const int pos_lo = pos0 + first_row / a.group, pos_hi = pos0 + last_row / a.group;
-  const int wave_upto = min(pos_hi + 1, limit), wave_from = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
+  // a wave without rows takes no part but in the staging
+  const int wave_upto = row0 + wave * 32 < rows ? min(pos_hi + 1, limit) : 0, wave_from = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
   const int all_upto = min(pos_lo + 1, limit), all_from = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0;
 
   // the tile's stages, and this part's share of them

@@ -7,8 +7,8 @@
 // rounded once to f32, so that the codes do not depend on a divider.
 //
 // Bound: HBM for prompts (new tokens read, codes written), launch latency for
-// single tokens.  One workgroup holds one (touched block, kv head) of k or of v,
-// so no two workgroups share a scale and nothing is atomic.  v is stored
+// single tokens.  One workgroup holds one (touched block, kv head), so no two
+// workgroups share a scale and nothing is atomic.  v is stored
 // transposed ([dim, block]): its codes pass through LDS and leave 16 tokens a
 // lane; a 16-token piece that also holds older tokens is merged with them.
 #include "mxq_device.h"
@@ -17,8 +17,6 @@
 namespace mxq {
 
 namespace {
-
-constexpr int kAppendThreads = 256;
 
 struct Touched {
   int seq, j;        // sequence and its block number
@@ -46,16 +44,6 @@ __device__ __forceinline__ void new_tokens(const KvAppendArgs& a, int s, int& t0
 __device__ Touched find_block(const KvAppendArgs& a, int unit) {
   Touched r{};
   const int b = a.pool.block, lane = threadIdx.x & 63;
-  if (a.starts == nullptr) {
-    const int pos = a.lens[unit] - 1;
-    r.seq = unit;
-    r.any = pos >= 0 && pos < a.width * b;
-    r.j = pos / b;
-    r.lo = pos;
-    r.hi = pos + 1;
-    r.token = unit;
-    return r;
-  }
   int before = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     const int s = s0 + lane;
@@ -88,27 +76,13 @@ __device__ Touched find_block(const KvAppendArgs& a, int unit) {
   return r;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const uint16_t* p, bool wide, float (&f)[8]) {
-  uint16_t h[8];
-  if (wide) {
-    const u4 v = *reinterpret_cast<const u4*>(p);
-    __builtin_memcpy(h, &v, 16);
-  } else {
+// Eight 16-bit values, as stored.
+__device__ __forceinline__ u4 load16(const uint16_t* p, bool wide) {
+  if (wide) return *reinterpret_cast<const u4*>(p);
+  uint32_t d[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = p[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = sb_to_f32<BF16>(h[i]);
-}
-
-// Largest over the workgroup.
-__device__ __forceinline__ float block_max(float m, float* red) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) m = fmaxf(m, __shfl_xor(m, d));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  for (int i = 0; i < 4; ++i) d[i] = static_cast<uint32_t>(p[2 * i]) | (static_cast<uint32_t>(p[2 * i + 1]) << 16);
+  return u4{d[0], d[1], d[2], d[3]};
 }
 
 // Four codes rescaled: those of `mask` bytes only.
@@ -120,88 +94,185 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   return pack_i8x4(c[0], c[1], c[2], c[3]);
 }
 
-}  // namespace
+// The scale with the new tokens' largest magnitude, what older codes are
+// multiplied by, and the inverse for new ones.
+struct Scaling {
+  float now, ratio, inv;
+};
+__device__ __forceinline__ Scaling scaling(float was, float most) {
+  Scaling s{fmaxf(was, static_cast<float>(static_cast<double>(most) / 127.0)), 0.0f, 0.0f};
+  if (s.now > 0.0f) {
+    s.ratio = static_cast<float>(static_cast<double>(was) / static_cast<double>(s.now));
+    s.inv = fminf(static_cast<float>(1.0 / static_cast<double>(s.now)), 3.402823466e38f);
+  }
+  return s;
+}
 
 template <bool BF16>
+__device__ __forceinline__ float absmax8(u4 v) {
+  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = fmaxf(m, fmaxf(fabsf(sb_to_f32<BF16>(static_cast<uint16_t>(d[i]))), fabsf(sb_to_f32<BF16>(static_cast<uint16_t>(d[i] >> 16)))));
+  return m;
+}
+template <bool BF16>
+__device__ __forceinline__ void quant8(u4 v, float inv, int (&q)[8]) {
+  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q[2 * i] = quant_i8(sb_to_f32<BF16>(static_cast<uint16_t>(d[i])), inv);
+    q[2 * i + 1] = quant_i8(sb_to_f32<BF16>(static_cast<uint16_t>(d[i] >> 16)), inv);
+  }
+}
+
+}  // namespace
+
+// One new token a sequence: one wave holds a (sequence, kv head), k in its
+// first 16 lanes and v in the next, so that both chains of loads run at once
+// and no barrier is met.  256 sequences of 8 heads: 2048 waves, one round of
+// the chip, where workgroups of 256 threads for each of k and v took two.
+template <bool BF16>
+__global__ __launch_bounds__(64) void kv_append_one_kernel(KvAppendArgs a) {
+  const int seq = blockIdx.x, head = blockIdx.y, lane = threadIdx.x, dim = a.pool.dim, b = a.pool.block;
+  const int pos = a.lens[seq] - 1;
+  if (pos < 0 || pos >= a.width * b) return;
+  const int j = pos / b, slot = pos - j * b, c = lane & 15;
+  const int page = a.table[static_cast<int64_t>(seq) * a.table_stride + j];
+  if (page < 0 || page >= a.pool.blocks) return;  // no such block: the token has no place
+  const int64_t ph = static_cast<int64_t>(page) * a.pool.kv_heads + head;
+  const bool is_v = (lane & 16) != 0, mine = lane < 32 && c * 8 < dim;
+  const uint16_t* x = is_v ? a.v + seq * a.v_token + head * a.v_head : a.k + seq * a.k_token + head * a.k_head;
+  float* scale_at = (is_v ? a.pool.v_scale : a.pool.k_scale) + ph;
+  const float was = slot > 0 ? *scale_at : 0.0f;
+  const u4 raw = mine ? load16(x + c * 8, a.wide) : u4{0, 0, 0, 0};
+  float m = absmax8<BF16>(raw);
+#pragma unroll
+  for (int d = 8; d > 0; d /= 2) m = fmaxf(m, __shfl_xor(m, d));
+  const Scaling s = scaling(was, m);
+  int8_t* k = a.pool.k + ph * dim * b;
+  int8_t* v = a.pool.v + ph * dim * b;
+  const float k_ratio = __shfl(s.ratio, 0), v_ratio = __shfl(s.ratio, 16);
+  if (slot > 0 && k_ratio != 1.0f)
+    for (int u = lane; u < slot * dim / 16; u += 64) {
+      u4* p = reinterpret_cast<u4*>(k) + u;
+      const u4 o = *p;
+      *p = u4{rescale4(o.x, k_ratio), rescale4(o.y, k_ratio), rescale4(o.z, k_ratio), rescale4(o.w, k_ratio)};
+    }
+  if (slot > 0 && v_ratio != 1.0f) {
+    const int pieces = (slot + 15) / 16;  // of a row; codes from `slot` on stay
+    for (int u = lane; u < dim * pieces; u += 64) {
+      const int r = u / pieces, g = u - r * pieces, older = slot - g * 16;
+      u4* p = reinterpret_cast<u4*>(v + static_cast<int64_t>(r) * b + g * 16);
+      const u4 old = *p;
+      const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = min(max(older - 4 * i, 0), 4);
+        const uint32_t keep = n == 4 ? 0u : ~0u << (8 * n);
+        o[i] = (rescale4(ow[i], v_ratio) & ~keep) | (ow[i] & keep);
+      }
+      *p = u4{o[0], o[1], o[2], o[3]};
+    }
+  }
+  // a lane's new codes lie behind the older ones, or (v) in a piece stored above by this wave
+  if (!mine) return;
+  if (c == 0) *scale_at = s.now;
+  int q[8];
+  quant8<BF16>(raw, s.inv, q);
+  if (!is_v) {
+    *reinterpret_cast<uint2*>(k + static_cast<int64_t>(slot) * dim + c * 8) =
+        uint2{pack_i8x4(q[0], q[1], q[2], q[3]), pack_i8x4(q[4], q[5], q[6], q[7])};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[static_cast<int64_t>(c * 8 + e) * b + slot] = static_cast<int8_t>(q[e]);
+  }
+}
+
+// Any number of new tokens: one workgroup holds one touched (block, kv head),
+// k and v of its new tokens in registers between the search for their largest
+// and the rounding.
+template <bool BF16, int kPer, int kAppendThreads>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvAppendArgs a) {
+  constexpr int kWaves = kAppendThreads / 64;     // kPer: pieces of 8 values a thread
   extern __shared__ __align__(16) int8_t tile[];  // v: [dim][block] codes of the new tokens
-  __shared__ float red[4];
+  __shared__ float red[2][kWaves];
   const Touched w = find_block(a, blockIdx.x);
   if (!w.any) return;
-  const int head = blockIdx.y, dim = a.pool.dim, b = a.pool.block;
+  const int head = blockIdx.y, dim = a.pool.dim, b = a.pool.block, tid = threadIdx.x;
   const int page = a.table[static_cast<int64_t>(w.seq) * a.table_stride + w.j];
   if (page < 0 || page >= a.pool.blocks) return;  // no such block: the tokens have no place
-  const bool is_v = blockIdx.z != 0;
   const int64_t ph = static_cast<int64_t>(page) * a.pool.kv_heads + head;
-  const int64_t ts = is_v ? a.v_token : a.k_token;
-  const uint16_t* x = (is_v ? a.v + head * a.v_head : a.k + head * a.k_head) + w.token * ts;
-  float* scale_at = (is_v ? a.pool.v_scale : a.pool.k_scale) + ph;
-  int8_t* codes = (is_v ? a.pool.v : a.pool.k) + ph * dim * b;
-  const int n = w.hi - w.lo, slot = w.lo - w.j * b, cols = dim / 8, units = n * cols;
-  // held: tokens that the block holds already (all before the first new one)
-  const int held = slot;
+  const uint16_t* kx = a.k + head * a.k_head + w.token * a.k_token;
+  const uint16_t* vx = a.v + head * a.v_head + w.token * a.v_token;
+  int8_t* k = a.pool.k + ph * dim * b;
+  int8_t* v = a.pool.v + ph * dim * b;
+  // slot: tokens that the block holds already (all before the first new one)
+  const int n = w.hi - w.lo, slot = w.lo - w.j * b, cols_log2 = dim == 64 ? 3 : 4, units = n << cols_log2;
 
-  float m = 0.0f;
-  for (int u = threadIdx.x; u < units; u += kAppendThreads) {
-    const int i = u / cols, c = u - i * cols;
-    float f[8];
-    load8<BF16>(x + i * ts + c * 8, a.wide, f);
+  u4 kr[kPer], vr[kPer];
+  float km = 0.0f, vm = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-  }
-  const float was = held > 0 ? *scale_at : 0.0f;
-  m = block_max(m, red);  // every thread has read `was` past its barrier
-  const float now = fmaxf(was, static_cast<float>(static_cast<double>(m) / 127.0));
-  float ratio = 0.0f, inv = 0.0f;
-  if (now > 0.0f) {
-    ratio = static_cast<float>(static_cast<double>(was) / static_cast<double>(now));
-    inv = fminf(static_cast<float>(1.0 / static_cast<double>(now)), 3.402823466e38f);
-  }
-  if (threadIdx.x == 0) *scale_at = now;
-  const bool rescale = held > 0 && ratio != 1.0f;
-
-  if (!is_v) {
-    if (rescale)
-      for (int u = threadIdx.x; u < held * dim / 4; u += kAppendThreads) {
-        uint32_t* p = reinterpret_cast<uint32_t*>(codes) + u;
-        *p = rescale4(*p, ratio);
-      }
-    for (int u = threadIdx.x; u < units; u += kAppendThreads) {
-      const int i = u / cols, c = u - i * cols;
-      float f[8];
-      load8<BF16>(x + i * ts + c * 8, a.wide, f);
-      int q[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = quant_i8(f[e], inv);
-      uint32_t* o = reinterpret_cast<uint32_t*>(codes + static_cast<int64_t>(slot + i) * dim + c * 8);
-      o[0] = pack_i8x4(q[0], q[1], q[2], q[3]);
-      o[1] = pack_i8x4(q[4], q[5], q[6], q[7]);
+  for (int j = 0; j < kPer; ++j) {
+    const int u = tid + j * kAppendThreads, i = u >> cols_log2, c = u & ((1 << cols_log2) - 1);
+    kr[j] = vr[j] = u4{0, 0, 0, 0};
+    if (u < units) {
+      kr[j] = load16(kx + i * a.k_token + c * 8, a.wide);
+      vr[j] = load16(vx + i * a.v_token + c * 8, a.wide);
     }
-    return;
   }
-
-  if (n == 1 && !rescale) {  // one token under the scale that is there: single bytes
-    for (int c = threadIdx.x; c < cols; c += kAppendThreads) {
-      float f[8];
-      load8<BF16>(x + c * 8, a.wide, f);
+  const float k_was = slot > 0 ? a.pool.k_scale[ph] : 0.0f, v_was = slot > 0 ? a.pool.v_scale[ph] : 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) codes[static_cast<int64_t>(c * 8 + e) * b + slot] = static_cast<int8_t>(quant_i8(f[e], inv));
+  for (int j = 0; j < kPer; ++j) {
+    km = fmaxf(km, absmax8<BF16>(kr[j]));
+    vm = fmaxf(vm, absmax8<BF16>(vr[j]));
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) {
+    km = fmaxf(km, __shfl_xor(km, d));
+    vm = fmaxf(vm, __shfl_xor(vm, d));
+  }
+  if ((tid & 63) == 0) {
+    red[0][tid >> 6] = km;
+    red[1][tid >> 6] = vm;
+  }
+  __syncthreads();  // every thread has read the scales
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    km = fmaxf(km, red[0][i]);
+    vm = fmaxf(vm, red[1][i]);
+  }
+  const Scaling ks = scaling(k_was, km), vs = scaling(v_was, vm);
+  if (tid == 0) {
+    a.pool.k_scale[ph] = ks.now;
+    a.pool.v_scale[ph] = vs.now;
+  }
+  if (slot > 0 && ks.ratio != 1.0f)
+    for (int u = tid; u < slot * dim / 4; u += kAppendThreads) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(k) + u;
+      *p = rescale4(*p, ks.ratio);
     }
-    return;
-  }
-  for (int u = threadIdx.x; u < units; u += kAppendThreads) {
-    const int i = u / cols, c = u - i * cols;
-    float f[8];
-    load8<BF16>(x + i * ts + c * 8, a.wide, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile[(c * 8 + e) * b + slot + i] = static_cast<int8_t>(quant_i8(f[e], inv));
+  for (int j = 0; j < kPer; ++j) {
+    const int u = tid + j * kAppendThreads, i = u >> cols_log2, c = u & ((1 << cols_log2) - 1);
+    if (u >= units) break;
+    int q[8];
+    quant8<BF16>(kr[j], ks.inv, q);
+    *reinterpret_cast<uint2*>(k + static_cast<int64_t>(slot + i) * dim + c * 8) =
+        uint2{pack_i8x4(q[0], q[1], q[2], q[3]), pack_i8x4(q[4], q[5], q[6], q[7])};
+    quant8<BF16>(vr[j], vs.inv, q);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[(c * 8 + e) * b + slot + i] = static_cast<int8_t>(q[e]);
   }
   __syncthreads();
   // pieces of 16 tokens that hold new tokens, or older ones to be rescaled
+  const bool rescale = slot > 0 && vs.ratio != 1.0f;
   const int end = slot + n, g0 = rescale ? 0 : slot / 16, g1 = (end + 15) / 16, pieces = g1 - g0;
-  for (int u = threadIdx.x; u < dim * pieces; u += kAppendThreads) {
+  for (int u = tid; u < dim * pieces; u += kAppendThreads) {
     const int r = u / pieces, g = g0 + u - r * pieces, at = g * 16;
-    u4* p = reinterpret_cast<u4*>(codes + static_cast<int64_t>(r) * b + at);
+    u4* p = reinterpret_cast<u4*>(v + static_cast<int64_t>(r) * b + at);
     const u4 fresh = *reinterpret_cast<const u4*>(tile + r * b + at);
     if (at >= slot && at + 16 <= end) {
       *p = fresh;
@@ -212,7 +283,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvAppendArgs 
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t scaled = rescale ? rescale4(ow[i], ratio) : ow[i];
+      const uint32_t scaled = rescale ? rescale4(ow[i], vs.ratio) : ow[i];
       o[i] = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -225,13 +296,33 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvAppendArgs 
   }
 }
 
-hipError_t launch_kv_append(const KvAppendArgs& a) {
-  const int64_t units = a.starts == nullptr ? a.seqs : a.tokens / a.pool.block + 2 * static_cast<int64_t>(a.seqs);
-  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(a.pool.kv_heads), 2), block(kAppendThreads);
+namespace {
+
+template <int PER, int THREADS>
+hipError_t launch_pages(const KvAppendArgs& a, dim3 grid) {
   const size_t lds = static_cast<size_t>(a.pool.dim) * a.pool.block;
-  if (a.bf16) hipLaunchKernelGGL((kv_append_kernel<true>), grid, block, lds, a.stream, a);
-  else hipLaunchKernelGGL((kv_append_kernel<false>), grid, block, lds, a.stream, a);
+  if (a.bf16) hipLaunchKernelGGL((kv_append_kernel<true, PER, THREADS>), grid, dim3(THREADS), lds, a.stream, a);
+  else hipLaunchKernelGGL((kv_append_kernel<false, PER, THREADS>), grid, dim3(THREADS), lds, a.stream, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppendArgs& a) {
+  const unsigned heads = static_cast<unsigned>(a.pool.kv_heads);
+  if (a.starts == nullptr) {
+    const dim3 grid(static_cast<unsigned>(a.seqs), heads);
+    if (a.bf16) hipLaunchKernelGGL((kv_append_one_kernel<true>), grid, dim3(64), 0, a.stream, a);
+    else hipLaunchKernelGGL((kv_append_one_kernel<false>), grid, dim3(64), 0, a.stream, a);
+    return hipGetLastError();
+  }
+  const dim3 grid(static_cast<unsigned>(a.tokens / a.pool.block + 2 * static_cast<int64_t>(a.seqs)), heads);
+  switch (a.pool.dim * a.pool.block / 2048) {
+    case 8: return launch_pages<4, 512>(a, grid);
+    case 4: return launch_pages<4, 256>(a, grid);
+    case 2: return launch_pages<2, 256>(a, grid);
+    default: return launch_pages<1, 256>(a, grid);
+  }
 }
 
 }  // namespace mxq
