@@ -64,6 +64,7 @@ def _load():
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = torch.cuda.current_device
+_empty_like = torch.empty_like
 
 
 def _call(f, dev, stream, *args):
@@ -88,12 +89,12 @@ def _elsewhere(who, dev, **tensors):
 
 def _rows(who, name, t, dtype):
     """Strides of a [tokens, heads, dim] tensor with a contiguous last dimension."""
-    if t.dtype != dtype or t.dim() != 3:
+    s = t.stride()
+    if t.dtype != dtype or len(s) != 3:
         raise TypeError(f"{who}: {name} must be a 3-D {str(dtype).replace('torch.', '')} tensor [tokens, heads, dim]")
-    a, b, c = t.stride()
-    if c != 1 and t.shape[2] > 1:
+    if s[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{who}: {name}'s last dimension must be contiguous")
-    return a, b
+    return s
 
 
 def _ints(who, name, t, shape):
@@ -115,43 +116,54 @@ def mxq_rope(q, k, inv_freq, positions, q_out=None, k_out=None, *, interleaved: 
     the two halves; the rest is copied.  Token and head strides are free.
     ``q_out`` and ``k_out`` may be ``q`` and ``k``.  ``k`` may be None."""
     who = "mxq_rope"
-    dev = _device(who, "q", q)
-    code = _HALF.get(q.dtype)
-    if code is None:
+    dtype, dev = q.dtype, q.device
+    code = _HALF.get(dtype)
+    if not q.is_cuda or code is None:
+        _device(who, "q", q)
         raise TypeError(f"{who}: q must be float16 or bfloat16")
-    n, heads, dim = q.shape if q.dim() == 3 else (0, 0, 0)
-    qs = _rows(who, "q", q, q.dtype)
+    qs = _rows(who, "q", q, dtype)
+    n, heads, dim = q.shape
     if inv_freq.dtype != _f32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"{who}: inv_freq must be a contiguous float32 vector")
     rot = 2 * inv_freq.shape[0]
     if rot > dim:
         raise ValueError(f"{who}: {rot // 2} frequencies rotate {rot} values, a head has {dim}")
-    _ints(who, "positions", positions, (n,))
+    if positions.dtype != _i32 or positions.shape != (n,) or not positions.is_contiguous():
+        _ints(who, "positions", positions, (n,))
     if inv_freq.device != dev or positions.device != dev:
         _elsewhere(who, dev, inv_freq=inv_freq, positions=positions)
-    if k is not None and k.device != dev or q_out is not None or k_out is not None:
-        _elsewhere(who, dev, k=k, q_out=q_out, k_out=k_out)
     if q_out is None:
-        q_out = q.new_empty(q.shape)
-    elif q_out.shape != q.shape:
-        raise ValueError(f"{who}: q_out must have q's shape")
-    qo = _rows(who, "q_out", q_out, q.dtype)
+        q_out = _empty_like(q)   # q's type, shape, place and order of dimensions
+        qo = q_out.stride()
+    else:
+        if q_out.shape != q.shape:
+            raise ValueError(f"{who}: q_out must have q's shape")
+        if q_out.device != dev:
+            _elsewhere(who, dev, q_out=q_out)
+        qo = _rows(who, "q_out", q_out, dtype)
     kv_heads, ks, ko, kp, kop = 0, (0, 0), (0, 0), None, None
     if k is not None:
-        ks = _rows(who, "k", k, q.dtype)
-        if k.shape[0] != n or k.shape[2] != dim:
+        ks = _rows(who, "k", k, dtype)
+        kn, kv_heads, kdim = k.shape
+        if kn != n or kdim != dim:
             raise ValueError(f"{who}: k must be [{n}, kv_heads, {dim}]")
-        kv_heads = k.shape[1]
+        if k.device != dev:
+            _elsewhere(who, dev, k=k)
         if k_out is None:
-            k_out = k.new_empty(k.shape)
-        elif k_out.shape != k.shape:
-            raise ValueError(f"{who}: k_out must have k's shape")
-        ko = _rows(who, "k_out", k_out, q.dtype)
+            k_out = _empty_like(k)
+            ko = k_out.stride()
+        else:
+            if k_out.shape != k.shape:
+                raise ValueError(f"{who}: k_out must have k's shape")
+            if k_out.device != dev:
+                _elsewhere(who, dev, k_out=k_out)
+            ko = _rows(who, "k_out", k_out, dtype)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError(f"{who}: k_out without k")
-    _call(_load().mxq_rope, dev, stream, q.data_ptr(), *qs, kp, *ks, q_out.data_ptr(), *qo, kop, *ko,
-          inv_freq.data_ptr(), positions.data_ptr(), n, heads, kv_heads, dim, rot, 1 if interleaved else 0, code)
+    _call(_load().mxq_rope, dev, stream, q.data_ptr(), qs[0], qs[1], kp, ks[0], ks[1], q_out.data_ptr(), qo[0], qo[1],
+          kop, ko[0], ko[1], inv_freq.data_ptr(), positions.data_ptr(), n, heads, kv_heads, dim, rot,
+          1 if interleaved else 0, code)
     return q_out, k_out
 
 
@@ -217,7 +229,8 @@ def _paging(who, dev, table, lens, starts, tokens):
     row, one = table.stride()
     if (one != 1 and width > 1) or (row < width and seqs > 1):
         raise ValueError(f"{who}: table's rows must be contiguous")
-    _ints(who, "lens", lens, (seqs,))
+    if lens.dtype != _i32 or lens.shape != (seqs,) or not lens.is_contiguous():
+        _ints(who, "lens", lens, (seqs,))
     if starts is None:
         if tokens != seqs:
             raise ValueError(f"{who}: {tokens} tokens for {seqs} sequences need starts")
@@ -240,15 +253,15 @@ def mxq_kv_append(cache, k, v, table, lens, starts=None, *, stream=None):
     if code is None:
         raise TypeError(f"{who}: k must be float16 or bfloat16")
     ks, vs = _rows(who, "k", k, k.dtype), _rows(who, "v", v, k.dtype)
-    n = k.shape[0]
+    n, heads, dim = k.shape
     st = cache._struct
-    if k.shape != v.shape or k.shape[1] != st.kv_heads or k.shape[2] != st.dim:
+    if k.shape != v.shape or heads != st.kv_heads or dim != st.dim:
         raise ValueError(f"{who}: k and v must be [tokens, {st.kv_heads}, {st.dim}]")
     if k.device != dev or v.device != dev:
         _elsewhere(who, dev, k=k, v=v)
     seqs, row, width, sp = _paging(who, dev, table, lens, starts, n)
-    _call(_load().mxq_kv_append, dev, stream, st, k.data_ptr(), *ks, v.data_ptr(), *vs, table.data_ptr(), row, width,
-          lens.data_ptr(), sp, n, seqs, code)
+    _call(_load().mxq_kv_append, dev, stream, st, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+          table.data_ptr(), row, width, lens.data_ptr(), sp, n, seqs, code)
     return cache
 
 
@@ -274,11 +287,11 @@ def mxq_attention(q, cache, table, lens, starts=None, out=None, *, window: int =
         _elsewhere(who, dev, q=q)
     seqs, row, width, sp = _paging(who, dev, table, lens, starts, n)
     if out is None:
-        out = q.new_empty(q.shape)
+        out = _empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
     elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"{who}: out must be a contiguous tensor of q's shape and type on {dev}")
     lse = torch.empty((n, heads), dtype=_f32, device=dev) if return_lse else None
-    _call(_load().mxq_attention, dev, stream, q.data_ptr(), *qs, st, table.data_ptr(), row, width, lens.data_ptr(), sp,
+    _call(_load().mxq_attention, dev, stream, q.data_ptr(), qs[0], qs[1], st, table.data_ptr(), row, width, lens.data_ptr(), sp,
           n, seqs, heads, window, dim ** -0.5 if scale is None else scale, out.data_ptr(),
           None if lse is None else lse.data_ptr(), code)
     return (out, lse) if return_lse else out
@@ -316,11 +329,11 @@ def mxq_sample(logits, u, tokens=None, probs=None, *, temperature=1.0, top_k=0, 
     p, p_all = _setting(who, "top_p", top_p, rows, _f32, dev)
     m, m_all = _setting(who, "min_p", min_p, rows, _f32, dev)
     if tokens is None:
-        tokens = torch.empty(rows, dtype=_i32, device=dev)
+        tokens = _empty_like(u, dtype=_i32)
     else:
         _ints(who, "tokens", tokens, (rows,))
     if probs is None:
-        probs = torch.empty(rows, dtype=_f32, device=dev)
+        probs = _empty_like(u)
     elif probs.dtype != _f32 or probs.shape != (rows,) or not probs.is_contiguous():
         raise ValueError(f"{who}: probs must be a contiguous float32 tensor [{rows}]")
     if tokens.device != dev or probs.device != dev:
