@@ -153,32 +153,66 @@ __device__ __forceinline__ Rule rule_of(const SampleArgs& a, int row) {
   return r;
 }
 
+// x of another lane by a DPP control, 0 where there is none (or the lane's row
+// of 16 is not in `rows`): a few cycles, where a shuffle through LDS takes 100.
+template <int CTRL, int ROWS, typename V>
+__device__ __forceinline__ V lane_move(V x) {
+  static_assert(sizeof(V) == 4 || sizeof(V) == 8, "one or two registers");
+  if constexpr (sizeof(V) == 4) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false));
+  } else {
+    const u64 w = __builtin_bit_cast(u64, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(w), CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(w >> 32), CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(V, (static_cast<u64>(hi) << 32) | lo);
+  }
+}
 template <typename V>
-__device__ __forceinline__ V wave_sum(V x) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) x += __shfl_xor(x, d);
+__device__ __forceinline__ V last_lane(V x) {
+  if constexpr (sizeof(V) == 4) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+  } else {
+    const u64 w = __builtin_bit_cast(u64, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(w), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(w >> 32), 63);
+    return __builtin_bit_cast(V, (static_cast<u64>(hi) << 32) | lo);
+  }
+}
+// Inclusive sums over the lanes, in their order: within rows of 16, then the
+// rows' last lanes handed on.
+template <typename V>
+__device__ __forceinline__ V wave_scan(V x) {
+  x += lane_move<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8
+  x += lane_move<0x112, 0xF>(x);
+  x += lane_move<0x114, 0xF>(x);
+  x += lane_move<0x118, 0xF>(x);
+  x += lane_move<0x142, 0xA>(x);  // row_bcast 15, 31
+  x += lane_move<0x143, 0xC>(x);
   return x;
 }
+template <typename V>
+__device__ __forceinline__ V wave_sum(V x) { return last_lane(wave_scan(x)); }
 __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) x = max(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), d)));
-  return x;
+  x = max(x, lane_move<0x111, 0xF>(x));
+  x = max(x, lane_move<0x112, 0xF>(x));
+  x = max(x, lane_move<0x114, 0xF>(x));
+  x = max(x, lane_move<0x118, 0xF>(x));
+  x = max(x, lane_move<0x142, 0xA>(x));
+  x = max(x, lane_move<0x143, 0xC>(x));
+  return last_lane(x);
+}
+__device__ __forceinline__ u64 wave_or(u64 x) {
+  x |= lane_move<0x111, 0xF>(x);
+  x |= lane_move<0x112, 0xF>(x);
+  x |= lane_move<0x114, 0xF>(x);
+  x |= lane_move<0x118, 0xF>(x);
+  x |= lane_move<0x142, 0xA>(x);
+  x |= lane_move<0x143, 0xC>(x);
+  return last_lane(x);
 }
 // How many of the lanes below this one are in `who`.
 __device__ __forceinline__ int lanes_below(u64 who) {
   return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(who >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(who), 0));
 }
-// Inclusive sums over the lanes, in their order.
-template <typename V>
-__device__ __forceinline__ V wave_scan(V x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const V up = __shfl_up(x, d);
-    if (lane >= d) x += up;
-  }
-  return x;
-}
-
 __device__ __forceinline__ const void* row_of(const SampleArgs& a, int row, int size) {
   return static_cast<const char*>(a.logits) + static_cast<int64_t>(row) * a.row_stride * size;
 }
@@ -265,11 +299,8 @@ __device__ __forceinline__ u64 select_word(Shared& sh, Get get, int m, bool by_m
     some |= word;
     any &= word;
   }
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) {
-    some |= __shfl_xor(some, d);
-    any &= __shfl_xor(any, d);
-  }
+  some = wave_or(some);
+  any = ~wave_or(~any);
   __syncthreads();
   if (lane == 0) {
     sh.wave_mass[wave] = some;
@@ -310,7 +341,7 @@ __device__ __forceinline__ u64 select_word(Shared& sh, Get get, int m, bool by_m
         here[j] = by_mass ? sh.digit.mass[d] : sh.digit.count[d];
         sum += here[j];
       }
-      u64 run = above + wave_scan(sum, lane) - sum;
+      u64 run = above + wave_scan(sum) - sum;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (static_cast<double>(run) < want && static_cast<double>(run + here[j]) >= want) {
@@ -357,6 +388,16 @@ __device__ __forceinline__ int compact(const uint32_t (&key)[8], uint32_t* to, W
   return held;
 }
 
+// Where u falls: the token drawn is the first, by index, whose sum is over it;
+// the last one with weight where u * total reaches the total.
+struct Border {
+  double target;
+  u64 all;
+  __device__ __forceinline__ bool over(u64 sum) const {
+    return static_cast<double>(all) > target ? static_cast<double>(sum) > target : sum >= all;
+  }
+};
+
 // The draw among tokens with word >= end and weight >= least: `listed` tokens
 // are looked at in the list, the kept weight of all others is in sh.piece.
 template <int T>
@@ -370,7 +411,7 @@ __device__ __forceinline__ void draw_kept(const SampleArgs& a, Shared& sh, int r
   // two pieces a thread, in index order
   const int p = 2 * tid;
   const u64 m0 = p < a.piece_count ? sh.piece[p] : 0, m1 = p + 1 < a.piece_count ? sh.piece[p + 1] : 0;
-  const u64 incl = wave_scan(m0 + m1, lane);
+  const u64 incl = wave_scan(m0 + m1);
   if (lane == 63) sh.wave_mass[wave] = incl;
   __syncthreads();
   u64 base = 0, all = 0;
@@ -378,9 +419,8 @@ __device__ __forceinline__ void draw_kept(const SampleArgs& a, Shared& sh, int r
     if (i == wave) base = all;
     all += sh.wave_mass[i];
   }
-  const double target = static_cast<double>(a.u[row]) * static_cast<double>(all);
-  const bool past = !(static_cast<double>(all) > target);  // u of 1 and up: the last token with weight
-  const auto over = [&](u64 sum) { return past ? sum >= all : static_cast<double>(sum) > target; };
+  const Border border{static_cast<double>(a.u[row]) * static_cast<double>(all), all};
+  const auto over = [&](u64 sum) { return border.over(sum); };
   const u64 stop = base + incl, start = stop - m0 - m1;
   if (!over(start) && over(stop)) {
     const bool second = !over(start + m0);
@@ -397,7 +437,7 @@ __device__ __forceinline__ void draw_kept(const SampleArgs& a, Shared& sh, int r
     if (word_of(key, i) >= end) mass = w.fixed(key);
     if (static_cast<double>(mass) < least) mass = 0;
   }
-  const u64 sum = wave_scan(mass, lane);
+  const u64 sum = wave_scan(mass);
   if (lane == 63) sh.wave_mass[wave] = sum;  // every thread is past its last use
   __syncthreads();
   u64 before = sh.above + sum - mass;
@@ -425,8 +465,8 @@ __device__ __forceinline__ Where locate(const SampleArgs& a, Shared& sh, int row
     const uint32_t* bin_count = a.bin_count + static_cast<int64_t>(row) * kBins;
     const uint32_t c0 = bin_count[2 * tid], c1 = bin_count[2 * tid + 1];
     const u64 m0 = bin_mass[2 * tid], m1 = bin_mass[2 * tid + 1];
-    const uint32_t count = wave_scan(c0 + c1, lane);
-    const u64 mass = wave_scan(m0 + m1, lane);
+    const uint32_t count = wave_scan(c0 + c1);
+    const u64 mass = wave_scan(m0 + m1);
     if (lane == 63) {
       sh.wave_count[wave] = count;
       sh.wave_mass[wave] = mass;
@@ -578,13 +618,13 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleArgs a) {
   uint32_t top = key[0];
 #pragma unroll
   for (int e = 1; e < 8; ++e) top = max(top, key[e]);
-#pragma unroll
-  for (int d = 1; d < 8; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+  top = max(top, lane_move<0xB1, 0xF>(top));   // lane ^ 1, ^ 2, and 7 - lane: the same in 8 lanes
+  top = max(top, lane_move<0x4E, 0xF>(top));
+  top = max(top, lane_move<0x141, 0xF>(top));
   if ((lane & 7) == 0 && first < n) a.cells[static_cast<int64_t>(row) * a.cell_count + first / kCell] = top;
   const Rule r = rule_of(a, row);
   if (!r.by_piece) return;
-#pragma unroll
-  for (int d = 8; d < 64; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+  top = wave_max(top);
   const Weigh w = weigher(top, r.t);
   double sum = 0.0;
 #pragma unroll
@@ -602,8 +642,19 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   const double* pieces = a.pieces + static_cast<int64_t>(row) * a.piece_count;
   const Rule rule = rule_of(a, row);
 
+  // this thread's cells: the first two in registers
+  constexpr int kHeld = 2;
+  uint32_t cell[kHeld];
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e) cell[e] = tid + e * kDrawThreads < a.cell_count ? cells[tid + e * kDrawThreads] : 0;
+  auto each_cell = [&](auto f) {
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e)
+      if (tid + e * kDrawThreads < a.cell_count) f(tid + e * kDrawThreads, cell[e]);
+    for (int c = tid + kHeld * kDrawThreads; c < a.cell_count; c += kDrawThreads) f(c, cells[c]);
+  };
   uint32_t top = 0;
-  for (int c = tid; c < a.cell_count; c += kDrawThreads) top = max(top, cells[c]);
+  each_cell([&](int, uint32_t key) { top = max(top, key); });
   if (tid == 0) {
     sh.found = 0x7FFFFFFF;
     sh.hits = sh.listed = 0;
@@ -613,11 +664,9 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   const Weigh w = weigher(top, rule.one ? 1.0f : rule.t);
 
   if (rule.one) {
-    for (int c = tid; c < a.cell_count; c += kDrawThreads)
-      if (cells[c] == top) {
-        atomicMin(&sh.found, static_cast<uint32_t>(c));
-        break;
-      }
+    each_cell([&](int c, uint32_t key) {
+      if (key == top) atomicMin(&sh.found, static_cast<uint32_t>(c));
+    });
     __syncthreads();
     if (wave == 0) {
       const int i = static_cast<int>(sh.found) * kCell + lane;
@@ -641,7 +690,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   };
   if (rule.by_piece) {
     for (int p = p0; p < p1; ++p) mine += piece_weight(p);
-    const double incl = wave_scan(mine, lane);
+    const double incl = wave_scan(mine);
     if (lane == 63) sh.wave_sum[wave] = incl;
     __syncthreads();
     double base = 0.0;
@@ -649,8 +698,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
       if (i == wave) base = total;
       total += sh.wave_sum[i];
     }
-    const double up = __shfl_up(incl, 1);
-    before = base + (lane == 0 ? 0.0 : up);
+    before = base + lane_move<0x138, 0xF>(incl);  // wave_shr 1
     mine = base + incl;  // from here on: the sum through this thread's pieces
   }
 
@@ -682,7 +730,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
       wt[e] = key[e] != 0 ? w.weight(key[e]) : 0.0;
       s += wt[e];
     }
-    const double incl = (past ? 0.0 : sh.at) + wave_scan(s, lane), edge = past ? 1e300 : want;
+    const double incl = (past ? 0.0 : sh.at) + wave_scan(s), edge = past ? 1e300 : want;
     const u64 hit = __ballot(incl > edge), some = __ballot(s > 0.0);
     // rounding may leave the piece's own sum a hair short of its weight: its last token with weight then
     const int src = hit != 0 ? __ffsll(hit) - 1 : 63 - __clzll(some | 1);
@@ -718,8 +766,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   uint32_t low = finite ? key_below(kDeepest) : top;
   // The cells that hold weight, the furthest of them
   uint32_t far = top;
-  for (int c = tid; c < a.cell_count; c += kDrawThreads)
-    if (cells[c] >= low) far = min(far, cells[c]);
+  each_cell([&](int, uint32_t key) { far = key >= low ? min(far, key) : far; });
   far = ~block_max(sh, ~far);
   const float spread = 2.0f * (top_x - value_of(far)), reach = kDeepest * rule.t;
   const float width = fminf(fmaxf(spread > 0.0f && spread < reach ? spread : reach, 1e-30f), 1e30f);
@@ -734,11 +781,12 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     // the guess-th largest cell, to within a bin: at least that many tokens reach its smallest member
     for (int i = tid; i < kBins; i += kDrawThreads) sh.bin[i] = 0;
     __syncthreads();
-    for (int c = tid; c < a.cell_count; c += kDrawThreads)
-      if (cells[c] >= low) atomicAdd(&sh.bin[bins.of(cells[c])], 1u);
+    each_cell([&](int, uint32_t key) {
+      if (key >= low) atomicAdd(&sh.bin[bins.of(key)], 1u);
+    });
     if (tid == 0) sh.found = 0;
     __syncthreads();
-    const uint32_t b0 = sh.bin[2 * tid], b1 = sh.bin[2 * tid + 1], incl = wave_scan(b0 + b1, lane);
+    const uint32_t b0 = sh.bin[2 * tid], b1 = sh.bin[2 * tid + 1], incl = wave_scan(b0 + b1);
     if (lane == 63) sh.wave_count[wave] = incl;
     __syncthreads();
     uint32_t stop = incl;
@@ -749,8 +797,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     const int bin = static_cast<int>(sh.found) - 1;
     if (bin >= 0) {
       uint32_t least = top;
-      for (int c = tid; c < a.cell_count; c += kDrawThreads)
-        if (cells[c] >= low && bins.of(cells[c]) <= bin) least = min(least, cells[c]);
+      each_cell([&](int, uint32_t key) { least = key >= low && bins.of(key) <= bin ? min(least, key) : least; });
       low = ~block_max(sh, ~least);
     }
   }
@@ -760,16 +807,16 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   if (floor && finite && !(limit_k && limit_p)) bound = low = max(low, key_below(-log(static_cast<double>(rule.min_p))));
 
   // the list: tokens of `low` and up, from cells that reach it, in no order
-  for (int c0 = wave * 64; c0 < a.cell_count; c0 += kDrawThreads) {
-    const int c = c0 + lane;
-    const bool hit = c < a.cell_count && cells[c] >= low;
-    const u64 who = __ballot(hit);
-    if (who == 0) continue;
-    uint32_t at = 0;
-    if (lane == 0) at = atomicAdd(&sh.hits, static_cast<uint32_t>(__popcll(who)));
-    at = __shfl(at, 0) + lanes_below(who);
-    if (hit && at < kList) sh.hit[at] = c;
-  }
+  // (more than kList tokens may be kept: not tried)
+  if (!limit_k || rule.k <= kList || n <= kList)
+    each_cell([&](int c, uint32_t key) {
+      if (key >= low) {
+        const uint32_t at = atomicAdd(&sh.hits, 1u);
+        if (at < kList) sh.hit[at] = c;
+      }
+    });
+  else if (tid == 0)
+    sh.hits = kList + 1;
   __syncthreads();
   const int hits = static_cast<int>(sh.hits);
   bool small = hits <= kList;
@@ -791,10 +838,12 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
         uint32_t count = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) count += key[e][i] >= low;
-        const uint32_t incl = wave_scan(count, lane);
+        const uint32_t incl = wave_scan(count);
         uint32_t at = 0;
         if (lane == 63) at = atomicAdd(&sh.listed, incl);
-        at = __shfl(at, 63) + incl - count;
+        const uint32_t base = last_lane(at);
+        if (base > kList) j = hits;  // too many: no further step
+        at = base + incl - count;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (key[e][i] >= low) {
@@ -812,17 +861,23 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   if (small) {
     for (int i = tid; i < listed; i += kDrawThreads) sh.mass[i] = w.fixed(key_in(sh.word[i]));
     __syncthreads();
-    u64 held = 0;  // the weight of the top_k
-    if (listed <= kShort) {
-      // each token's place, and the weight before it, from a look at all others: four threads a token
+    u64 held = 0;  // the weight of the top_k, or of the list
+    if (guessed) {
+      for (int i = tid; i < listed; i += kDrawThreads) held += sh.mass[i];
+      held = block_sum(sh, held);
+      small = static_cast<double>(held) >= static_cast<double>(rule.p) * total * kFix;
+    }
+    if (small && listed <= kShort) {
+      // A look from each token at all others, by four threads a token: its
+      // place and the weight before it, then the kept weight before it by index.
       const int i = tid & (kShort - 1), team = tid / kShort, share = (listed + 3) / 4;
+      const int j0 = team * share, j1 = min(j0 + share, listed);
+      const u64 word = i < listed ? sh.word[i] : 0, mass = i < listed ? sh.mass[i] : 0;
       if (i < listed) {
-        const u64 word = sh.word[i];
-        const int j1 = min((team + 1) * share, listed);
         uint32_t rank = 0;
         u64 ahead = 0;
 #pragma unroll 4
-        for (int j = team * share; j < j1; ++j) {
+        for (int j = j0; j < j1; ++j) {
           const bool earlier = sh.word[j] > word;
           rank += earlier;
           ahead += earlier ? sh.mass[j] : 0;
@@ -830,30 +885,49 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
         sh.pairs.rank[team][i] = rank;
         sh.pairs.ahead[team][i] = ahead;
       }
-      if (tid == 0) sh.end = 0;
       __syncthreads();
+      const bool mine = tid < listed;
+      const uint32_t last = static_cast<uint32_t>(min(rule.k, listed)) - 1;
       uint32_t rank = 0;
-      u64 ahead = 0, word = 0, mass = 0;
-      bool within = false;
-      if (tid < listed) {
+      u64 ahead = 0;
+      if (mine) {
         for (int t = 0; t < 4; ++t) {
           rank += sh.pairs.rank[t][tid];
           ahead += sh.pairs.ahead[t][tid];
         }
-        word = sh.word[tid];
-        mass = sh.mass[tid];
-        within = rank < static_cast<uint32_t>(rule.k);
-        if (!limit_p && rank + 1 == static_cast<uint32_t>(rule.k)) sh.end = word;
+        if (rank == last) sh.above = ahead + mass;
       }
-      held = block_sum(sh, within ? mass : 0);
-      const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total * kFix);
-      if (limit_p && within && static_cast<double>(ahead) < want &&
-          (static_cast<double>(ahead + mass) >= want || rank + 1 == static_cast<uint32_t>(rule.k)))
-        sh.end = word;
       __syncthreads();
-      end = sh.end;
-      small = !(guessed && static_cast<double>(held) < want);
-    } else {
+      const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(sh.above) : total * kFix);
+      const bool in = mine && rank <= last && (rank == 0 || !limit_p || static_cast<double>(ahead) < want) &&
+                      static_cast<double>(mass) >= least;
+      if (mine) sh.mass[tid] = in ? mass : 0;
+      __syncthreads();
+      if (i < listed) {
+        const uint32_t mark = static_cast<uint32_t>(index_in(word));
+        u64 sum = 0, all = 0;
+#pragma unroll 4
+        for (int j = j0; j < j1; ++j) {
+          const u64 m = sh.mass[j];
+          all += m;
+          sum += static_cast<uint32_t>(index_in(sh.word[j])) <= mark ? m : 0;
+        }
+        sh.pairs.ahead[team][i] = sum;
+        if (i == 0) sh.wave_mass[team] = all;
+      }
+      __syncthreads();
+      if (!in) return;
+      const u64 all = sh.wave_mass[0] + sh.wave_mass[1] + sh.wave_mass[2] + sh.wave_mass[3];
+      u64 sum = 0;
+      for (int t = 0; t < 4; ++t) sum += sh.pairs.ahead[t][tid];
+      const Border border{static_cast<double>(a.u[row]) * static_cast<double>(all), all};
+      if (border.over(sum) && !border.over(sum - mass)) {
+        a.tokens[row] = index_in(word);
+        a.probs[row] = static_cast<float>(w.weight(key_in(word)) * kFix / static_cast<double>(all));
+      }
+      return;
+    }
+    if (small) {
       const auto item = [&](int i, bool, u64& word, u64& mass) {
         word = sh.word[i];
         mass = sh.mass[i];
@@ -861,11 +935,13 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
       };
       if (limit_k && rule.k < listed) end = select_word(sh, item, listed, false, rule.k, 0);
       if (limit_p) {
-        for (int i = tid; i < listed; i += kDrawThreads) held += sh.word[i] >= end ? sh.mass[i] : 0;
-        held = block_sum(sh, held);
+        if (limit_k) {
+          held = 0;
+          for (int i = tid; i < listed; i += kDrawThreads) held += sh.word[i] >= end ? sh.mass[i] : 0;
+          held = block_sum(sh, held);
+        }
         const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total * kFix);
-        small = !(guessed && static_cast<double>(held) < want);
-        if (small) end = max(end, select_word(sh, item, listed, true, want, 0));
+        end = max(end, select_word(sh, item, listed, true, want, 0));
       }
     }
   }
@@ -955,10 +1031,10 @@ __global__ __launch_bounds__(kDrawThreads) void sample_wide_kernel(SampleArgs a)
         else if (b <= where.last || b == where.k_bin) in_list |= 1u << e;
       }
       if (__ballot(in_list != 0) != 0) {
-        const uint32_t count = __popc(in_list), incl = wave_scan(count, lane);
+        const uint32_t count = __popc(in_list), incl = wave_scan(count);
         uint32_t at = 0;
         if (lane == 63) at = atomicAdd(&sh.hits, incl);
-        at = __shfl(at, 63) + incl - count;
+        at = last_lane(at) + incl - count;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if ((in_list >> e) & 1u) {
