@@ -1,6 +1,7 @@
 // Device helpers shared by the attention kernels over the 8-bit cache.
 #pragma once
 
+#include "lanes_device.h"
 #include "mxq_device.h"
 #include "serve_internal.h"
 

@@ -78,8 +78,7 @@ __device__ Part find_part(const AttendArgs& a, int slot, int seq) {
     mine = share_of<MT>(a, s0 + lane);
     total += static_cast<long long>(mine.chunks) * mine.groups * hk;
   }
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) total += __shfl_xor(total, d);
+  total = wave_sum(total);
   const long long even = (total + a.target - 1) / a.target;
   Part p{};
   p.step = static_cast<int>(max(even, static_cast<long long>(kMinChunks)));
@@ -88,26 +87,21 @@ __device__ Part find_part(const AttendArgs& a, int slot, int seq) {
     if (a.seqs > 64) mine = share_of<MT>(a, s0 + lane);
     const int splits = max(1, (mine.chunks + p.step - 1) / p.step);
     const int count = mine.groups * splits * hk;
-    int sum = count;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
-    }
+    const int sum = wave_scan(count);
     const unsigned long long hit = slot >= 0 ? __ballot(before + sum > slot) : (seq < s0 + 64 ? 1ull << (seq - s0) : 0);
     if (hit != 0) {
       const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
       p.any = true;
       p.seq = s0 + src;
-      p.base = before + __shfl(sum, src) - __shfl(count, src);
+      p.base = before + __builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(count, src);
       p.nth = slot - p.base;
-      p.splits = __shfl(splits, src);
-      p.share.c0 = __shfl(mine.c0, src);
-      p.share.chunks = __shfl(mine.chunks, src);
-      p.share.groups = __shfl(mine.groups, src);
+      p.splits = __builtin_amdgcn_readlane(splits, src);
+      p.share.c0 = __builtin_amdgcn_readlane(mine.c0, src);
+      p.share.chunks = __builtin_amdgcn_readlane(mine.chunks, src);
+      p.share.groups = __builtin_amdgcn_readlane(mine.groups, src);
       return p;
     }
-    before += __shfl(sum, 63);
+    before += last_lane(sum);
   }
   return p;
 }
@@ -445,15 +439,28 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   const int team = threadIdx.x / kLanes, d = (threadIdx.x - team * kLanes) * 4;
   float top = kNegInf, total = 0.0f;
   f4 y = f4{0, 0, 0, 0};
-  for (int s = team; s < part.splits; s += kTeams) {
-    const int64_t at = (part.base + (static_cast<int64_t>(s) * part.share.groups + rg) * hk + head) * kRows + row;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-    const f4 v = *reinterpret_cast<const f4*>(a.part + at * DIM + d);
-    const float now = fmaxf(top, ml.x), ref = now == kNegInf ? 0.0f : now;
-    const float e0 = __builtin_amdgcn_exp2f(top - ref), e1 = __builtin_amdgcn_exp2f(ml.x - ref);
-    y = y * e0 + v * e1;
-    total = total * e0 + ml.y * e1;
-    top = now;
+  // four parts at a time, so that their loads run together
+  for (int s0 = team; s0 < part.splits; s0 += 4 * kTeams) {
+    float2 ml[4];
+    f4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = min(s0 + i * kTeams, part.splits - 1);
+      // (starts that descend may give more than there are: not read)
+      const int64_t slot = min(part.base + (static_cast<int64_t>(s) * part.share.groups + rg) * hk + head, static_cast<int64_t>(a.slots) - 1);
+      const int64_t at = slot * kRows + row;
+      ml[i] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+      v[i] = *reinterpret_cast<const f4*>(a.part + at * DIM + d);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s0 + i * kTeams >= part.splits) continue;
+      const float now = fmaxf(top, ml[i].x), ref = now == kNegInf ? 0.0f : now;
+      const float e0 = __builtin_amdgcn_exp2f(top - ref), e1 = __builtin_amdgcn_exp2f(ml[i].x - ref);
+      y = y * e0 + v[i] * e1;
+      total = total * e0 + ml[i].y * e1;
+      top = now;
+    }
   }
   *reinterpret_cast<f4*>(&sums[team][d]) = y;
   if (d == 0) {
@@ -531,6 +538,7 @@ hipError_t launch_attend(const AttendArgs& given, const DeviceInfo& dev) {
   const bool joined = few && static_cast<int64_t>(a.width) * a.pool.block > kMinChunks * kChunk;
   const int64_t slots = ends + (joined ? a.target : 0);
   if (slots > INT32_MAX) return hipErrorInvalidValue;
+  a.slots = static_cast<int>(slots);
   const size_t sums = joined ? static_cast<size_t>(slots) * per * a.pool.dim * 4 : 0;
   const size_t few_bytes = joined ? sums + static_cast<size_t>(slots) * per * 8 : 0;
 

@@ -83,20 +83,15 @@ __device__ bool find_tile(const AttendArgs& a, int index, int& seq, int& first) 
   int before = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     const int count = tiles_of(a, s0 + lane);
-    int sum = count;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
-    }
+    const int sum = wave_scan(count);
     const unsigned long long hit = index >= 0 ? __ballot(before + sum > index) : (seq < s0 + 64 ? 1ull << (seq - s0) : 0);
     if (hit != 0) {
       const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
       seq = s0 + src;
-      first = before + __shfl(sum, src) - __shfl(count, src);
+      first = before + __builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(count, src);
       return true;
     }
-    before += __shfl(sum, 63);
+    before += last_lane(sum);
   }
   return false;
 }
@@ -440,7 +435,7 @@ __global__ __launch_bounds__(64) void attend_many_join_kernel(AttendArgs a) {
   float top = kNegInf, total = 0.0f;
   f4 y = f4{0, 0, 0, 0};
   for (int s = 0; s < a.many_splits; ++s) {
-    const int64_t at = ((tile * a.many_splits + s) * hk + head) * kManyRows + i % kManyRows;
+    const int64_t at = min((tile * a.many_splits + s) * hk + head, static_cast<int64_t>(a.many_units) - 1) * kManyRows + i % kManyRows;
     const float2 ml = *reinterpret_cast<const float2*>(a.many_ml + at * 2);
     const f4 v = *reinterpret_cast<const f4*>(a.many_part + at * DIM + d);
     const float now = fmaxf(top, ml.x), ref = now == kNegInf ? 0.0f : now;
@@ -494,6 +489,7 @@ hipError_t launch_many(const AttendArgs& given, float* ws) {
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
   a.many_part = ws;
+  a.many_units = static_cast<int>(grid);
   a.many_ml = ws + grid * kManyRows * a.pool.dim;
   const unsigned g = static_cast<unsigned>(grid);
   if (a.pool.dim == 64) return a.bf16 ? launch_many_of<64, true>(a, g) : launch_many_of<64, false>(a, g);

@@ -11,6 +11,7 @@
 // workgroups share a scale and nothing is atomic.  v is stored
 // transposed ([dim, block]): its codes pass through LDS and leave 16 tokens a
 // lane; a 16-token piece that also holds older tokens is merged with them.
+#include "lanes_device.h"
 #include "mxq_device.h"
 #include "serve_internal.h"
 
@@ -50,19 +51,14 @@ __device__ Touched find_block(const KvAppendArgs& a, int unit) {
     int t0 = 0, n = 0, first = 0;
     if (s < a.seqs) new_tokens(a, s, t0, n, first);
     const int count = n > 0 ? (first + n - 1) / b - first / b + 1 : 0;
-    int sum = count;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
-    }
+    const int sum = wave_scan(count);
     const unsigned long long hit = __ballot(before + sum > unit);
     if (hit != 0) {
-      const int src = __ffsll(hit) - 1;
-      const int nth = unit - before - (__shfl(sum, src) - __shfl(count, src));
-      t0 = __shfl(t0, src);
-      n = __shfl(n, src);
-      first = __shfl(first, src);
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
+      const int nth = unit - before - (__builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(count, src));
+      t0 = __builtin_amdgcn_readlane(t0, src);
+      n = __builtin_amdgcn_readlane(n, src);
+      first = __builtin_amdgcn_readlane(first, src);
       r.seq = s0 + src;
       r.j = first / b + nth;
       r.lo = max(first, r.j * b);
@@ -71,7 +67,7 @@ __device__ Touched find_block(const KvAppendArgs& a, int unit) {
       r.any = true;
       return r;
     }
-    before += __shfl(sum, 63);
+    before += last_lane(sum);
   }
   return r;
 }

@@ -37,6 +37,7 @@
 //           equal logits) it searches the row itself
 #include <cfloat>
 
+#include "lanes_device.h"
 #include "mxq_device.h"
 #include "serve_internal.h"
 
@@ -44,7 +45,6 @@ namespace mxq {
 
 namespace {
 
-typedef unsigned long long u64;
 constexpr int kDrawThreads = 1024, kDrawWaves = 16;
 constexpr int kCell = 64, kPiece = 512, kStatTokens = 2048;  // tokens of a cell, a piece, a stats workgroup
 constexpr int kList = 2048, kShort = 256, kBins = 2048, kMaxPieces = 2048;
@@ -72,24 +72,36 @@ __device__ __forceinline__ float load_logit(const void* row, int i) {
   else return sb_to_f32<T == kBF16In>(static_cast<const uint16_t*>(row)[i]);
 }
 
-// Keys of 8 tokens from i on; 0 past n.  `wide`: they are 16-byte aligned.
+// Keys of 8 tokens from i on; 0 past n.  Rows may start at any element: the
+// loads are wide all the same, global memory takes them at any address.
 template <int T>
-__device__ __forceinline__ void load_keys8(const void* row, int i, int n, bool wide, uint32_t (&key)[8]) {
-  if (wide && i + 8 <= n) {
+__device__ __forceinline__ void load_keys8(const void* row, int i, int n, uint32_t (&key)[8]) {
+  const int at = min(i, max(n - 8, 0));  // a whole piece, or the row's last 8
+  if (n >= 8) {
     float f[8];
     if constexpr (T == kF32In) {
-      __builtin_memcpy(f, static_cast<const float*>(row) + i, 32);
+      __builtin_memcpy(f, static_cast<const float*>(row) + at, 32);
     } else {
-      const u4 v = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(row) + i);
-      const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+      uint16_t h[8];
+      __builtin_memcpy(h, static_cast<const uint16_t*>(row) + at, 16);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = sb_to_f32<T == kBF16In>(static_cast<uint16_t>(d[e >> 1] >> (16 * (e & 1))));
+      for (int e = 0; e < 8; ++e) f[e] = sb_to_f32<T == kBF16In>(h[e]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) key[e] = key_of(f[e]);
+    if (at != i) {  // the first of them belong to the piece before
+      const int skip = i - at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t k = 0;
+#pragma unroll
+        for (int d = e; d < 8; ++d) k = d == e + skip ? key[d] : k;
+        key[e] = k;
+      }
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) key[e] = i + e < n ? key_of(load_logit<T>(row, i + e)) : 0;
+    for (int e = 0; e < 8; ++e) key[e] = i + e < n ? key_of(load_logit<T>(row, min(i + e, n - 1))) : 0;
   }
 }
 
@@ -153,66 +165,6 @@ __device__ __forceinline__ Rule rule_of(const SampleArgs& a, int row) {
   return r;
 }
 
-// x of another lane by a DPP control, 0 where there is none (or the lane's row
-// of 16 is not in `rows`): a few cycles, where a shuffle through LDS takes 100.
-template <int CTRL, int ROWS, typename V>
-__device__ __forceinline__ V lane_move(V x) {
-  static_assert(sizeof(V) == 4 || sizeof(V) == 8, "one or two registers");
-  if constexpr (sizeof(V) == 4) {
-    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false));
-  } else {
-    const u64 w = __builtin_bit_cast(u64, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(w), CTRL, ROWS, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(w >> 32), CTRL, ROWS, 0xF, false);
-    return __builtin_bit_cast(V, (static_cast<u64>(hi) << 32) | lo);
-  }
-}
-template <typename V>
-__device__ __forceinline__ V last_lane(V x) {
-  if constexpr (sizeof(V) == 4) {
-    return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
-  } else {
-    const u64 w = __builtin_bit_cast(u64, x);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(w), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(w >> 32), 63);
-    return __builtin_bit_cast(V, (static_cast<u64>(hi) << 32) | lo);
-  }
-}
-// Inclusive sums over the lanes, in their order: within rows of 16, then the
-// rows' last lanes handed on.
-template <typename V>
-__device__ __forceinline__ V wave_scan(V x) {
-  x += lane_move<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8
-  x += lane_move<0x112, 0xF>(x);
-  x += lane_move<0x114, 0xF>(x);
-  x += lane_move<0x118, 0xF>(x);
-  x += lane_move<0x142, 0xA>(x);  // row_bcast 15, 31
-  x += lane_move<0x143, 0xC>(x);
-  return x;
-}
-template <typename V>
-__device__ __forceinline__ V wave_sum(V x) { return last_lane(wave_scan(x)); }
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-  x = max(x, lane_move<0x111, 0xF>(x));
-  x = max(x, lane_move<0x112, 0xF>(x));
-  x = max(x, lane_move<0x114, 0xF>(x));
-  x = max(x, lane_move<0x118, 0xF>(x));
-  x = max(x, lane_move<0x142, 0xA>(x));
-  x = max(x, lane_move<0x143, 0xC>(x));
-  return last_lane(x);
-}
-__device__ __forceinline__ u64 wave_or(u64 x) {
-  x |= lane_move<0x111, 0xF>(x);
-  x |= lane_move<0x112, 0xF>(x);
-  x |= lane_move<0x114, 0xF>(x);
-  x |= lane_move<0x118, 0xF>(x);
-  x |= lane_move<0x142, 0xA>(x);
-  x |= lane_move<0x143, 0xC>(x);
-  return last_lane(x);
-}
-// How many of the lanes below this one are in `who`.
-__device__ __forceinline__ int lanes_below(u64 who) {
-  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(who >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(who), 0));
-}
 __device__ __forceinline__ const void* row_of(const SampleArgs& a, int row, int size) {
   return static_cast<const char*>(a.logits) + static_cast<int64_t>(row) * a.row_stride * size;
 }
@@ -285,7 +237,7 @@ __device__ __forceinline__ uint32_t block_max(Shared& sh, uint32_t x) {
 }
 
 // The word at which the count (or weight) of the larger ones and its own
-// reaches `want`, or 0, digit by digit (8 bits) from the first in which the
+// reaches `want`, or 0, digit by digit (8 bits) from the first bit in which the
 // words differ.  get(i, word, mass) gives item i of `m`, or false; `above` is
 // what is larger than all items.
 template <typename Get>
@@ -313,10 +265,10 @@ __device__ __forceinline__ u64 select_word(Shared& sh, Get get, int m, bool by_m
   }
   if (some == 0) return 0;
   const u64 differ = some & ~any;
-  int shift = differ != 0 ? (63 - __clzll(differ)) / 8 * 8 : 0;
+  int shift = max(56 - __clzll(differ | 1), 0);  // the first differing bit is the digit's highest
   u64 mask = ~0ull << shift << 8, prefix = some & any & mask;
 #pragma clang loop unroll(disable)
-  for (; shift >= 0; shift -= 8) {
+  for (;; shift = max(shift - 8, 0)) {
     __syncthreads();
     if (tid < 256) {
       sh.digit.mass[tid] = 0;
@@ -358,7 +310,8 @@ __device__ __forceinline__ u64 select_word(Shared& sh, Get get, int m, bool by_m
     prefix |= static_cast<u64>(sh.found - 1) << shift;
     above = sh.above;
     mask |= 255ull << shift;
-    if (sh.hits == 1 && shift > 0) {  // it alone
+    if (shift == 0) return prefix;
+    if (sh.hits == 1) {  // it alone
       for (int i = tid; i < m; i += kDrawThreads) {
         u64 word, mass;
         if (get(i, false, word, mass) && (word & mask) == prefix) sh.end = word;
@@ -367,7 +320,6 @@ __device__ __forceinline__ u64 select_word(Shared& sh, Get get, int m, bool by_m
       return sh.end;
     }
   }
-  return prefix;
 }
 
 // Of a wave's 8 keys a lane those that `which` holds for, put side by side into
@@ -614,7 +566,7 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleArgs a) {
   const int first = blockIdx.x * kStatTokens + threadIdx.x * 8;
   const void* x = row_of(a, row, T == kF32In ? 4 : 2);
   uint32_t key[8];
-  load_keys8<T>(x, first, n, a.wide, key);
+  load_keys8<T>(x, first, n, key);
   uint32_t top = key[0];
 #pragma unroll
   for (int e = 1; e < 8; ++e) top = max(top, key[e]);
@@ -723,7 +675,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     const bool past = sh.found == 0;
     const int p = past ? a.piece_count - 1 : static_cast<int>(sh.found) - 1, i0 = p * kPiece + lane * 8;
     uint32_t key[8];
-    load_keys8<T>(x, i0, n, a.wide, key);
+    load_keys8<T>(x, i0, n, key);
     double wt[8], s = 0.0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -821,36 +773,26 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   const int hits = static_cast<int>(sh.hits);
   bool small = hits <= kList;
   if (small) {
-    // 8 cells a wave at a time, 8 tokens a lane, two such steps in flight
+    // 8 cells a wave at a time, 8 tokens a lane
 #pragma clang loop unroll(disable)
-    for (int j = wave * 8; j < hits; j += 2 * kDrawWaves * 8) {
-      uint32_t key[2][8];
-      int first[2];
+    for (int j = wave * 8; j < hits; j += kDrawWaves * 8) {
+      const int h = j + (lane >> 3), first = h < hits ? sh.hit[h] * kCell + (lane & 7) * 8 : n;
+      uint32_t key[8], count = 0;
+      load_keys8<T>(x, first, n, key);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = j + e * kDrawWaves * 8 + (lane >> 3);
-        first[e] = h < hits ? sh.hit[h] * kCell + (lane & 7) * 8 : n;
-      }
+      for (int i = 0; i < 8; ++i) count += key[i] >= low;
+      const uint32_t incl = wave_scan(count);
+      uint32_t at = 0;
+      if (lane == 63) at = atomicAdd(&sh.listed, incl);
+      const uint32_t base = last_lane(at);
+      if (base > kList) break;  // too many
+      at = base + incl - count;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) load_keys8<T>(x, first[e], n, a.wide, key[e]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t count = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) count += key[e][i] >= low;
-        const uint32_t incl = wave_scan(count);
-        uint32_t at = 0;
-        if (lane == 63) at = atomicAdd(&sh.listed, incl);
-        const uint32_t base = last_lane(at);
-        if (base > kList) j = hits;  // too many: no further step
-        at = base + incl - count;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (key[e][i] >= low) {
-            if (at < kList) sh.word[at] = word_of(key[e][i], first[e] + i);
-            ++at;
-          }
-      }
+      for (int i = 0; i < 8; ++i)
+        if (key[i] >= low) {
+          if (at < kList) sh.word[at] = word_of(key[i], first + i);
+          ++at;
+        }
     }
     __syncthreads();
     small = sh.listed <= kList;
@@ -982,7 +924,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_bins_kernel(SampleArgs a)
   const int upto = min((static_cast<int>(blockIdx.x) + 1) * a.span, a.vocab);
   for (int i = blockIdx.x * a.span + wave * kPiece; i < upto; i += kDrawWaves * kPiece) {
     uint32_t key[8];
-    load_keys8<T>(x, i + lane * 8, a.vocab, a.wide, key);
+    load_keys8<T>(x, i + lane * 8, a.vocab, key);
     // those that can be kept, side by side
     const int held = compact(key, some[wave], [&](uint32_t k) { return k >= plan.low; });
     for (int j = lane; j < held; j += 64) {
@@ -1022,7 +964,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_wide_kernel(SampleArgs a)
     for (int q = blockIdx.x * (a.span / kPiece) + wave; q < p_end; q += kDrawWaves) {
       const int i = q * kPiece + lane * 8;
       uint32_t key[8], in_list = 0, sure = 0;
-      load_keys8<T>(x, i, n, a.wide, key);
+      load_keys8<T>(x, i, n, key);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int b = bins.of(key[e]);
@@ -1161,8 +1103,6 @@ hipError_t launch_sample_type(const SampleArgs& a, int64_t most_rows, bool wide,
 
 hipError_t launch_sample(const SampleArgs& given, const DeviceInfo& dev) {
   SampleArgs a = given;
-  const int size = a.type == kF32In ? 4 : 2;
-  a.wide = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.rows == 1 || (a.row_stride * size) % 16 == 0);
   a.cell_count = (a.vocab + kCell - 1) / kCell;
   a.piece_count = (a.vocab + kPiece - 1) / kPiece;
   // a row longer than a list may need the last two kernels, unless its settings are known here and ask for no prefix

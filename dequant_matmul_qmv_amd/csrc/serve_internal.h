@@ -107,12 +107,14 @@ struct AttendArgs {
   // set by the launcher
   float* part;            // sums [slots, rows, dim]
   float* part_ml;         // (maximum, weight) [slots, rows, 2]
+  int slots;              // of them
   int target;             // workgroups the few-row work is split for
   int few_rows;           // most rows (new tokens times group) of a sequence that the few-row kernel takes
   int join_new;           // most new tokens of such a sequence
   float* many_part;       // the same of the many-row kernel
   float* many_ml;
   int many_splits;        // parts of its key axis
+  int many_units;         // workgroups
 };
 // The many-row kernel (attend_many.hip): its tiles at most, the bytes of its
 // partial results, its launch (with the second one that joins them).
@@ -153,7 +155,6 @@ struct SampleArgs {
   uint32_t* cells;     // largest key of each 64 tokens [rows, cell_count]
   double* pieces;      // weight of each 512 tokens [rows, piece_count]
   int cell_count, piece_count;
-  bool wide;           // rows are 16-byte aligned
   // of rows whose kept tokens are more than a list (null where none can be)
   SamplePlan* plans;
   unsigned long long* bin_mass;  // weight of each bin by value [rows, 2048]
