@@ -39,6 +39,11 @@ namespace {
 constexpr int kFewThreads = 256, kFewWaves = 4;
 constexpr int kChunk = 64;      // keys a wave takes at a time
 constexpr int kMinChunks = 4;   // at least one chunk for each wave of a workgroup
+// Tables of up to this many keys are not split: four rounds of a workgroup's
+// waves.  One sequence of 8 kv heads, split and joined / not split: 11.5 / 10.3 us
+// at 777 keys of 64 values, 11.1 / 12.8 us at 128 values; 11.1 / 9.0 us at 512 keys;
+// inside a graph, which then has no workspace to allocate, 20 / 7 .. 13 us.
+constexpr int kLoneKeys = 1024;
 constexpr float kTiny = 1e-30f;
 
 // One sequence's share of the few-row work.
@@ -81,7 +86,7 @@ __device__ Part find_part(const AttendArgs& a, int slot, int seq) {
   total = wave_sum(total);
   const long long even = (total + a.target - 1) / a.target;
   Part p{};
-  p.step = static_cast<int>(max(even, static_cast<long long>(kMinChunks)));
+  p.step = static_cast<int>(max(even, static_cast<long long>(a.min_chunks)));
   int before = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     if (a.seqs > 64) mine = share_of<MT>(a, s0 + lane);
@@ -535,7 +540,8 @@ hipError_t launch_attend(const AttendArgs& given, const DeviceInfo& dev) {
   int64_t few_total = all_rows;
   if (many && few_total > static_cast<int64_t>(a.seqs) * kFewRows) few_total = static_cast<int64_t>(a.seqs) * kFewRows;
   const int64_t per = 16 * mt, ends = few ? (few_total / per + a.seqs) * hk : 0;
-  const bool joined = few && static_cast<int64_t>(a.width) * a.pool.block > kMinChunks * kChunk;
+  const bool joined = few && static_cast<int64_t>(a.width) * a.pool.block > kLoneKeys;
+  a.min_chunks = joined ? kMinChunks : kLoneKeys / kChunk;
   const int64_t slots = ends + (joined ? a.target : 0);
   if (slots > INT32_MAX) return hipErrorInvalidValue;
   a.slots = static_cast<int>(slots);

@@ -109,6 +109,7 @@ struct AttendArgs {
   float* part_ml;         // (maximum, weight) [slots, rows, 2]
   int slots;              // of them
   int target;             // workgroups the few-row work is split for
+  int min_chunks;         // least 64-key chunks of a part
   int few_rows;           // most rows (new tokens times group) of a sequence that the few-row kernel takes
   int join_new;           // most new tokens of such a sequence
   float* many_part;       // the same of the many-row kernel
