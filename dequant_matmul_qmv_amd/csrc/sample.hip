@@ -942,12 +942,14 @@ __global__ __launch_bounds__(kDrawThreads) void sample_bins_kernel(SampleArgs a)
   }
 }
 
-template <int T>
+// JOINED: the row's last workgroup draws.  Without that the kernel needs few
+// registers, and two workgroups fit a compute unit (192 rows: 36 us with both in one).
+template <int T, bool JOINED>
 __global__ __launch_bounds__(kDrawThreads) void sample_wide_kernel(SampleArgs a) {
   __shared__ Shared sh;
   const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.vocab;
   const SamplePlan plan = a.plans[row];
-  if (plan.state == kDone || (plan.state == kSearch && (blockIdx.x != 0 || !a.joined))) return;
+  if (plan.state == kDone || (plan.state == kSearch && (blockIdx.x != 0 || !JOINED))) return;
   const void* x = row_of(a, row, T == kF32In ? 4 : 2);
   const Rule rule = rule_of(a, row);
   const Weigh w = weigher(plan.top, rule.t);
@@ -1003,7 +1005,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_wide_kernel(SampleArgs a)
     __syncthreads();
     for (uint32_t i = tid; i < min(own, static_cast<uint32_t>(kList)); i += kDrawThreads)
       if (sh.found + i < kList) list[sh.found + i] = sh.word[i];
-    if (!a.joined) return;
+    if constexpr (!JOINED) return;
     // the row's last workgroup goes on, with what all have written
     __syncthreads();
     if (tid == 0) {
@@ -1014,7 +1016,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_wide_kernel(SampleArgs a)
     __syncthreads();
     if (sh.found + 1 != gridDim.x) return;
   }
-  finish_row<T>(a, sh, row, x, rule, w, bins, plan, where);
+  if constexpr (JOINED) finish_row<T>(a, sh, row, x, rule, w, bins, plan, where);
 }
 
 template <int T>
@@ -1087,11 +1089,12 @@ hipError_t launch_sample_type(const SampleArgs& a, int64_t most_rows, bool wide,
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     // a last workgroup has to wait for its caches' write-back: less than a launch for few of them, more for many
-    b.joined = static_cast<int64_t>(grid.x) * rows <= num_cu;
-    hipLaunchKernelGGL(sample_wide_kernel<T>, grid, dim3(kDrawThreads), 0, a.stream, b);
+    const bool joined = static_cast<int64_t>(grid.x) * rows <= num_cu;
+    if (joined) hipLaunchKernelGGL((sample_wide_kernel<T, true>), grid, dim3(kDrawThreads), 0, a.stream, b);
+    else hipLaunchKernelGGL((sample_wide_kernel<T, false>), grid, dim3(kDrawThreads), 0, a.stream, b);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (b.joined) continue;
+    if (joined) continue;
     hipLaunchKernelGGL(sample_finish_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kDrawThreads), 0, a.stream, b);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
