@@ -194,6 +194,36 @@ def test_scales_of_any_size(new):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 1, 64), (2, 2, 128)])
+def test_long_sequences(heads, kv_heads, dim, t):
+    """Key axes split into many parts, beside short ones; one token and drafts."""
+    _run([9000, 3, 2500, 0, 1024, 1025], [1] * 6, heads, kv_heads, dim, 32, t, seed=13)
+    _run([7001, 40], [3, 2], heads, kv_heads, dim, 64, t, window=6000, seed=14)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 260])
+@pytest.mark.parametrize("step", [1.0, -1.0])
+def test_rising_and_falling_scores(new, step):
+    """Scores whose largest grows (or falls) from page to page, far past what one reference can stand for."""
+    gen = torch.Generator().manual_seed(15)
+    block, length = 16, 400
+    blocks, tab = paging([length], block, gen)
+    pool = list(random_pool(blocks, 1, block, 64, gen))
+    for j in range(length // block):
+        pool[2][int(tab[0, j])] = 0.002 * 2.0 ** (0.25 * step * (j - 12))
+    q = torch.randn(new, 3, 64, generator=gen).half()
+    ref = attention_ref(q, pool, tab, [length], [new], 0, 1.0)
+    cache = mxq.KvCache(*[x.to(DEV) for x in pool])
+    note(f"attention scores by page, step {step}, {new} new")
+    out, lse = mxq.mxq_attention(q.to(DEV), cache, tab.to(DEV), torch.tensor([length], dtype=torch.int32, device=DEV),
+                                 torch.tensor([0, new], dtype=torch.int32, device=DEV), scale=1.0, return_lse=True)
+    torch.cuda.synchronize()
+    _check(out, lse, ref, "scores by page")
+
+
+@pytest.mark.gpu
 def test_no_pages_at_all():
     cache = mxq.KvCache.empty(0, 2, 16, 64, DEV)
     q = torch.ones(3, 4, 64, dtype=torch.float16, device=DEV)

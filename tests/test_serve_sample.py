@@ -157,6 +157,56 @@ def test_settings_at_their_ends():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "f32"])
+@pytest.mark.parametrize("rows,vocab", [(300, 9001), (1030, 2100), (40, 70001)])
+def test_many_rows(rows, vocab, t):
+    """More rows than one launch holds, and more than one last workgroup a row would serve; every row its own settings."""
+    x, u = _logits(rows, vocab, t, 30 + rows, spread=1.5)
+    cols = [[SETTINGS[(7 * r) % len(SETTINGS)][j] for r in range(rows)] for j in range(4)]
+    _check(x, u, *cols, f"sample rows={rows} vocab={vocab} {t}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 200])
+def test_wide_prefixes(rows):
+    """Flat rows: prefixes of thousands of tokens by count, by weight, by both, and cut by min-p."""
+    x, u = _logits(rows, 20000, "f32", 40, spread=0.7)
+    for s in ((1.0, 0, 0.9, 0.0), (1.0, 9000, 1.0, 0.0), (2.0, 9000, 0.8, 0.0), (2.0, 9000, 0.8, 0.01), (1.0, 0, 1.0, 1e-4),
+              (5.0, 0, 0.99, 0.02), (3.0, 19999, 0.999, 0.0)):
+        _check(x, u, *s, f"sample wide rows={rows} {s}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [2, 150])
+def test_wide_prefixes_of_equals(rows):
+    """More equal logits than a list holds: the end of the prefix is found in the row itself."""
+    gen = torch.Generator().manual_seed(41)
+    x = torch.randint(0, 3, (rows, 15000), generator=gen).float().half()
+    u = torch.rand(rows, generator=gen)
+    for s in ((1.0, 7000, 1.0, 0.0), (1.0, 0, 0.7, 0.0), (1.5, 12000, 0.9, 0.3), (1.0, 6000, 0.5, 0.0)):
+        _check(x, u, *s, f"sample equals rows={rows} {s}")
+
+
+@pytest.mark.gpu
+def test_odd_base_of_every_type():
+    for t in ("f16", "bf16", "f32"):
+        x, u = _logits(4, 3001, t, 42)
+        wide = torch.full((4, 3011), 50.0).to(TYPES[t])
+        wide[:, 5:3006] = x
+        view = wide.to(DEV)[:, 5:3006]
+        for s in ((0.9, 40, 0.9, 0.0), (1.7, 0, 0.95, 0.0), (1.0, 0, 1.0, 0.0), (1.0, 2500, 1.0, 0.0)):
+            note(f"sample odd base {t} {s}")
+            kw = dict(temperature=s[0], top_k=s[1], top_p=s[2], min_p=s[3])
+            a, b = mxq.mxq_sample(view, u.to(DEV), **kw), mxq.mxq_sample(x.to(DEV), u.to(DEV), **kw)
+            torch.cuda.synchronize()
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for n in (1, 5, 7, 8, 9):
+        gen = torch.Generator().manual_seed(43 + n)
+        x, u = torch.randn(4, n, generator=gen).half(), torch.rand(4, generator=gen)
+        _check(x, u, 1.0, 0, 0.9, 0.0, f"sample vocab={n}")
+
+
+@pytest.mark.gpu
 def test_strided_rows_and_odd_base():
     x, u = _logits(6, 4001, "f16", 8)
     wide = torch.zeros(6, 4500, dtype=torch.float16)
