@@ -232,3 +232,29 @@ def test_append_zeros_and_places_missing():
         return tab
     _run_append([60, 60], [60, 30], 2, 16, 64, "f16", 23, table=spoil)
     _run_append([60, 60], [60, 50], 2, 16, 64, "f16", 23, table=lambda tab: tab[:, :2].contiguous())
+
+
+# ------------------------------------------------------------------------------------------------ larger than the L2s
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_beyond_the_caches(interleaved, t):
+    """More bytes than the L2s hold, out of a fused projection and in place; more units a token than are loaded ahead."""
+    gen = torch.Generator().manual_seed(51)
+    n, heads, kv_heads, dim, half = 1100, 28, 4, 256, 48
+    base = torch.randn(n, (heads + 2 * kv_heads) * dim, generator=gen).to(HALF[t])
+    qkv = base.to(DEV)
+    q = qkv[:, :heads * dim].view(n, heads, dim)
+    k = qkv[:, heads * dim:(heads + kv_heads) * dim].view(n, kv_heads, dim)
+    f = (10000.0 ** (-torch.arange(half) / half)).float().to(DEV)
+    pos = torch.randint(0, 131072, (n,), generator=gen, dtype=torch.int32).to(DEV)
+    note(f"rope beyond the caches interleaved={interleaved} {t}")
+    q2, k2 = mxq.mxq_rope(q, k, f, pos, interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert torch.equal(qkv.cpu(), base)
+    _check_rope(q2, q, f, pos, interleaved, "q")
+    _check_rope(k2, k, f, pos, interleaved, "k")
+    mxq.mxq_rope(q, k, f, pos, q, k, interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert torch.equal(q, q2) and torch.equal(k, k2)
+    assert torch.equal(qkv[:, (heads + kv_heads) * dim:].cpu(), base[:, (heads + kv_heads) * dim:])
