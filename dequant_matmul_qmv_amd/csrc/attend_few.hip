@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kFewThreads = 256, kFewWaves = 4;
 constexpr int kChunk = 64;      // keys a wave takes at a time
+constexpr int kLongRounds = 3;
 constexpr int kMinChunks = 4;   // at least one chunk for each wave of a workgroup
 // Tables of up to this many keys are not split: four rounds of a workgroup's
 // waves.  One sequence of 8 kv heads, split and joined / not split: 11.5 / 10.3 us
@@ -84,9 +85,14 @@ __device__ Part find_part(const AttendArgs& a, int slot, int seq) {
     total += static_cast<long long>(mine.chunks) * mine.groups * hk;
   }
   total = wave_sum(total);
-  const long long even = (total + a.target - 1) / a.target;
+  // Four workgroups a compute unit, or two where four would still have
+  // kLongRounds chunks a wave (64 sequences up to 8192 keys: 45 us with four, 48
+  // with two; 8 of 16384: 59 and 55; two of 131071: 105 and 101); parts of whole
+  // rounds of the four waves (64 sequences: 48 us with parts of 9 chunks, 45 with 12).
+  long long even = (total + a.target - 1) / a.target;
+  if (even >= kLongRounds * kFewWaves) even *= 2;
   Part p{};
-  p.step = static_cast<int>(max(even, static_cast<long long>(a.min_chunks)));
+  p.step = static_cast<int>((max(even, static_cast<long long>(a.min_chunks)) + kFewWaves - 1) / kFewWaves * kFewWaves);
   int before = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     if (a.seqs > 64) mine = share_of<MT>(a, s0 + lane);
@@ -427,9 +433,9 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_f
 
 // One workgroup for each (token, query head): the parts of its row, 4 values a
 // lane, the parts dealt over the workgroup's groups of DIM / 4 lanes.
-template <int DIM, int MT, bool BF16>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-  constexpr int kLanes = DIM / 4, kTeams = 256 / kLanes, kRows = 16 * MT;
+template <int DIM, int MT, bool BF16, int THREADS>
+__global__ __launch_bounds__(THREADS) void attend_join_kernel(AttendArgs a) {
+  constexpr int kLanes = DIM / 4, kTeams = THREADS / kLanes, kRows = 16 * MT;
   __shared__ float sums[kTeams][DIM];
   __shared__ float team_m[kTeams], team_l[kTeams];
   // one token a sequence, or up to `join_new`
@@ -505,8 +511,14 @@ hipError_t launch_mt(const AttendArgs& a, unsigned slots, bool joined) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !joined) return e;
   const dim3 grid(static_cast<unsigned>(a.seqs) * static_cast<unsigned>(a.join_new), static_cast<unsigned>(a.heads));
-  if (a.bf16) hipLaunchKernelGGL((attend_join_kernel<DIM, MT, true>), grid, dim3(256), 0, a.stream, a);
-  else hipLaunchKernelGGL((attend_join_kernel<DIM, MT, false>), grid, dim3(256), 0, a.stream, a);
+  // one wave a row where the sequences are too many to have many parts each (64 sequences: 45.4 -> 44.1 us)
+  if (8 * static_cast<int64_t>(a.seqs) * a.pool.kv_heads >= a.target) {
+    if (a.bf16) hipLaunchKernelGGL((attend_join_kernel<DIM, MT, true, 64>), grid, dim3(64), 0, a.stream, a);
+    else hipLaunchKernelGGL((attend_join_kernel<DIM, MT, false, 64>), grid, dim3(64), 0, a.stream, a);
+  } else {
+    if (a.bf16) hipLaunchKernelGGL((attend_join_kernel<DIM, MT, true, 256>), grid, dim3(256), 0, a.stream, a);
+    else hipLaunchKernelGGL((attend_join_kernel<DIM, MT, false, 256>), grid, dim3(256), 0, a.stream, a);
+  }
   return hipGetLastError();
 }
 
