@@ -16,7 +16,7 @@
 // several parts, a second kernel joins those.  Measured (a copy of 1 GiB runs at
 // 5.2 TB/s): two sequences of 131071 keys (537 MB) 100.6 us, 5.3 TB/s, 5 of them the
 // join; 64 sequences of 5 .. 8192 keys (141 MB) 43.5 us, 3.3 TB/s, where launch, the
-// search for the parts, the first loads and the join are a third; one of 777 keys 10.3 us.
+// search for the parts, the first loads and the join are a third; one of 777 keys 9.2 us.
 //
 // Both products run on the matrix cores with the codes as exact f16, straight
 // from registers.  S^T = K Q^T leaves each lane 16 keys of one query row, and
@@ -39,14 +39,15 @@ namespace mxq {
 
 namespace {
 
-constexpr int kFewThreads = 256, kFewWaves = 4;
+constexpr int kFewWaves = 4;    // of a workgroup; twice that where it takes all keys
 constexpr int kChunk = 64;      // keys a wave takes at a time
 constexpr int kLongRounds = 3;
 constexpr int kMinChunks = 4;   // at least one chunk for each wave of a workgroup
-// Tables of up to this many keys are not split: four rounds of a workgroup's
-// waves.  One sequence of 8 kv heads, split and joined / not split: 11.5 / 10.3 us
-// at 777 keys of 64 values, 11.1 / 12.8 us at 128 values; 11.1 / 9.0 us at 512 keys;
-// inside a graph, which then has no workspace to allocate, 20 / 7 .. 13 us.
+// Tables of up to this many keys are not split: a workgroup of eight waves takes
+// all keys of its rows, in two rounds at most.  One sequence of 8 kv heads, split
+// and joined / not split: 11.5 / 9.2 us at 777 keys of 64 values (10.3 with four
+// waves), 11.1 / 12.1 us at 128 values; 11.1 / 8.9 us at 512 keys; inside a graph,
+// which then has no workspace to allocate, 20 / 7 .. 13 us.
 constexpr int kLoneKeys = 1024;
 constexpr float kTiny = 1e-30f;
 
@@ -142,11 +143,11 @@ struct Pages {
 
 }  // namespace
 
-template <int DIM, int MT, bool BF16>
-__global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_few_kernel(AttendArgs a) {
+template <int DIM, int MT, bool BF16, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ? 1 : 2) void attend_few_kernel(AttendArgs a) {
   constexpr int U = DIM / 64, DB = DIM / 16, kRows = 16 * MT;
-  __shared__ float join[kFewWaves][16][DIM + 4];
-  __shared__ float join_m[kFewWaves][16], join_l[kFewWaves][16];
+  __shared__ float join[WAVES][16][DIM + 4];
+  __shared__ float join_m[WAVES][16], join_l[WAVES][16];
   const Part part = find_part<MT>(a, blockIdx.x, -1);
   if (!part.any) return;
   const int hk = a.pool.kv_heads, block = a.pool.block;
@@ -245,7 +246,7 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_f
   // one chunk: as soon as k's registers are free they take the next chunk's
   // rows, and v's do after the second product
   auto step = [&](int c, Raw<DIM>& r, Pages& ahead) {
-    const bool more_chunks = c + kFewWaves < c_end;
+    const bool more_chunks = c + WAVES < c_end;
     f4 s[MT][4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_f
         }
       }
     }
-    if (more_chunks) load_k(c + kFewWaves, ahead, r);
+    if (more_chunks) load_k(c + WAVES, ahead, r);
     const float was_vs = top_vs;
     top_vs = fmaxf(top_vs, max_xor16(max_xor32(r.vs)));
     const float share = r.vs / top_vs, shrink = was_vs / top_vs;
@@ -369,8 +370,8 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_f
       }
     }
     if (more_chunks) {
-      load_v(c + kFewWaves, ahead, r);
-      ahead = pages_of(c + 2 * kFewWaves);
+      load_v(c + WAVES, ahead, r);
+      ahead = pages_of(c + 2 * WAVES);
     }
   };
 
@@ -380,8 +381,8 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_f
     Pages ahead = pages_of(c);
     load_k(c, ahead, raw);
     load_v(c, ahead, raw);
-    ahead = pages_of(c + kFewWaves);   // past the end: -1, or a page that is not used
-    for (; c < c_end; c += kFewWaves) step(c, raw, ahead);
+    ahead = pages_of(c + WAVES);   // past the end: -1, or a page that is not used
+    for (; c < c_end; c += WAVES) step(c, raw, ahead);
   }
 
   // join the waves, 16 rows at a time
@@ -397,17 +398,17 @@ __global__ __launch_bounds__(kFewThreads, MT * DIM >= 256 ? 1 : 2) void attend_f
     for (int db = 0; db < DB; ++db)
       *reinterpret_cast<f4*>(&join[wave][rho][db * 16 + h * 4]) = acc[mt][db] * top_vs;
     __syncthreads();
-    for (int u = threadIdx.x; u < 16 * (DIM / 4); u += kFewThreads) {
+    for (int u = threadIdx.x; u < 16 * (DIM / 4); u += 64 * WAVES) {
       const int row = u / (DIM / 4), d = (u - row * (DIM / 4)) * 4, i = mt * 16 + row;
       if (i < rows) {
         float top = join_m[0][row];
 #pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) top = fmaxf(top, join_m[w][row]);
+        for (int w = 1; w < WAVES; ++w) top = fmaxf(top, join_m[w][row]);
         const float ref = top == kNegInf ? 0.0f : top;
         f4 y = f4{0, 0, 0, 0};
         float total = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
           const float e = __builtin_amdgcn_exp2f(join_m[w][row] - ref);
           y += *reinterpret_cast<const f4*>(&join[w][row][d]) * e;
           total += join_l[w][row] * e;
@@ -507,11 +508,20 @@ __global__ __launch_bounds__(THREADS) void attend_join_kernel(AttendArgs a) {
 
 namespace {
 
+template <int DIM, int MT, int WAVES>
+hipError_t launch_parts(const AttendArgs& a, unsigned slots) {
+  const dim3 grid(slots), block(64 * WAVES);
+  if (a.bf16) hipLaunchKernelGGL((attend_few_kernel<DIM, MT, true, WAVES>), grid, block, 0, a.stream, a);
+  else hipLaunchKernelGGL((attend_few_kernel<DIM, MT, false, WAVES>), grid, block, 0, a.stream, a);
+  return hipGetLastError();
+}
+
 template <int DIM, int MT>
 hipError_t launch_mt(const AttendArgs& a, unsigned slots, bool joined) {
-  if (a.bf16) hipLaunchKernelGGL((attend_few_kernel<DIM, MT, true>), dim3(slots), dim3(kFewThreads), 0, a.stream, a);
-  else hipLaunchKernelGGL((attend_few_kernel<DIM, MT, false>), dim3(slots), dim3(kFewThreads), 0, a.stream, a);
-  hipError_t e = hipGetLastError();
+  const bool lone = !joined && static_cast<int64_t>(a.width) * a.pool.block > kFewWaves * kChunk;
+  // (32 rows of 128 values do not fit the registers of that many waves)
+  constexpr int kLoneWaves = MT * DIM >= 256 ? kFewWaves : 2 * kFewWaves;
+  hipError_t e = lone ? launch_parts<DIM, MT, kLoneWaves>(a, slots) : launch_parts<DIM, MT, kFewWaves>(a, slots);
   if (e != hipSuccess || !joined) return e;
   const dim3 grid(static_cast<unsigned>(a.seqs) * static_cast<unsigned>(a.join_new), static_cast<unsigned>(a.heads));
   // one wave a row where the sequences are too many to have many parts each (64 sequences: 45.4 -> 44.1 us)
