@@ -29,16 +29,18 @@
 //           cell bounds the k-th largest token), and only cells that reach it
 //           are read again, into a list of at most 2048 tokens in LDS.  Rows
 //           whose kept tokens are more than that are left to the last two
-//   bins    many workgroups a row: counts and weights of 2048 bins by value
+//   bins    many workgroups a row: counts and weights of 2048 bins by value.  For
+//           few rows these are further workgroups of the draw kernel, which work
+//           before it is known whether they are needed
 //   wide    many workgroups a row: the bins say in which of them the prefix
 //           ends; their tokens go to a list, those before them into the kept
 //           weight of their piece.  The row's last workgroup (a fifth kernel where
 //           the rows are many) finds the end in
 //           the list and draws.  Where a bin has more tokens than a list (many
 //           equal logits) it searches the row itself
-// Measured: one row of 128256, top-k 40 and top-p, 15 us (draw 9, stats 2.7, the
-// last two 2 .. 4 to find nothing); 192 rows of mixed settings 117 us (stats 23,
-// draw 33, bins 22, wide 29, the draw after it 13); 17 rows of 32003 by min-p 21 us.
+// Measured: one row of 128256, top-k 40 and top-p, 14 us (draw 9, stats 2.7), or
+// 35 .. 37 with a prefix of thousands; 192 rows of mixed settings 118 us (stats 23,
+// draw 33, bins 22, wide 29, the draw after it 13); 17 rows of 32003 by min-p 20 us.
 // One workgroup a row for everything took 323, 528 and 40 us.
 #include <cfloat>
 
@@ -214,6 +216,7 @@ struct Shared {
     };
     uint32_t some[kDrawWaves][kPiece];  // keys of a wave's piece
   };
+  uint32_t bin_count[kBins];            // beside word, which then holds the bins' weights
   u64 wave_mass[kDrawWaves], wave_bits[kDrawWaves];
   uint32_t wave_count[kDrawWaves], red[kDrawWaves];
   double wave_sum[kDrawWaves];
@@ -405,6 +408,41 @@ __device__ __forceinline__ void draw_kept(const SampleArgs& a, Shared& sh, int r
   }
 }
 
+// Adds the tokens of part `part` of a row, from `low` up, to the row's bins.
+template <int T>
+__device__ __forceinline__ void fill_bins(const SampleArgs& a, Shared& sh, int row, const void* x, const Rule& rule, const Weigh& w,
+                                          const Bins& bins, uint32_t low, int part) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool limit_k = rule.k < a.vocab, limit_p = rule.p < 1.0f;
+  u64* mass = sh.word;
+  uint32_t* count = sh.bin_count;
+  __syncthreads();
+  for (int i = tid; i < kBins; i += kDrawThreads) {
+    mass[i] = 0;
+    count[i] = 0;
+  }
+  __syncthreads();
+  const int upto = min((part + 1) * a.span, a.vocab);
+  for (int i = part * a.span + wave * kPiece; i < upto; i += kDrawWaves * kPiece) {
+    uint32_t key[8];
+    load_keys8<T>(x, i + lane * 8, a.vocab, key);
+    // those that can be kept, side by side
+    const int held = compact(key, sh.some[wave], [&](uint32_t k) { return k >= low; });
+    for (int j = lane; j < held; j += 64) {
+      const uint32_t k = sh.some[wave][j];
+      const int b = bins.of(k);
+      if (limit_k) atomicAdd(&count[b], 1u);
+      if (limit_p) atomicAdd(&mass[b], w.fixed(k));
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  for (int i = tid; i < kBins; i += kDrawThreads) {
+    if (mass[i] != 0) atomicAdd(&a.bin_mass[static_cast<int64_t>(row) * kBins + i], mass[i]);
+    if (count[i] != 0) atomicAdd(&a.bin_count[static_cast<int64_t>(row) * kBins + i], count[i]);
+  }
+}
+
 // Where the prefix ends, by the bins: the one in which the top_k end, and what
 // is before it (kBins: all that is there); top_p of their weight, between that
 // without and with this bin, ends in the bins from `first` to `last`.
@@ -570,6 +608,11 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleArgs a) {
   const int row = blockIdx.y, lane = threadIdx.x & 63, n = a.vocab;
   const int first = blockIdx.x * kStatTokens + threadIdx.x * 8;
   const void* x = row_of(a, row, T == kF32In ? 4 : 2);
+  if (a.ahead)
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < kBins; i += gridDim.x * 256) {
+      a.bin_mass[static_cast<int64_t>(row) * kBins + i] = 0;
+      a.bin_count[static_cast<int64_t>(row) * kBins + i] = 0;
+    }
   uint32_t key[8];
   load_keys8<T>(x, first, n, key);
   uint32_t top = key[0];
@@ -590,6 +633,9 @@ __global__ __launch_bounds__(256) void sample_stats_kernel(SampleArgs a) {
   if (lane == 0 && first < n) a.pieces[static_cast<int64_t>(row) * a.piece_count + first / kPiece] = sum;
 }
 
+// Where the grid has a second dimension, all but its first workgroups fill the
+// row's bins meanwhile: idle compute units' work, which saves a launch (one row:
+// 16.0 us with the launch, 13.6 without; a prefix of thousands: 41.7 and 36.5).
 template <int T>
 __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a) {
   __shared__ Shared sh;
@@ -598,6 +644,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   const uint32_t* cells = a.cells + static_cast<int64_t>(row) * a.cell_count;
   const double* pieces = a.pieces + static_cast<int64_t>(row) * a.piece_count;
   const Rule rule = rule_of(a, row);
+  if (blockIdx.y != 0 && (rule.one || rule.open)) return;
 
   // this thread's cells: the first two in registers
   constexpr int kHeld = 2;
@@ -615,7 +662,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   if (tid == 0) {
     sh.found = 0x7FFFFFFF;
     sh.hits = sh.listed = 0;
-    if (a.plans) a.plans[row].state = kDone;
+    if (a.plans && blockIdx.y == 0) a.plans[row].state = kDone;
   }
   top = block_max(sh, top);
   const Weigh w = weigher(top, rule.one ? 1.0f : rule.t);
@@ -733,6 +780,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   // tokens of less than (1 - p) / n of the total: all of them together are less than what top_p leaves out
   if (guessed && finite) low = max(low, key_below(log(static_cast<double>(n) / ((1.0 - static_cast<double>(rule.p)) * total))));
   const uint32_t start = low;
+  const bool binned = finite && (limit_k || limit_p);
   const int guess = limit_k ? rule.k : guessed ? min(kGuess, a.cell_count / 2) : 0;
   if (finite && n > kList && guess > 0 && guess <= a.cell_count && guess <= kList) {
     // the guess-th largest cell, to within a bin: at least that many tokens reach its smallest member
@@ -762,6 +810,11 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   uint32_t bound = guessed ? start : low;
   // top_p of the top_k needs the weight of all of those, also below min_p
   if (floor && finite && !(limit_k && limit_p)) bound = low = max(low, key_below(-log(static_cast<double>(rule.min_p))));
+
+  if (blockIdx.y != 0) {
+    if (binned) fill_bins<T>(a, sh, row, x, rule, w, bins, bound, blockIdx.y - 1);
+    return;
+  }
 
   // the list: tokens of `low` and up, from cells that reach it, in no order
   // (more than kList tokens may be kept: not tried)
@@ -894,13 +947,14 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   }
   if (!small) {
     if (tid == 0) {
-      const int state = !finite ? kSearch : limit_k || limit_p ? kBinned : kSums;
+      const int state = binned ? kBinned : finite && !limit_k && !limit_p ? kSums : kSearch;
       a.plans[row] = SamplePlan{state, top, bound, bins.scale, 0, 0, total * kFix};
     }
-    for (int i = tid; i < kBins; i += kDrawThreads) {
-      a.bin_mass[static_cast<int64_t>(row) * kBins + i] = 0;
-      a.bin_count[static_cast<int64_t>(row) * kBins + i] = 0;
-    }
+    if (!a.ahead)
+      for (int i = tid; i < kBins; i += kDrawThreads) {
+        a.bin_mass[static_cast<int64_t>(row) * kBins + i] = 0;
+        a.bin_count[static_cast<int64_t>(row) * kBins + i] = 0;
+      }
     return;
   }
   __syncthreads();
@@ -910,41 +964,13 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
 
 template <int T>
 __global__ __launch_bounds__(kDrawThreads) void sample_bins_kernel(SampleArgs a) {
-  __shared__ u64 mass[kBins];
-  __shared__ uint32_t count[kBins];
-  __shared__ uint32_t some[kDrawWaves][kPiece];
-  const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ Shared sh;
+  const int row = blockIdx.y;
   const SamplePlan plan = a.plans[row];
   if (plan.state != kBinned) return;
-  const void* x = row_of(a, row, T == kF32In ? 4 : 2);
   const Rule rule = rule_of(a, row);
-  const Weigh w = weigher(plan.top, rule.t);
-  const Bins bins{value_of(plan.top), plan.scale};
-  const bool limit_k = rule.k < a.vocab, limit_p = rule.p < 1.0f;
-  for (int i = tid; i < kBins; i += kDrawThreads) {
-    mass[i] = 0;
-    count[i] = 0;
-  }
-  __syncthreads();
-  const int upto = min((static_cast<int>(blockIdx.x) + 1) * a.span, a.vocab);
-  for (int i = blockIdx.x * a.span + wave * kPiece; i < upto; i += kDrawWaves * kPiece) {
-    uint32_t key[8];
-    load_keys8<T>(x, i + lane * 8, a.vocab, key);
-    // those that can be kept, side by side
-    const int held = compact(key, some[wave], [&](uint32_t k) { return k >= plan.low; });
-    for (int j = lane; j < held; j += 64) {
-      const uint32_t k = some[wave][j];
-      const int b = bins.of(k);
-      if (limit_k) atomicAdd(&count[b], 1u);
-      if (limit_p) atomicAdd(&mass[b], w.fixed(k));
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
-  __syncthreads();
-  for (int i = tid; i < kBins; i += kDrawThreads) {
-    if (mass[i] != 0) atomicAdd(&a.bin_mass[static_cast<int64_t>(row) * kBins + i], mass[i]);
-    if (count[i] != 0) atomicAdd(&a.bin_count[static_cast<int64_t>(row) * kBins + i], count[i]);
-  }
+  fill_bins<T>(a, sh, row, row_of(a, row, T == kF32In ? 4 : 2), rule, weigher(plan.top, rule.t), Bins{value_of(plan.top), plan.scale},
+               plan.low, blockIdx.x);
 }
 
 // JOINED: the row's last workgroup draws.  Without that the kernel needs few
@@ -1076,30 +1102,35 @@ hipError_t launch_sample_type(const SampleArgs& a, int64_t most_rows, bool wide,
     if (b.min_p) b.min_p += r0;
     b.tokens += r0;
     b.probs += r0;
-    const unsigned parts = static_cast<unsigned>((a.vocab + kStatTokens - 1) / kStatTokens);
-    hipLaunchKernelGGL(sample_stats_kernel<T>, dim3(parts, static_cast<unsigned>(rows)), dim3(256), 0, a.stream, b);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(sample_draw_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kDrawThreads), 0, a.stream, b);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (!wide) continue;
     // a row in as many parts as give each compute unit eight workgroups, of 8 tokens a thread at least
     int64_t spans = 8 * num_cu / rows;
     if (spans < 1) spans = 1;
     const int64_t least = kDrawThreads * 8, each = ((a.vocab + spans - 1) / spans + least - 1) / least * least;
     b.span = static_cast<int>(each);
     const dim3 grid(static_cast<unsigned>((a.vocab + each - 1) / each), static_cast<unsigned>(rows));
+    // a last workgroup has to wait for its caches' write-back: less than a launch for few of them, more for many
+    const bool joined = static_cast<int64_t>(grid.x) * rows <= num_cu;
+    b.ahead = wide && joined;
+    const unsigned parts = static_cast<unsigned>((a.vocab + kStatTokens - 1) / kStatTokens);
+    hipLaunchKernelGGL(sample_stats_kernel<T>, dim3(parts, static_cast<unsigned>(rows)), dim3(256), 0, a.stream, b);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sample_draw_kernel<T>, dim3(static_cast<unsigned>(rows), b.ahead ? 1 + grid.x : 1), dim3(kDrawThreads), 0, a.stream, b);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (!wide) continue;
+    if (joined) {
+      hipLaunchKernelGGL((sample_wide_kernel<T, true>), grid, dim3(kDrawThreads), 0, a.stream, b);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      continue;
+    }
     hipLaunchKernelGGL(sample_bins_kernel<T>, grid, dim3(kDrawThreads), 0, a.stream, b);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // a last workgroup has to wait for its caches' write-back: less than a launch for few of them, more for many
-    const bool joined = static_cast<int64_t>(grid.x) * rows <= num_cu;
-    if (joined) hipLaunchKernelGGL((sample_wide_kernel<T, true>), grid, dim3(kDrawThreads), 0, a.stream, b);
-    else hipLaunchKernelGGL((sample_wide_kernel<T, false>), grid, dim3(kDrawThreads), 0, a.stream, b);
+    hipLaunchKernelGGL((sample_wide_kernel<T, false>), grid, dim3(kDrawThreads), 0, a.stream, b);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (joined) continue;
     hipLaunchKernelGGL(sample_finish_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(kDrawThreads), 0, a.stream, b);
     e = hipGetLastError();
     if (e != hipSuccess) return e;

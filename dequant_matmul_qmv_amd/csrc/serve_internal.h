@@ -163,6 +163,7 @@ struct SampleArgs {
   unsigned long long* list;      // tokens of the bins in which the prefix ends [rows, 2048]
   unsigned long long* kept;      // kept weight of each piece but for the list's [rows, piece_count]
   int span;            // tokens of a workgroup, a multiple of 8192
+  bool ahead;          // bins are filled beside the draw
 };
 hipError_t launch_sample(const SampleArgs& a, const DeviceInfo& dev);
 
