@@ -425,15 +425,15 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   }
 }
 
-// Joins a row's parts where the key axis was split: one workgroup for each
-// (token, query head), 4 values a lane, the parts dealt over its groups of
-// DIM / 4 lanes.
+// Joins a row's parts where the key axis was split: a workgroup for each token
+// and as many query heads as it has groups of DIM / 4 lanes, one of them a group.
+// Eight parts are read at a time (24 parts of 51 tokens over 6204 keys, the
+// whole call: 33 us one by one; two parts of 1281 tokens of 16 heads: 16 us with
+// a workgroup a row).
 template <int DIM, bool BF16>
-__global__ __launch_bounds__(128) void attend_many_join_kernel(AttendArgs a) {
-  constexpr int kLanes = DIM / 4, kTeams = 128 / kLanes;
-  __shared__ float sums[kTeams][DIM];
-  __shared__ float team_m[kTeams], team_l[kTeams];
-  const int tok = blockIdx.x, hq = blockIdx.y, hk = a.pool.kv_heads, head = hq / a.group;
+__global__ __launch_bounds__(256) void attend_many_join_kernel(AttendArgs a) {
+  constexpr int kLanes = DIM / 4, kTeams = 256 / kLanes;
+  const int tok = blockIdx.x, hk = a.pool.kv_heads;
   int lo = 0, hi = a.seqs;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -443,51 +443,31 @@ __global__ __launch_bounds__(128) void attend_many_join_kernel(AttendArgs a) {
   const SeqSpan sp = seq_span(a, seq);
   if (tok < sp.t0 || tok >= sp.t0 + sp.n || static_cast<int64_t>(sp.n) * a.group <= a.few_rows) return;
   find_tile(a, -1, seq, first);
-  const int i = (tok - sp.t0) * a.group + hq - head * a.group;
+  const int team = threadIdx.x / kLanes, d = (threadIdx.x - team * kLanes) * 4, hq = blockIdx.y * kTeams + team;
+  if (hq >= a.heads) return;
+  const int head = hq / a.group, i = (tok - sp.t0) * a.group + hq - head * a.group;
   const int64_t tile = first + i / kManyRows;
-  const int team = threadIdx.x / kLanes, d = (threadIdx.x - team * kLanes) * 4;
   float top = kNegInf, total = 0.0f;
   f4 y = f4{0, 0, 0, 0};
-  // four parts of a team at a time, so that their loads run together (24 parts of
-  // 51 tokens over 6204 keys: 33 us one by one)
-  for (int s0 = team; s0 < a.many_splits; s0 += 4 * kTeams) {
-    float2 ml[4];
-    f4 v[4];
+  for (int s0 = 0; s0 < a.many_splits; s0 += 8) {
+    float2 ml[8];
+    f4 v[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int s = min(s0 + e * kTeams, a.many_splits - 1);
+    for (int e = 0; e < 8; ++e) {
+      const int s = min(s0 + e, a.many_splits - 1);
       const int64_t at = min((tile * a.many_splits + s) * hk + head, static_cast<int64_t>(a.many_units) - 1) * kManyRows + i % kManyRows;
       ml[e] = *reinterpret_cast<const float2*>(a.many_ml + at * 2);
       v[e] = *reinterpret_cast<const f4*>(a.many_part + at * DIM + d);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (s0 + e * kTeams >= a.many_splits) continue;
+    for (int e = 0; e < 8; ++e) {
+      if (s0 + e >= a.many_splits) continue;
       const float now = fmaxf(top, ml[e].x), ref = now == kNegInf ? 0.0f : now;
       const float e0 = __builtin_amdgcn_exp2f(top - ref), e1 = __builtin_amdgcn_exp2f(ml[e].x - ref);
       y = y * e0 + v[e] * e1;
       total = total * e0 + ml[e].y * e1;
       top = now;
     }
-  }
-  *reinterpret_cast<f4*>(&sums[team][d]) = y;
-  if (d == 0) {
-    team_m[team] = top;
-    team_l[team] = total;
-  }
-  __syncthreads();
-  if (threadIdx.x >= kLanes) return;
-  top = team_m[0];
-#pragma unroll
-  for (int t = 1; t < kTeams; ++t) top = fmaxf(top, team_m[t]);
-  const float ref = top == kNegInf ? 0.0f : top;
-  y = f4{0, 0, 0, 0};
-  total = 0.0f;
-#pragma unroll
-  for (int t = 0; t < kTeams; ++t) {
-    const float e = __builtin_amdgcn_exp2f(team_m[t] - ref);
-    y += *reinterpret_cast<const f4*>(&sums[t][d]) * e;
-    total += team_l[t] * e;
   }
   const int64_t at = static_cast<int64_t>(tok) * a.heads + hq;
   const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
@@ -510,8 +490,9 @@ hipError_t launch_many_of(const AttendArgs& a, unsigned grid) {
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(kManyThreads), lds, a.stream, a);
   hipError_t le = hipGetLastError();
   if (le != hipSuccess || a.many_splits == 1) return le;
-  hipLaunchKernelGGL((attend_many_join_kernel<DIM, BF16>), dim3(static_cast<unsigned>(a.tokens), static_cast<unsigned>(a.heads)),
-                     dim3(128), 0, a.stream, a);
+  constexpr int kHeads = 256 / (DIM / 4);
+  hipLaunchKernelGGL((attend_many_join_kernel<DIM, BF16>), dim3(static_cast<unsigned>(a.tokens), static_cast<unsigned>((a.heads + kHeads - 1) / kHeads)),
+                     dim3(256), 0, a.stream, a);
   return hipGetLastError();
 }
 
