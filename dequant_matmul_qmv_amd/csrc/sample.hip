@@ -56,7 +56,7 @@ constexpr int kDrawThreads = 1024, kDrawWaves = 16;
 constexpr int kCell = 64, kPiece = 512, kStatTokens = 2048;  // tokens of a cell, a piece, a stats workgroup
 constexpr int kList = 2048, kShort = 256, kBins = 2048, kMaxPieces = 2048;
 constexpr int kGuess = 192;      // cells that a list for top_p alone is taken from
-constexpr int kMostRows = 1024;  // rows of one launch: 70 KB of workspace each
+constexpr int kMostRows = 1024;  // rows of one launch: 52 KB of workspace each at 128256 logits
 constexpr double kFix = 8796093022208.0;  // 2^43
 constexpr float kDeepest = 30.6f;         // 44 ln 2: a token this many temperatures below the largest has no weight
 

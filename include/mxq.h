@@ -386,7 +386,9 @@ typedef struct mxq_sampling {
  * order of summation and is the same from run to run.
  *   logits  f16|bf16|f32, row r at r * row_stride, 1 <= vocab <= 2^20
  *   u       f32 [rows];  tokens i32 [rows];  probs f32 [rows]
- * `settings` is a host structure, read during the call.
+ * `settings` is a host structure, read during the call.  Rows use the split
+ * workspace (see above), about 52 KB each at 128256 logits and at most 1024 of
+ * them at a time; MXQ_ERR_HIP if that cannot be had.
  */
 mxq_status mxq_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab, mxq_dtype dtype,
                       const float* u, const mxq_sampling* settings, int32_t* tokens, float* probs, void* stream);
