@@ -67,7 +67,7 @@ __device__ __forceinline__ Share share_of(const AttendArgs& a, int s) {
   const int hi = min(max(q.len, 0), a.width * a.pool.block);
   const int lo = a.window > 0 ? max(0, q.len - q.n - a.window + 1) : 0;
   r.c0 = lo / kChunk;
-  r.chunks = max(0, (hi + kChunk - 1) / kChunk - r.c0);
+  r.chunks = max(0, hi / kChunk + (hi % kChunk != 0) - r.c0);  // (hi may be near 2^31)
   return r;
 }
 
@@ -207,9 +207,11 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
 
   auto pages_of = [&](int c) {
     Pages p;
-    const int jk = (c * kChunk + kgroup * 16) / block, jv = (c * kChunk + h * 16) / block;
-    p.k = jk < a.width ? table[jk] : -1;
-    p.v = jv < a.width ? table[jv] : -1;
+    // (a chunk past the end may lie past 2^31)
+    const uint32_t key = static_cast<uint32_t>(c) * kChunk, width = a.width;
+    const uint32_t jk = (key + kgroup * 16) / block, jv = (key + h * 16) / block;
+    p.k = jk < width ? table[jk] : -1;
+    p.v = jv < width ? table[jv] : -1;
     return p;
   };
   auto load_k = [&](int c, Pages p, Raw<DIM>& r) {
@@ -267,7 +269,7 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
     const float was_vs = top_vs;
     top_vs = fmaxf(top_vs, max_xor16(max_xor32(r.vs)));
     const float share = r.vs / top_vs, shrink = was_vs / top_vs;
-    const bool whole = __all(r.ok) && c * kChunk >= all_from && (c + 1) * kChunk <= all_upto;
+    const bool whole = __all(r.ok) && c * kChunk >= all_from && c * kChunk <= all_upto - kChunk;
     const int key0 = c * kChunk + h * 16;
     bool low = false;
     float ref[MT];

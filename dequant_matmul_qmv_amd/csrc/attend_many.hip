@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   const int tile_last = min(row0 + kManyRows, rows) - 1;
   const int key_hi = min(pos0 + tile_last / a.group + 1, limit);
   const int key_lo = a.window > 0 ? max(0, pos0 + row0 / a.group - a.window + 1) : 0;
-  const int s_lo = key_lo / kStage, s_hi = max(s_lo, (key_hi + kStage - 1) / kStage);
+  const int s_lo = key_lo / kStage, s_hi = max(s_lo, key_hi / kStage + (key_hi % kStage > 0));
   const int per = (s_hi - s_lo + a.many_splits - 1) / a.many_splits;
   const int begin = min(s_lo + part * per, s_hi), end = min(begin + per, s_hi);
 
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
       log_top_vs = __builtin_amdgcn_logf(largest);
     }
     const bool there = __all(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])) >= 0.0f);
-    const bool masked = !(there && s * kStage >= all_from && (s + 1) * kStage <= all_upto);
+    const bool masked = !(there && s * kStage >= all_from && s * kStage <= all_upto - kStage);
     if (masked) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
         fetch(s + 1);
         pages(min(s + 2, end - 1));
       }
-      if (s * kStage < wave_upto && (s + 1) * kStage > wave_from) compute(s, at);
+      if (s * kStage < wave_upto && s * kStage > wave_from - kStage) compute(s, at);
       if (next) put(stage[at ^ 1]);
       __syncthreads();
     }

@@ -1,0 +1,66 @@
+"""The serving operators at the ends of their ranges: lengths near 2^31, windows, scales and scores far apart, launches
+past a grid's limit, values and settings at their borders.  References and bounds as in the operators' own tests."""
+
+import numpy as np
+import pytest
+import torch
+
+import dequant_matmul_qmv_amd as mxq
+from tests.gpu_util import note
+from tests.serve_util import HALF, append_ref, attention_ref, random_pool
+from tests.test_serve_attention import _check
+
+DEV = "cuda:0"
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _attend(q, pool, tab, lens, new, **kw):
+    """(out, lse) of a call on the pool's copy on the GPU."""
+    cache = mxq.KvCache(*[x.to(DEV) for x in pool])
+    starts = None if all(n == 1 for n in new) else _i32(np.cumsum([0] + new).tolist())
+    out, lse = mxq.mxq_attention(q.to(DEV), cache, tab.to(DEV), _i32(lens), starts, return_lse=True, **kw)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+# ------------------------------------------------------------------------------------------- long sequences
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 5, 90])
+@pytest.mark.parametrize("dim,block", [(64, 128), (128, 16)])
+def test_attention_of_the_longest_sequence(dim, block, new):
+    """A sequence of nearly 2^31 tokens (a table as wide as is allowed, its early pages all one): the last 1000 keys
+    are those of a short sequence that ends in the same pages."""
+    gen = torch.Generator().manual_seed(block)
+    width, last = (2 ** 31 - 1) // block, 1500 // block
+    pool = random_pool(last + 1, 1, block, dim, gen)
+    tab = torch.zeros(1, width, dtype=torch.int32)
+    tab[0, -last:] = 1 + torch.arange(last, dtype=torch.int32)
+    q = torch.randn(new, 3, dim, generator=gen).half()
+    for cut in (0, 3):
+        length = width * block - cut
+        ref = attention_ref(q, pool, tab[:, -last:], [last * block - cut], [new], 1000, dim ** -0.5)
+        note(f"attention, {new} new of {length} tokens, dim {dim}")
+        out, lse = _attend(q, pool, tab, [length], [new], window=1000)
+        _check(out, lse, ref, f"longest {length}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 70])
+def test_append_to_the_longest_sequence(new):
+    gen = torch.Generator().manual_seed(17)
+    block, dim = 64, 64
+    width, last = (2 ** 31 - 1) // block, 3
+    pool = random_pool(last + 1, 2, block, dim, gen)
+    tab = torch.zeros(1, width, dtype=torch.int32)
+    tab[0, -last:] = 1 + torch.arange(last, dtype=torch.int32)
+    k, v = (torch.randn(new, 2, dim, generator=gen).half() for _ in range(2))
+    want = append_ref(pool, k, v, tab[:, -last:], [last * block - 5], [new], block)
+    cache = mxq.KvCache(*[x.to(DEV) for x in pool])
+    note(f"append of {new} at {width * block - 5}")
+    mxq.mxq_kv_append(cache, k.to(DEV), v.to(DEV), tab.to(DEV), _i32([width * block - 5]), None if new == 1 else _i32([0, new]))
+    torch.cuda.synchronize()
+    for got, w in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), want):
+        assert np.array_equal(got.cpu().numpy(), w)
