@@ -48,6 +48,23 @@ constexpr float kLift = 14.0f;
 constexpr float kF16Normal = 6.103515625e-05f;  // 2^-14, f16's smallest normal value
 constexpr float kLowLift = 16777216.0f;         // 2^24
 constexpr float kUnlift = 1.0f / 16384.0f;
+
+// Weights below f16's normal range go through products of their own, a band of
+// 2^24 at a time, each lifted into that range.  The fifth band ends at 2^-134
+// (an f32 weight times its page's share of the largest v scale can be smaller):
+// what is below, 2^-148 of the row's largest weight times the largest v scale,
+// is dropped, since a sixth lift would be past f32's range.
+struct Band {
+  float ceiling = kF16Normal, floor = kF16Normal / kLowLift, lift = kLowLift;
+  __device__ __forceinline__ float lifted(float p) const { return p < ceiling && p >= floor ? p * lift : 0.0f; }
+  __device__ __forceinline__ bool below(float p) const { return p > 0.0f && p < floor; }
+  __device__ __forceinline__ bool last() const { return lift >= 0x1p120f; }
+  __device__ __forceinline__ void next() {
+    ceiling = floor;
+    floor *= 1.0f / kLowLift;
+    lift *= kLowLift;
+  }
+};
 constexpr float kLn2 = 0.69314718055994530942f;
 // Natural log-sum of weights held as 2^kLift times 2^(x - ref).
 __device__ __forceinline__ float log_sum(float ref, float total) { return (ref + log2f(total * kUnlift)) * kLn2; }

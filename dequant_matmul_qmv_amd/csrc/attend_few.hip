@@ -337,27 +337,24 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
         acc[mt][db] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, as_h8(pf[mt][1]), acc[mt][db], 0, 0, 0);
       }
     }
-    // values below f16's normal range: products of their own, 2^24, 2^48, ..
-    // times larger, until none is left (an f32 weight ends at 2^-126)
-    float floor = kF16Normal, lift = kLowLift;
-    for (bool more = any_low; more; floor *= 1.0f / kLowLift, lift *= kLowLift) {
+    // values below f16's normal range: products of their own, until none is left
+    Band band;
+    for (bool more = any_low; more; band.next()) {
       bool left = false;
-      const float next = floor * (1.0f / kLowLift);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           const float p0 = s[mt][i >> 2][i & 3], p1 = s[mt][i >> 2][(i & 3) + 1];
-          left |= (p0 > 0.0f && p0 < next) || (p1 > 0.0f && p1 < next);
-          const h2 pk = {static_cast<_Float16>(p0 < floor && p0 >= next ? p0 * lift : 0.0f),
-                         static_cast<_Float16>(p1 < floor && p1 >= next ? p1 * lift : 0.0f)};
+          left |= band.below(p0) || band.below(p1);
+          const h2 pk = {static_cast<_Float16>(band.lifted(p0)), static_cast<_Float16>(band.lifted(p1))};
           w[i / 2] = as_u32(pk);
         }
         pf[mt][0] = u4{w[0], w[1], w[2], w[3]};
         pf[mt][1] = u4{w[4], w[5], w[6], w[7]};
       }
-      more = __any(left);
+      more = __any(left && !band.last());
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
         const u4 w = anew(r.v[db]);
@@ -367,7 +364,7 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
           f4 t = f4{0, 0, 0, 0};
           t = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, as_h8(pf[mt][0]), t, 0, 0, 0);
           t = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, as_h8(pf[mt][1]), t, 0, 0, 0);
-          acc[mt][db] += t * (1.0f / lift);
+          acc[mt][db] += t * (1.0f / band.lift);
         }
       }
     }

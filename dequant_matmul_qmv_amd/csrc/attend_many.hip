@@ -346,10 +346,9 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
     }
     if (!rare) return;
     // the weights of [2^-38, 2^-14), then those 2^24 times smaller, .., until none is left
-    float ceiling = kF16Normal, times = kLowLift;
+    Band band;
 #pragma clang loop unroll(disable)
-    for (bool more = true; more; ceiling *= 1.0f / kLowLift, times *= kLowLift) {
-      const float floor = ceiling * (1.0f / kLowLift);
+    for (bool more = true; more; band.next()) {
       bool left = false;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -357,9 +356,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const float p0 = x[g >> 1][(g & 1) * 8 + i], p1 = x[g >> 1][(g & 1) * 8 + i + 1];
-          left |= (p0 > 0.0f && p0 < floor) || (p1 > 0.0f && p1 < floor);
-          const h2 pk2 = {static_cast<_Float16>(p0 < ceiling && p0 >= floor ? p0 * times : 0.0f),
-                          static_cast<_Float16>(p1 < ceiling && p1 >= floor ? p1 * times : 0.0f)};
+          left |= band.below(p0) || band.below(p1);
+          const h2 pk2 = {static_cast<_Float16>(band.lifted(p0)), static_cast<_Float16>(band.lifted(p1))};
           w[i / 2] = as_u32(pk2);
         }
         const h8 pf = as_h8(u4{w[0], w[1], w[2], w[3]});
@@ -369,11 +367,11 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
 #pragma unroll
           for (int i = 0; i < 16; ++i) t[i] = 0.0f;
           t = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(again(v_piece(db, g))), pf, t, 0, 0, 0);
-          acc[db] += t * (1.0f / times);
+          acc[db] += t * (1.0f / band.lift);
           __builtin_amdgcn_sched_barrier(0);  // one product's registers at a time
         }
       }
-      more = __any(left);
+      more = __any(left && !band.last());
     }
   };
 

@@ -64,3 +64,42 @@ def test_append_to_the_longest_sequence(new):
     torch.cuda.synchronize()
     for got, w in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), want):
         assert np.array_equal(got.cpu().numpy(), w)
+
+
+# --------------------------------------------------------------------------------- small weights, small v scales
+def _spread_pool(lens, heads, dim, block, gen, fall, v_bits):
+    """(pool, table, q): scores that fall up to `fall` below a row's largest in small steps, pages whose v scales lie up
+    to 2^v_bits apart, one of them below f32's normal range.  A key holds one code throughout, a query one value, so that
+    the scores are exact but for their scaling."""
+    counts = [-(-n // block) for n in lens]
+    blocks = sum(counts)
+    k, v, ks, vs = random_pool(blocks, heads, block, dim, gen)
+    codes = torch.randint(-127, 128, (blocks, heads, block, 1), generator=gen, dtype=torch.int32)
+    codes[:, :, 0] = 127                                       # every page holds a key of the largest score
+    k = codes.to(torch.int8).expand(-1, -1, -1, dim).contiguous()
+    ks[:] = fall / 254 / dim ** 0.5                            # score = dim^-0.5 * dim * ks * code
+    vs = vs * 2.0 ** -torch.randint(0, v_bits + 1, vs.shape, generator=gen)
+    tab = torch.full((len(lens), max(counts)), -1, dtype=torch.int32)
+    ids, at = torch.randperm(blocks, generator=gen).int(), 0
+    for s, c in enumerate(counts):
+        tab[s, :c] = ids[at:at + c]
+        at += c
+    vs[int(tab[0, counts[0] // 2])] = 1e-39
+    return (k, v, ks, vs), tab
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 7, 150])
+def test_small_weights_in_pages_of_small_scales(new, dim, t):
+    """A weight times its page's share of the largest v scale passes below every f32 number."""
+    gen = torch.Generator().manual_seed(dim + new)
+    lens, block = [301, 1210], 16
+    for fall, v_bits in ((110.0, 40), (95.0, 12), (60.0, 70)):
+        pool, tab = _spread_pool(lens, 2, dim, block, gen, fall, v_bits)
+        q = torch.ones(2 * new, 4, dim).to(HALF[t])
+        ref = attention_ref(q, pool, tab, lens, [new, new], 0, dim ** -0.5)
+        note(f"attention fall {fall} v scales 2^-{v_bits} {new} new, dim {dim} {t}")
+        out, lse = _attend(q, pool, tab, lens, [new, new])
+        _check(out, lse, ref, f"fall {fall} {v_bits}")
