@@ -311,7 +311,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      float p[8], sum = 0.0f, weigh = top_vs * st.inv_vs[g];
+      // (finite: a group that is masked throughout has the sum 0, whatever its page's scale is)
+      float p[8], sum = 0.0f, weigh = fminf(top_vs * st.inv_vs[g], FLT_MAX);
       if (rare) {
         off[g] = lift;
         weigh = 1.0f;

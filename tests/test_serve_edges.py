@@ -103,3 +103,22 @@ def test_small_weights_in_pages_of_small_scales(new, dim, t):
         note(f"attention fall {fall} v scales 2^-{v_bits} {new} new, dim {dim} {t}")
         out, lse = _attend(q, pool, tab, lens, [new, new])
         _check(out, lse, ref, f"fall {fall} {v_bits}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 6, 150])
+def test_masked_pages_of_tiny_scales(new, dim):
+    """Pages whose v scales' quotient is past f32's range, the small one's keys masked for the rows beside the large one."""
+    gen = torch.Generator().manual_seed(3 * dim + new)
+    block, length = 16, 150
+    pool = random_pool(10, 1, block, dim, gen)
+    pool[3][::3] *= 6000.0                         # up to 180
+    pool[3][2::3] = 2.0 ** -126 * 1.5
+    tab = torch.arange(10, dtype=torch.int32)[None]
+    q = torch.randn(new, 8, dim, generator=gen).half() * 0.2
+    for window in (0, 20):
+        ref = attention_ref(q, pool, tab, [length], [new], window, dim ** -0.5)
+        note(f"attention tiny v scales, {new} new, dim {dim}, window {window}")
+        out, lse = _attend(q, pool, tab, [length], [new], window=window)
+        _check(out, lse, ref, f"tiny scales {window}")
