@@ -32,8 +32,8 @@ struct Touched {
 __device__ __forceinline__ void new_tokens(const KvAppendArgs& a, int s, int& t0, int& n, int& first) {
   t0 = min(max(a.starts[s], 0), a.tokens);
   n = min(max(a.starts[s + 1], t0), a.tokens) - t0;
-  const int len = min(max(a.lens[s], 0), a.width * a.pool.block);
-  const int over = a.lens[s] - len;  // tokens past the table's last block are dropped
+  const int all = max(a.lens[s], 0), len = min(all, a.width * a.pool.block);
+  const int over = all - len;        // tokens past the table's last block are dropped
   first = len + over - n;
   if (over > 0) n = max(0, n - over);
   if (first < 0) {                   // more new tokens than the length: the first of them have no place
@@ -134,7 +134,7 @@ __device__ __forceinline__ void quant8(u4 v, float inv, int (&q)[8]) {
 template <bool BF16>
 __global__ __launch_bounds__(64) void kv_append_one_kernel(KvAppendArgs a) {
   const int seq = blockIdx.x, head = blockIdx.y, lane = threadIdx.x, dim = a.pool.dim, b = a.pool.block;
-  const int pos = a.lens[seq] - 1;
+  const int pos = max(a.lens[seq], 0) - 1;
   if (pos < 0 || pos >= a.width * b) return;
   const int j = pos / b, slot = pos - j * b, c = lane & 15;
   const int page = a.table[static_cast<int64_t>(seq) * a.table_stride + j];

@@ -305,7 +305,7 @@ typedef struct mxq_kv_cache {
 /*
  * mxq_kv_append -- quantize new keys and values into the cache.
  *
- * Sequence s has lens[s] tokens with its new ones, which are its last; its new
+ * Sequence s has lens[s] tokens (below 0: none) with its new ones, which are its last; its new
  * rows of k and v are starts[s] .. starts[s + 1] (starts: i32 [seqs + 1], from
  * 0 to `tokens`, not descending), or row s alone where starts is null (then
  * tokens == seqs).  For each page that gets new tokens, and each head:

@@ -122,3 +122,25 @@ def test_masked_pages_of_tiny_scales(new, dim):
         note(f"attention tiny v scales, {new} new, dim {dim}, window {window}")
         out, lse = _attend(q, pool, tab, [length], [new], window=window)
         _check(out, lse, ref, f"tiny scales {window}")
+
+
+# ------------------------------------------------------------------------------------- windows, odd lengths
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [-1, -70, -2 ** 31])
+def test_negative_lengths_are_empty(length):
+    gen = torch.Generator().manual_seed(19)
+    pool = random_pool(4, 1, 16, 64, gen)
+    tab = torch.arange(4, dtype=torch.int32)[None]
+    for new in (1, 6, 100):
+        q = torch.randn(new, 2, 64, generator=gen).half()
+        for window in (0, 5):
+            note(f"attention of a length {length}, {new} new, window {window}")
+            out, lse = _attend(q, pool, tab, [length], [new], window=window)
+            assert int(torch.count_nonzero(out)) == 0 and bool(torch.isneginf(lse).all())
+        cache = mxq.KvCache(*[x.to(DEV) for x in pool])
+        kv = torch.randn(new, 1, 64, generator=gen).half().to(DEV)
+        note(f"append to a length {length}, {new} new")
+        mxq.mxq_kv_append(cache, kv, kv, tab.to(DEV), _i32([length]), None if new == 1 else _i32([0, new]))
+        torch.cuda.synchronize()
+        for got, was in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), pool):
+            assert torch.equal(got.cpu(), was)
