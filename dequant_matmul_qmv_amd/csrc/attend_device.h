@@ -116,8 +116,12 @@ __device__ __forceinline__ SeqSpan seq_span(const AttendArgs& a, int s) {
     r.t0 = min(max(a.starts[s], 0), a.tokens);
     r.n = min(max(a.starts[s + 1], r.t0), a.tokens) - r.t0;
   }
-  r.len = a.lens[s];
+  r.len = max(a.lens[s], 0);
   return r;
 }
+
+// The first key that a token at `pos` sees (negative positions see none; a
+// window up to 2^31 - 1 must not wrap there).
+__device__ __forceinline__ int first_seen(const AttendArgs& a, int pos) { return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0; }
 
 }  // namespace mxq

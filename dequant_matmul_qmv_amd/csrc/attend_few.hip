@@ -64,8 +64,8 @@ __device__ __forceinline__ Share share_of(const AttendArgs& a, int s) {
   const int64_t rows = static_cast<int64_t>(q.n) * a.group;
   if (rows > a.few_rows) return r;
   r.groups = static_cast<int>((rows + 16 * MT - 1) / (16 * MT));
-  const int hi = min(max(q.len, 0), a.width * a.pool.block);
-  const int lo = a.window > 0 ? max(0, q.len - q.n - a.window + 1) : 0;
+  const int hi = min(q.len, a.width * a.pool.block);
+  const int lo = first_seen(a, q.len - q.n);
   r.c0 = lo / kChunk;
   r.chunks = max(0, hi / kChunk + (hi % kChunk != 0) - r.c0);  // (hi may be near 2^31)
   return r;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rho = lane & 15, h = lane >> 4;
   const int row0 = rg * kRows, rows = min(kRows, sp.n * a.group - row0);
   const int pos0 = sp.len - sp.n;
-  const int limit = min(max(sp.len, 0), a.width * block);
+  const int limit = min(sp.len, a.width * block);
 
   // query rows of this lane (one of 16 for each mt), their fragments and key ranges
   u4 qf[MT][2 * U];
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
     factor[mt] = a.scale2 * inverse;
     const int pos = pos0 + tok;
     upto[mt] = min(pos + 1, limit);  // rows past the last repeat the first; they are not stored
-    from[mt] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    from[mt] = first_seen(a, pos);
     if (real) {
       all_from = max(all_from, from[mt]);
       all_upto = min(all_upto, upto[mt]);

@@ -127,13 +127,13 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   sp.len = __builtin_amdgcn_readfirstlane(sp.len);
   const int row0 = (tile_index - first) * kManyRows, rows = sp.n * a.group;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, h = lane >> 5;
-  const int limit = min(max(sp.len, 0), a.width * block), pos0 = sp.len - sp.n;
+  const int limit = min(sp.len, a.width * block), pos0 = sp.len - sp.n;
 
   // this lane's query row; rows past the last repeat it and are not stored
   const int mine = row0 + wave * 32 + col, row = min(mine, rows - 1);
   const int tok = row / a.group, hq = head * a.group + row - tok * a.group;
   const int pos = pos0 + tok;
-  const int upto = min(pos + 1, limit), from = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  const int upto = min(pos + 1, limit), from = first_seen(a, pos);
   u4 qf[KS];
   {
     const uint16_t* q = a.q + static_cast<int64_t>(sp.t0 + tok) * a.q_token + static_cast<int64_t>(hq) * a.q_head;
@@ -160,13 +160,13 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   const int last_row = min(row0 + wave * 32 + 31, rows - 1), first_row = min(row0 + wave * 32, rows - 1);
   const int pos_lo = pos0 + first_row / a.group, pos_hi = pos0 + last_row / a.group;
   // a wave without rows takes no part but in the staging
-  const int wave_upto = row0 + wave * 32 < rows ? min(pos_hi + 1, limit) : 0, wave_from = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
-  const int all_upto = min(pos_lo + 1, limit), all_from = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0;
+  const int wave_upto = row0 + wave * 32 < rows ? min(pos_hi + 1, limit) : 0, wave_from = first_seen(a, pos_lo);
+  const int all_upto = min(pos_lo + 1, limit), all_from = first_seen(a, pos_hi);
 
   // the tile's stages, and this part's share of them
   const int tile_last = min(row0 + kManyRows, rows) - 1;
   const int key_hi = min(pos0 + tile_last / a.group + 1, limit);
-  const int key_lo = a.window > 0 ? max(0, pos0 + row0 / a.group - a.window + 1) : 0;
+  const int key_lo = first_seen(a, pos0 + row0 / a.group);
   const int s_lo = key_lo / kStage, s_hi = max(s_lo, key_hi / kStage + (key_hi % kStage > 0));
   const int per = (s_hi - s_lo + a.many_splits - 1) / a.many_splits;
   const int begin = min(s_lo + part * per, s_hi), end = min(begin + per, s_hi);

@@ -126,6 +126,23 @@ def test_masked_pages_of_tiny_scales(new, dim):
 
 # ------------------------------------------------------------------------------------- windows, odd lengths
 @pytest.mark.gpu
+@pytest.mark.parametrize("window", [1, 2 ** 31 - 40, 2 ** 31 - 1, 2 ** 31, 2 ** 40])
+def test_wide_windows_and_more_new_tokens_than_keys(window):
+    """The first new tokens of a sequence shorter than they are have no keys, the others theirs, under any window."""
+    gen = torch.Generator().manual_seed(18)
+    block = 16
+    for lens, new in (([5, 3, 40], [9, 12, 7]), ([50, 3, 70], [130, 100, 70]), ([60], [200]), ([0, 9], [4, 9])):
+        pool = random_pool(12, 2, block, 64, gen)
+        tab = torch.randperm(12, generator=gen)[:len(lens) * 4].view(len(lens), 4).int() if len(lens) < 3 else torch.arange(12).view(3, 4).int()
+        tab = torch.cat((tab, tab[:, :1]), 1)
+        q = torch.randn(sum(new), 4, 64, generator=gen).half()
+        ref = attention_ref(q, pool, tab, lens, new, window, 0.125)
+        note(f"attention {lens} {new} window {window}")
+        out, lse = _attend(q, pool, tab, lens, new, window=window)
+        _check(out, lse, ref, f"{lens} {new} {window}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("length", [-1, -70, -2 ** 31])
 def test_negative_lengths_are_empty(length):
     gen = torch.Generator().manual_seed(19)
