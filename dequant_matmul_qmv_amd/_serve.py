@@ -173,9 +173,10 @@ class KvCache:
     ``k`` int8 [blocks, kv_heads, block, dim], ``v`` int8 [blocks, kv_heads, dim, block],
     ``k_scale`` and ``v_scale`` float32 [blocks, kv_heads], contiguous, on one device;
     block 16, 32, 64 or 128, dim 64 or 128.  A sequence's tokens ``j * block ..`` are in
-    the page ``table[s, j]`` of the table that the calls take."""
+    the page ``table[s, j]`` of the table that the calls take.  The tensors are read-only
+    attributes: the calls work on the memory that the cache was made of."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "device", "_struct")
+    __slots__ = ("_tensors", "_device", "_struct")
 
     def __init__(self, k, v, k_scale, v_scale):
         if k.dtype != torch.int8 or k.dim() != 4 or v.dtype != torch.int8 or v.dim() != 4:
@@ -192,7 +193,7 @@ class KvCache:
                 raise ValueError(f"KvCache: {name} must be contiguous and on {dev}")
         if block not in (16, 32, 64, 128) or dim not in (64, 128):
             raise ValueError(f"KvCache: block must be 16, 32, 64 or 128 and dim 64 or 128, got {block} and {dim}")
-        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, dev
+        self._tensors, self._device = (k, v, k_scale, v_scale), dev
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), blocks,
                                     kv_heads, block, dim)
 
@@ -203,6 +204,26 @@ class KvCache:
                    torch.zeros((blocks, kv_heads, dim, block), dtype=torch.int8, device=device),
                    torch.zeros((blocks, kv_heads), dtype=_f32, device=device),
                    torch.zeros((blocks, kv_heads), dtype=_f32, device=device))
+
+    @property
+    def k(self):
+        return self._tensors[0]
+
+    @property
+    def v(self):
+        return self._tensors[1]
+
+    @property
+    def k_scale(self):
+        return self._tensors[2]
+
+    @property
+    def v_scale(self):
+        return self._tensors[3]
+
+    @property
+    def device(self):
+        return self._device
 
     @property
     def blocks(self):
@@ -248,7 +269,7 @@ def mxq_kv_append(cache, k, v, table, lens, starts=None, *, stream=None):
     ``starts[s]:starts[s + 1]`` of k and v, or row s alone without ``starts``.
     The scheme, and what becomes of tokens without a page, is in include/mxq.h."""
     who = "mxq_kv_append"
-    dev = cache.device
+    dev = cache._device
     code = _HALF.get(k.dtype)
     if code is None:
         raise TypeError(f"{who}: k must be float16 or bfloat16")
@@ -274,7 +295,7 @@ def mxq_attention(q, cache, table, lens, starts=None, out=None, *, window: int =
     [tokens, heads, dim] in q's type, or (out, lse) with the log-sums float32
     [tokens, heads].  A row without keys gives 0 and -inf."""
     who = "mxq_attention"
-    dev = cache.device
+    dev = cache._device
     code = _HALF.get(q.dtype)
     if code is None:
         raise TypeError(f"{who}: q must be float16 or bfloat16")

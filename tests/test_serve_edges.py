@@ -161,3 +161,13 @@ def test_negative_lengths_are_empty(length):
         torch.cuda.synchronize()
         for got, was in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), pool):
             assert torch.equal(got.cpu(), was)
+
+
+# ------------------------------------------------------------------------------------------------ the cache
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale", "device", "blocks", "kv_heads", "block", "dim"])
+def test_a_caches_parts_cannot_be_replaced(name):
+    """The calls pass the addresses of the tensors that a cache was made of: another tensor in their place would leave
+    them with memory that may be freed."""
+    cache = object.__new__(mxq.KvCache)
+    with pytest.raises(AttributeError):
+        setattr(cache, name, None)
