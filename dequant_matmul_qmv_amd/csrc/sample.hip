@@ -176,6 +176,12 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int row, int 
   return static_cast<const char*>(a.logits) + static_cast<int64_t>(row) * a.row_stride * size;
 }
 
+// The row's uniform number; below 0 as 0, so that every row has a token to draw.
+__device__ __forceinline__ double uniform_of(const SampleArgs& a, int row) {
+  const float u = a.u[row];
+  return u < 0.0f ? 0.0 : static_cast<double>(u);
+}
+
 // A token's place in the descending order: its key, equals by index.
 __device__ __forceinline__ u64 word_of(uint32_t key, int i) { return (static_cast<u64>(key) << 20) | (0xFFFFFu - static_cast<uint32_t>(i)); }
 __device__ __forceinline__ uint32_t key_in(u64 word) { return static_cast<uint32_t>(word >> 20); }
@@ -379,7 +385,7 @@ __device__ __forceinline__ void draw_kept(const SampleArgs& a, Shared& sh, int r
     if (i == wave) base = all;
     all += sh.wave_mass[i];
   }
-  const Border border{static_cast<double>(a.u[row]) * static_cast<double>(all), all};
+  const Border border{uniform_of(a, row) * static_cast<double>(all), all};
   const auto over = [&](u64 sum) { return border.over(sum); };
   const u64 stop = base + incl, start = stop - m0 - m1;
   if (!over(start) && over(stop)) {
@@ -707,7 +713,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   }
 
   if (rule.open) {
-    const double want = static_cast<double>(a.u[row]) * total;
+    const double want = uniform_of(a, row) * total;
     // the piece that `want` falls in; the last of them where it reaches the total
     if (tid == 0) sh.found = 0;
     __syncthreads();
@@ -920,7 +926,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
       const u64 all = sh.wave_mass[0] + sh.wave_mass[1] + sh.wave_mass[2] + sh.wave_mass[3];
       u64 sum = 0;
       for (int t = 0; t < 4; ++t) sum += sh.pairs.ahead[t][tid];
-      const Border border{static_cast<double>(a.u[row]) * static_cast<double>(all), all};
+      const Border border{uniform_of(a, row) * static_cast<double>(all), all};
       if (border.over(sum) && !border.over(sum - mass)) {
         a.tokens[row] = index_in(word);
         a.probs[row] = static_cast<float>(w.weight(key_in(word)) * kFix / static_cast<double>(all));

@@ -380,7 +380,7 @@ typedef struct mxq_sampling {
  *   w_i >= min_p;
  * the first token always is.  tokens[r] is the first, in index order, whose
  * running sum of kept weights exceeds u[r] times their total, u in [0, 1)
- * (beyond: the last kept one); probs[r] its weight over that total.  A
+ * (below: as 0; beyond or NaN: the last kept one); probs[r] its weight over that total.  A
  * temperature <= 0 takes the largest logit, the first of equals, at
  * probability 1; so do top_p <= 0 or NaN and min_p > 1 or NaN.  A NaN logit
  * counts as -inf; a row of nothing but -inf is uniform.  Weights are taken in

@@ -171,3 +171,34 @@ def test_a_caches_parts_cannot_be_replaced(name):
     cache = object.__new__(mxq.KvCache)
     with pytest.raises(AttributeError):
         setattr(cache, name, None)
+
+
+# ------------------------------------------------------------------------------------------------- sampling
+DRAWS = [(1.0, 0, 1.0, 0.0), (0.8, 40, 0.95, 0.0), (1.0, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.02), (1.0, 2500, 1.0, 0.0),
+         (3.0, 3000, 0.9, 0.1), (0.0, 0, 1.0, 0.0)]
+
+
+def _draw(x, u, s, **kw):
+    rows = x.shape[0]
+    tok = torch.full((rows,), -7, dtype=torch.int32, device=DEV)
+    prob = torch.full((rows,), -7.0, device=DEV)
+    mxq.mxq_sample(x, u, tok, prob, temperature=s[0], top_k=s[1], top_p=s[2], min_p=s[3], **kw)
+    torch.cuda.synchronize()
+    return tok.cpu().tolist(), prob.cpu().tolist()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 150])
+@pytest.mark.parametrize("vocab", [300, 9001])
+def test_uniform_numbers_outside_their_range(vocab, rows):
+    """Below 0 as 0; 1, beyond it and NaN: the last kept token, by index."""
+    gen = torch.Generator().manual_seed(50)
+    x = (torch.randn(rows, vocab, generator=gen) * 0.7).half().to(DEV)
+    full = lambda v: torch.full((rows,), v, device=DEV)  # noqa: E731
+    for s in DRAWS:
+        note(f"sample u outside, rows {rows} vocab {vocab} {s}")
+        zero, last = _draw(x, full(0.0), s), _draw(x, full(1 - 2.0 ** -24), s)
+        for v in (-0.0, -1e-30, -0.5, -3.0, -float("inf")):
+            assert _draw(x, full(v), s) == zero, (s, v)
+        for v in (1.0, 7.0, float("inf"), float("nan")):
+            assert _draw(x, full(v), s) == last, (s, v)
