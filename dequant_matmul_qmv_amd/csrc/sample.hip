@@ -113,9 +113,10 @@ __device__ __forceinline__ void load_keys8(const void* row, int i, int n, uint32
 }
 
 // 2^z for z <= 0: whole part by the exponent, the rest, within a half, by the
-// series of exp(r ln 2) to r^11 (6e-15).
+// series of exp(r ln 2) to r^11 (6e-15).  0 for -infinity (and NaN: 0 times it,
+// a masked token at an infinite temperature).
 __device__ __forceinline__ double exp2_neg(double z) {
-  z = fmax(z, -1000.0);
+  z = fmax(z, -1100.0);
   const double n = __builtin_rint(z), r = (z - n) * 0.69314718055994530942;
   double y = 1.0 / 39916800.0;
   y = __builtin_fma(y, r, 1.0 / 3628800.0);
@@ -225,9 +226,7 @@ struct Shared {
   uint32_t bin_count[kBins];            // beside word, which then holds the bins' weights
   u64 wave_mass[kDrawWaves], wave_bits[kDrawWaves];
   uint32_t wave_count[kDrawWaves], red[kDrawWaves];
-  double wave_sum[kDrawWaves];
   u64 above, end, other;
-  double at;
   uint32_t found, hits, listed;
 };
 static_assert(kMaxPieces * kPiece == 1 << 20 && kMaxPieces == 2 * kDrawThreads && kBins == 2 * kDrawThreads, "two a thread");
@@ -689,49 +688,42 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     return;
   }
 
-  // the whole row's weight, by pieces in index order: this thread's, and that before it
-  double total = 0.0, before = 0.0, mine = 0.0;
-  const int pieces_each = (a.piece_count + kDrawThreads - 1) / kDrawThreads;
-  const int p0 = min(tid * pieces_each, a.piece_count), p1 = min(p0 + pieces_each, a.piece_count);
-  auto piece_weight = [&](int p) {
-    uint32_t m = 0;
-    for (int c = p * (kPiece / kCell); c < min((p + 1) * (kPiece / kCell), a.cell_count); ++c) m = max(m, cells[c]);
-    return pieces[p] * w.weight(m);
-  };
+  // The whole row's weight: that of each piece, rounded to the integers' unit,
+  // so that the sums before and through a piece are exact and ascend.
+  double total = 0.0;
+  const int pieces_each = (a.piece_count + kDrawThreads - 1) / kDrawThreads, p0 = tid * pieces_each;
+  u64 piece[2] = {0, 0}, before = 0, all = 0;  // of this thread, before them, of the row
   if (rule.by_piece) {
-    for (int p = p0; p < p1; ++p) mine += piece_weight(p);
-    const double incl = wave_scan(mine);
-    if (lane == 63) sh.wave_sum[wave] = incl;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (e < pieces_each && p0 + e < a.piece_count) {
+        uint32_t m = 0;
+        for (int c = (p0 + e) * (kPiece / kCell); c < min((p0 + e + 1) * (kPiece / kCell), a.cell_count); ++c) m = max(m, cells[c]);
+        piece[e] = static_cast<u64>(__builtin_rint(pieces[p0 + e] * w.weight(m) * kFix));
+      }
+    const u64 incl = wave_scan(piece[0] + piece[1]);
+    if (lane == 63) sh.wave_mass[wave] = incl;
     __syncthreads();
-    double base = 0.0;
+    u64 base = 0;
     for (int i = 0; i < kDrawWaves; ++i) {
-      if (i == wave) base = total;
-      total += sh.wave_sum[i];
+      if (i == wave) base = all;
+      all += sh.wave_mass[i];
     }
-    before = base + lane_move<0x138, 0xF>(incl);  // wave_shr 1
-    mine = base + incl;  // from here on: the sum through this thread's pieces
+    before = base + incl - piece[0] - piece[1];
+    total = static_cast<double>(all);
   }
 
   if (rule.open) {
-    const double want = uniform_of(a, row) * total;
-    // the piece that `want` falls in; the last of them where it reaches the total
-    if (tid == 0) sh.found = 0;
-    __syncthreads();
-    if (before <= want && mine > want) {
-      double run = before;
-      int p = p0;
-      for (; p < p1 - 1; ++p) {
-        const double next = run + piece_weight(p);
-        if (next > want) break;
-        run = next;
-      }
-      sh.found = static_cast<uint32_t>(p) + 1;
-      sh.at = run;
+    // the piece that the border falls in; the last with weight where it reaches the total
+    const Border border{uniform_of(a, row) * total, all};
+    if (!border.over(before) && border.over(before + piece[0] + piece[1])) {
+      const bool second = !border.over(before + piece[0]);
+      sh.found = static_cast<uint32_t>(p0) + second;
+      sh.above = second ? before + piece[0] : before;
     }
     __syncthreads();
     if (wave != 0) return;
-    const bool past = sh.found == 0;
-    const int p = past ? a.piece_count - 1 : static_cast<int>(sh.found) - 1, i0 = p * kPiece + lane * 8;
+    const int i0 = static_cast<int>(sh.found) * kPiece + lane * 8;
     uint32_t key[8];
     load_keys8<T>(x, i0, n, key);
     double wt[8], s = 0.0;
@@ -740,10 +732,10 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
       wt[e] = key[e] != 0 ? w.weight(key[e]) : 0.0;
       s += wt[e];
     }
-    const double incl = (past ? 0.0 : sh.at) + wave_scan(s), edge = past ? 1e300 : want;
+    const double incl = static_cast<double>(sh.above) / kFix + wave_scan(s), edge = total > border.target ? border.target / kFix : 1e300;
     const u64 hit = __ballot(incl > edge), some = __ballot(s > 0.0);
-    // rounding may leave the piece's own sum a hair short of its weight: its last token with weight then
-    const int src = hit != 0 ? __ffsll(hit) - 1 : 63 - __clzll(some | 1);
+    // rounding may leave the tokens' sum a hair short of the piece's: its last token with weight then
+    const int src = hit != 0 ? __ffsll(hit) - 1 : 63 - __clzll(some);
     if (lane == src) {
       double run = incl - s;
       int last = 0, pick = -1;
@@ -758,7 +750,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
 #pragma unroll
       for (int e = 0; e < 8; ++e) chosen = e == pick ? wt[e] : chosen;
       a.tokens[row] = i0 + pick;
-      a.probs[row] = static_cast<float>(chosen / total);
+      a.probs[row] = static_cast<float>(chosen * kFix / total);
     }
     return;
   }
@@ -784,7 +776,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   // top_p alone: a list of what is likely; it is no use where it does not hold the whole prefix
   const bool guessed = limit_p && !limit_k && !floor && n > kList;
   // tokens of less than (1 - p) / n of the total: all of them together are less than what top_p leaves out
-  if (guessed && finite) low = max(low, key_below(log(static_cast<double>(n) / ((1.0 - static_cast<double>(rule.p)) * total))));
+  if (guessed && finite) low = max(low, key_below(log(static_cast<double>(n) / ((1.0 - static_cast<double>(rule.p)) * (total / kFix)))));
   const uint32_t start = low;
   const bool binned = finite && (limit_k || limit_p);
   const int guess = limit_k ? rule.k : guessed ? min(kGuess, a.cell_count / 2) : 0;
@@ -871,7 +863,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
     if (guessed) {
       for (int i = tid; i < listed; i += kDrawThreads) held += sh.mass[i];
       held = block_sum(sh, held);
-      small = static_cast<double>(held) >= static_cast<double>(rule.p) * total * kFix;
+      small = static_cast<double>(held) >= static_cast<double>(rule.p) * total;
     }
     if (small && listed <= kShort) {
       // A look from each token at all others, by four threads a token: its
@@ -904,7 +896,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
         if (rank == last) sh.above = ahead + mass;
       }
       __syncthreads();
-      const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(sh.above) : total * kFix);
+      const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(sh.above) : total);
       const bool in = mine && rank <= last && (rank == 0 || !limit_p || static_cast<double>(ahead) < want) &&
                       static_cast<double>(mass) >= least;
       if (mine) sh.mass[tid] = in ? mass : 0;
@@ -946,7 +938,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
           for (int i = tid; i < listed; i += kDrawThreads) held += sh.word[i] >= end ? sh.mass[i] : 0;
           held = block_sum(sh, held);
         }
-        const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total * kFix);
+        const double want = static_cast<double>(rule.p) * (limit_k ? static_cast<double>(held) : total);
         end = max(end, select_word(sh, item, listed, true, want, 0));
       }
     }
@@ -954,7 +946,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   if (!small) {
     if (tid == 0) {
       const int state = binned ? kBinned : finite && !limit_k && !limit_p ? kSums : kSearch;
-      a.plans[row] = SamplePlan{state, top, bound, bins.scale, 0, 0, total * kFix};
+      a.plans[row] = SamplePlan{state, top, bound, bins.scale, 0, 0, total};
     }
     if (!a.ahead)
       for (int i = tid; i < kBins; i += kDrawThreads) {

@@ -383,9 +383,12 @@ typedef struct mxq_sampling {
  * (below: as 0; beyond or NaN: the last kept one); probs[r] its weight over that total.  A
  * temperature <= 0 takes the largest logit, the first of equals, at
  * probability 1; so do top_p <= 0 or NaN and min_p > 1 or NaN.  A NaN logit
- * counts as -inf; a row of nothing but -inf is uniform.  Weights are taken in
- * f64 and summed exactly in steps of 2^-43: the draw does not depend on the
- * order of summation and is the same from run to run.
+ * counts as -inf; a row of nothing but -inf is uniform, in others -inf has no
+ * weight.  Weights are taken in f64.  What is added in no fixed order is added in
+ * whole steps of 2^-43, exactly: tokens where a row has limits (those below
+ * 2^-44 then have no weight), and pieces of 512 neighbours where it has none, or
+ * for the total that top_p without top_k asks for; within a piece f64 sums in a
+ * fixed order.  So the draw is the same from run to run.
  *   logits  f16|bf16|f32, row r at r * row_stride, 1 <= vocab <= 2^20
  *   u       f32 [rows];  tokens i32 [rows];  probs f32 [rows]
  * `settings` is a host structure, read during the call.  Rows use the split

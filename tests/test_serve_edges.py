@@ -202,3 +202,29 @@ def test_uniform_numbers_outside_their_range(vocab, rows):
             assert _draw(x, full(v), s) == zero, (s, v)
         for v in (1.0, 7.0, float("inf"), float("nan")):
             assert _draw(x, full(v), s) == last, (s, v)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("vocab", [9, 700, 5000, 128256])
+def test_masked_tokens_are_never_drawn(vocab, t):
+    """Rows without limits (and with), whose last tokens, or whole pieces of tokens, are -inf or NaN."""
+    gen = torch.Generator().manual_seed(51)
+    x = torch.randn(6, vocab, generator=gen).to({**HALF, "f32": torch.float32}[t])
+    x[0, vocab // 2:] = -torch.inf
+    x[1, 1:] = torch.nan
+    x[2, :-1] = -torch.inf
+    x[3, ::2] = -torch.inf
+    x[4, vocab // 3:] = torch.nan
+    x[4, -1] = -torch.inf
+    ok = ~(torch.isneginf(x) | torch.isnan(x))
+    last = [int(torch.nonzero(r).max()) for r in ok]
+    xd = x.to(DEV)
+    for s in DRAWS + [(1e30, 0, 1.0, 0.0), (float("inf"), 0, 1.0, 0.0), (1e30, 0, 0.9, 0.0)]:
+        for v in (0.0, 0.3, 0.99, 1 - 2.0 ** -24, 1.0, float("nan")):
+            note(f"sample masked {vocab} {t} {s} {v}")
+            tok, prob = _draw(xd, torch.full((6,), v, device=DEV), s)
+            assert all(bool(ok[r, i]) for r, i in enumerate(tok)), (s, v, tok)
+            assert all(0 < p <= 1 for p in prob), (s, v, prob)
+            if s == DRAWS[0] and not v < 1:
+                assert tok == last, (s, v)
