@@ -84,12 +84,13 @@ __device__ __forceinline__ u4 bf16_to_scaled_f16(u4 v, float factor) {
   return u4{o[0], o[1], o[2], o[3]};
 }
 
-// A power of two that brings `top` (a bf16 row's largest magnitude) into
-// [1, 2), and its inverse.  Zero, infinite and NaN rows keep 1.
+// A power of two that brings `top` (a bf16 row's largest magnitude) near 1 (to
+// [1, 4); below it for rows under bf16's normal range), and its inverse.  Zero,
+// infinite and NaN rows keep 1.
 __device__ __forceinline__ void row_factor(float top, float& factor, float& inverse) {
-  const uint32_t e = (__float_as_uint(top) >> 23) & 0xFFu;
   // 2^(127-e) stays a normal number for e of 1 .. 253
-  const bool fine = top > 0.0f && e >= 1 && e <= 253;
+  const uint32_t e = min(max((__float_as_uint(top) >> 23) & 0xFFu, 1u), 253u);
+  const bool fine = top > 0.0f && top < __builtin_inff();
   factor = fine ? __uint_as_float((254u - e) << 23) : 1.0f;
   inverse = fine ? __uint_as_float(e << 23) : 1.0f;
 }

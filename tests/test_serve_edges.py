@@ -112,7 +112,7 @@ def test_masked_pages_of_tiny_scales(new, dim):
     """Pages whose v scales' quotient is past f32's range, the small one's keys masked for the rows beside the large one."""
     gen = torch.Generator().manual_seed(3 * dim + new)
     block, length = 16, 150
-    pool = random_pool(10, 1, block, dim, gen)
+    pool = list(random_pool(10, 1, block, dim, gen))
     pool[3][::3] *= 6000.0                         # up to 180
     pool[3][2::3] = 2.0 ** -126 * 1.5
     tab = torch.arange(10, dtype=torch.int32)[None]
@@ -228,3 +228,24 @@ def test_masked_tokens_are_never_drawn(vocab, t):
             assert all(0 < p <= 1 for p in prob), (s, v, prob)
             if s == DRAWS[0] and not v < 1:
                 assert tok == last, (s, v)
+
+
+# --------------------------------------------------------------------------------------- queries of any size
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 5, 140])
+def test_bf16_queries_at_the_ends_of_their_range(new, dim):
+    """Rows whose largest value has bf16's highest exponent, or is below its normal range, over keys of the opposite
+    size: the scores are ordinary."""
+    gen = torch.Generator().manual_seed(dim + new)
+    block, length = 32, 200
+    tab = torch.randperm(7, generator=gen).int()[None]
+    for size, key in ((2.0 ** 127, 2.0 ** -127), (2.0 ** -130, 2.0 ** 126)):
+        pool = list(random_pool(7, 2, block, dim, gen))
+        pool[2] *= key
+        q = ((torch.rand(new, 4, dim, generator=gen) + 0.5).clamp(max=1.9) * size * torch.randn(new, 4, dim, generator=gen).sign()).bfloat16()
+        assert bool(torch.isfinite(q).all())
+        ref = attention_ref(q, pool, tab, [length], [new], 0, dim ** -0.5)
+        note(f"attention bf16 q of {size}, {new} new, dim {dim}")
+        out, lse = _attend(q, pool, tab, [length], [new])
+        _check(out, lse, ref, f"q of {size}")
