@@ -138,7 +138,9 @@ mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const m
   if (heads > 0 && (a.pool.kv_heads == 0 || heads % a.pool.kv_heads != 0))
     return report(MXQ_ERR_UNSUPPORTED, "mxq_attention: heads must be a multiple of the cache's kv_heads");
   if (heads == 0) return MXQ_OK;
-  if (!(scale - scale == 0.0f)) return report(MXQ_ERR_INVALID_ARG, "mxq_attention: scale must be finite");
+  // the kernels take it times log2(e)
+  const float scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  if (!(scale2 - scale2 == 0.0f)) return report(MXQ_ERR_INVALID_ARG, "mxq_attention: scale must be finite, also times log2(e)");
   st = check_paging("mxq_attention", a.pool, table, table_stride, width, lens, starts, tokens, seqs);
   if (st != MXQ_OK) return st;
   if (tokens == 0 || seqs == 0) return MXQ_OK;
@@ -162,7 +164,7 @@ mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const m
   a.heads = heads;
   a.group = heads / a.pool.kv_heads;
   a.window = static_cast<int>(window > INT32_MAX ? 0 : window);
-  a.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  a.scale2 = scale2;
   a.bf16 = dtype == MXQ_BF16;
   a.stream = static_cast<hipStream_t>(stream);
   mxq::DeviceInfo dev;

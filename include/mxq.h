@@ -305,10 +305,10 @@ typedef struct mxq_kv_cache {
 /*
  * mxq_kv_append -- quantize new keys and values into the cache.
  *
- * Sequence s has lens[s] tokens (below 0: none) with its new ones, which are its last; its new
- * rows of k and v are starts[s] .. starts[s + 1] (starts: i32 [seqs + 1], from
- * 0 to `tokens`, not descending), or row s alone where starts is null (then
- * tokens == seqs).  For each page that gets new tokens, and each head:
+ * Sequence s has lens[s] tokens (below 0: none) with its new ones, which are its
+ * last; its new rows of k and v are starts[s] .. starts[s + 1] (starts: i32
+ * [seqs + 1], from 0 to `tokens`, not descending), or row s alone where starts is
+ * null (then tokens == seqs).  For each page that gets new tokens, and each head:
  *   fresh = max |x| / 127 over its new tokens,
  *   scale = max(old scale, fresh) where the page holds older tokens of the
  *           sequence, else fresh,
@@ -336,7 +336,8 @@ mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_tok
  * window > 0, and an existing page (a table entry in 0 .. blocks - 1); query
  * head h reads kv head h / (heads / kv_heads).  pos(t) is lens[s] minus the
  * number of the sequence's new tokens from t on.  A row without keys gives 0.
- * Sequences, their rows and their table as for mxq_kv_append.
+ * Sequences, their rows and their table as for mxq_kv_append.  scale times log2(e)
+ * is finite.
  *   q    f16|bf16, element (t, h, d) at t * q_token + h * q_head + d, rows
  *        16-byte aligned (strides multiples of 8)
  *   out  the same type [tokens, heads, dim], 8-byte aligned
@@ -346,9 +347,9 @@ mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_tok
  * probabilities f16 relative to their row's largest (a bf16 q's smallest values
  * are rounded at 2^-25 of its row's largest).  A value below 2^-148 of the row's
  * largest p_j times the largest scale of v in the sequence may be left out of
- * the sum over p_j v_j.  Results are the same bits from
- * run to run.  Partial results of a split key axis go to the split workspace
- * (see above); MXQ_ERR_HIP if that cannot be had.
+ * the sum over p_j v_j.  Results are the same bits from run to run.  Partial
+ * results of a split key axis go to the split workspace (see above); MXQ_ERR_HIP
+ * if that cannot be had.
  */
 mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const mxq_kv_cache* cache,
                          const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
@@ -380,8 +381,8 @@ typedef struct mxq_sampling {
  *   w_i >= min_p;
  * the first token always is.  tokens[r] is the first, in index order, whose
  * running sum of kept weights exceeds u[r] times their total, u in [0, 1)
- * (below: as 0; beyond or NaN: the last kept one); probs[r] its weight over that total.  A
- * temperature <= 0 takes the largest logit, the first of equals, at
+ * (below: as 0; beyond or NaN: the last kept one); probs[r] its weight over that
+ * total.  A temperature <= 0 takes the largest logit, the first of equals, at
  * probability 1; so do top_p <= 0 or NaN and min_p > 1 or NaN.  A NaN logit
  * counts as -inf; a row of nothing but -inf is uniform, in others -inf has no
  * weight.  Weights are taken in f64.  What is added in no fixed order is added in

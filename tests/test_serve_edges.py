@@ -8,6 +8,7 @@ import torch
 import dequant_matmul_qmv_amd as mxq
 from tests.gpu_util import note
 from tests.serve_util import HALF, append_ref, attention_ref, random_pool
+from tests.test_serve_attention import _call as _attention_call
 from tests.test_serve_attention import _check
 
 DEV = "cuda:0"
@@ -249,3 +250,8 @@ def test_bf16_queries_at_the_ends_of_their_range(new, dim):
         note(f"attention bf16 q of {size}, {new} new, dim {dim}")
         out, lse = _attend(q, pool, tab, [length], [new])
         _check(out, lse, ref, f"q of {size}")
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38, float("nan"), float("-inf")])
+def test_a_scale_that_overflows_is_refused(scale):
+    assert _attention_call(scale=scale) == mxq.MXQ_ERR_INVALID_ARG
