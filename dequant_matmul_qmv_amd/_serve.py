@@ -325,7 +325,8 @@ def _setting(who, name, value, rows, dtype, dev):
             raise ValueError(f"{who}: {name} must be a number or a contiguous "
                              f"{str(dtype).replace('torch.', '')} tensor [{rows}] on {dev}")
         return value.data_ptr(), 0
-    return None, value
+    # (ctypes keeps an int's low 32 bits)
+    return None, min(max(value, -1), 0x7FFFFFFF) if dtype == _i32 else value
 
 
 def mxq_sample(logits, u, tokens=None, probs=None, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):

@@ -255,3 +255,15 @@ def test_bf16_queries_at_the_ends_of_their_range(new, dim):
 @pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38, float("nan"), float("-inf")])
 def test_a_scale_that_overflows_is_refused(scale):
     assert _attention_call(scale=scale) == mxq.MXQ_ERR_INVALID_ARG
+
+
+def test_numbers_past_32_bits_as_top_k():
+    """A number that the library's int32 cannot hold stays what it means: no limit."""
+    from dequant_matmul_qmv_amd import _serve
+    for k in (2 ** 31, 2 ** 32 + 5, 2 ** 63, 10 ** 30):
+        p, k_all = _serve._setting("mxq_sample", "top_k", k, 3, torch.int32, None)
+        assert p is None and _serve._SamplingStruct(None, None, None, None, 1.0, k_all, 1.0, 0.0).top_k_all == 2 ** 31 - 1
+    for k in (-1, -2 ** 31, -2 ** 32 + 5, -10 ** 30, 0):
+        _, k_all = _serve._setting("mxq_sample", "top_k", k, 3, torch.int32, None)
+        assert _serve._SamplingStruct(None, None, None, None, 1.0, k_all, 1.0, 0.0).top_k_all <= 0
+    assert _serve._setting("mxq_sample", "top_k", 40, 3, torch.int32, None) == (None, 40)
