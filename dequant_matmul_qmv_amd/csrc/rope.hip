@@ -178,6 +178,7 @@ __global__ __launch_bounds__(256) void rope_narrow_kernel(RopeArgs a) {
 namespace {
 
 constexpr int64_t kL2Bytes = 32 << 20;  // of the eight dies
+constexpr int64_t kPartTokens = 1 << 23;  // of a launch, whose grid ends below 2^32 threads
 
 template <bool BF16, bool INTER>
 hipError_t launch_wide(const RopeArgs& a) {
@@ -189,9 +190,7 @@ hipError_t launch_wide(const RopeArgs& a) {
   return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_rope(const RopeArgs& a) {
+hipError_t launch_part(const RopeArgs& a) {
   bool wide = a.dim % 8 == 0 && a.rot % (a.interleaved ? 8 : 16) == 0;
   for (const RopeSide& s : a.side)
     if (s.heads > 0)
@@ -203,6 +202,24 @@ hipError_t launch_rope(const RopeArgs& a) {
   if (a.bf16) hipLaunchKernelGGL((rope_narrow_kernel<true>), grid, dim3(256), 0, a.stream, a);
   else hipLaunchKernelGGL((rope_narrow_kernel<false>), grid, dim3(256), 0, a.stream, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeArgs& a) {
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += kPartTokens) {
+    RopeArgs b = a;
+    b.tokens = a.tokens - t0 < kPartTokens ? a.tokens - t0 : kPartTokens;
+    b.positions += t0;
+    for (RopeSide& s : b.side)
+      if (s.heads > 0) {
+        s.in += t0 * s.in_token;
+        s.out += t0 * s.out_token;
+      }
+    const hipError_t e = launch_part(b);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace mxq

@@ -7,7 +7,7 @@ import torch
 
 import dequant_matmul_qmv_amd as mxq
 from tests.gpu_util import note
-from tests.serve_util import HALF, append_ref, attention_ref, random_pool
+from tests.serve_util import HALF, append_ref, attention_ref, random_pool, rope_ref
 from tests.test_serve_attention import _call as _attention_call
 from tests.test_serve_attention import _check
 
@@ -267,3 +267,24 @@ def test_numbers_past_32_bits_as_top_k():
         _, k_all = _serve._setting("mxq_sample", "top_k", k, 3, torch.int32, None)
         assert _serve._SamplingStruct(None, None, None, None, 1.0, k_all, 1.0, 0.0).top_k_all <= 0
     assert _serve._setting("mxq_sample", "top_k", 40, 3, torch.int32, None) == (None, 40)
+
+
+# --------------------------------------------------------------------------------------------- large launches
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,rot", [(2, 2), (16, 16)])
+def test_rope_of_more_tokens_than_a_grid_holds(dim, rot):
+    """A workgroup of 256 threads a token: 2^24 of them are one grid's limit."""
+    n = 2 ** 24 + 9
+    gen = torch.Generator(device=DEV).manual_seed(60)
+    q = torch.randn(n, 1, dim, generator=gen, device=DEV).half()
+    positions = torch.randint(0, 131072, (n,), generator=gen, device=DEV, dtype=torch.int32)
+    inv_freq = torch.logspace(0, -3, rot // 2, device=DEV)
+    note(f"rope of {n} tokens, dim {dim}")
+    out, _ = mxq.mxq_rope(q, None, inv_freq, positions)
+    torch.cuda.synchronize()
+    for at in (0, 2 ** 23 - 4, 2 ** 24 - 4, n - 8):
+        part = slice(at, at + 8)
+        want = rope_ref(q[part], inv_freq, positions[part], False)
+        err = np.abs(out[part].double().cpu().numpy() - want)
+        # a turn in f32 (2^-22 of the pair's size), rounded once to f16
+        assert (err <= np.abs(want) * 2.0 ** -11 + 2.0 ** -25 + np.abs(want).max() * 2.0 ** -21).all(), at
