@@ -515,16 +515,23 @@ hipError_t launch_parts(const AttendArgs& a, unsigned slots) {
   return hipGetLastError();
 }
 
+// Waves of a workgroup: twice as many where it takes all keys of more than a
+// round (32 rows of 128 values do not fit the registers of that many waves).
+constexpr int lone_waves(int values) { return values >= 256 ? kFewWaves : 2 * kFewWaves; }
+int few_waves(const AttendArgs& a, int values, bool joined) {
+  return !joined && static_cast<int64_t>(a.width) * a.pool.block > kFewWaves * kChunk ? lone_waves(values) : kFewWaves;
+}
+// One wave a row joins where the sequences are too many to have many parts each
+// (64 sequences: 45.4 -> 44.1 us).
+int join_threads(const AttendArgs& a) { return 8 * static_cast<int64_t>(a.seqs) * a.pool.kv_heads >= a.target ? 64 : 256; }
+
 template <int DIM, int MT>
 hipError_t launch_mt(const AttendArgs& a, unsigned slots, bool joined) {
-  const bool lone = !joined && static_cast<int64_t>(a.width) * a.pool.block > kFewWaves * kChunk;
-  // (32 rows of 128 values do not fit the registers of that many waves)
-  constexpr int kLoneWaves = MT * DIM >= 256 ? kFewWaves : 2 * kFewWaves;
-  hipError_t e = lone ? launch_parts<DIM, MT, kLoneWaves>(a, slots) : launch_parts<DIM, MT, kFewWaves>(a, slots);
+  hipError_t e = few_waves(a, MT * DIM, joined) == kFewWaves ? launch_parts<DIM, MT, kFewWaves>(a, slots)
+                                                             : launch_parts<DIM, MT, lone_waves(MT * DIM)>(a, slots);
   if (e != hipSuccess || !joined) return e;
   const dim3 grid(static_cast<unsigned>(a.seqs) * static_cast<unsigned>(a.join_new), static_cast<unsigned>(a.heads));
-  // one wave a row where the sequences are too many to have many parts each (64 sequences: 45.4 -> 44.1 us)
-  if (8 * static_cast<int64_t>(a.seqs) * a.pool.kv_heads >= a.target) {
+  if (join_threads(a) == 64) {
     if (a.bf16) hipLaunchKernelGGL((attend_join_kernel<DIM, MT, true, 64>), grid, dim3(64), 0, a.stream, a);
     else hipLaunchKernelGGL((attend_join_kernel<DIM, MT, false, 64>), grid, dim3(64), 0, a.stream, a);
   } else {
@@ -567,7 +574,9 @@ hipError_t launch_attend(const AttendArgs& given, const DeviceInfo& dev) {
   const bool joined = few && static_cast<int64_t>(a.width) * a.pool.block > kLoneKeys;
   a.min_chunks = joined ? kMinChunks : kLoneKeys / kChunk;
   const int64_t slots = ends + (joined ? a.target : 0);
-  if (slots > INT32_MAX) return hipErrorInvalidValue;
+  if (few && (!grid_fits(slots, 64 * few_waves(a, mt * a.pool.dim, joined)) ||
+              (joined && !grid_fits(static_cast<int64_t>(a.seqs) * a.join_new, join_threads(a)))))
+    return kTooLarge;
   a.slots = static_cast<int>(slots);
   const size_t sums = joined ? static_cast<size_t>(slots) * per * a.pool.dim * 4 : 0;
   const size_t few_bytes = joined ? sums + static_cast<size_t>(slots) * per * 8 : 0;
@@ -581,6 +590,7 @@ hipError_t launch_attend(const AttendArgs& given, const DeviceInfo& dev) {
     if (splits > 32) splits = 32;
     if (splits > 1) a.many_splits = static_cast<int>(splits);
   }
+  if (many && (!grid_fits(many_tiles(a) * hk * a.many_splits, 256) || (a.many_splits > 1 && !grid_fits(a.tokens, 256)))) return kTooLarge;
   const size_t many_bytes = many ? many_part_bytes(a) : 0;
 
   const auto enqueue = [&](float* ws) {

@@ -511,7 +511,6 @@ size_t many_part_bytes(const AttendArgs& a) {
 hipError_t launch_many(const AttendArgs& given, float* ws) {
   AttendArgs a = given;
   const int64_t grid = many_tiles(a) * a.pool.kv_heads * a.many_splits;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
   a.many_part = ws;
   a.many_units = static_cast<int>(grid);

@@ -297,7 +297,10 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvAppendArgs 
 namespace {
 
 template <int PER, int THREADS>
-hipError_t launch_pages(const KvAppendArgs& a, dim3 grid) {
+hipError_t launch_pages(const KvAppendArgs& a) {
+  const int64_t pages = a.tokens / a.pool.block + 2 * static_cast<int64_t>(a.seqs);
+  if (!grid_fits(pages, THREADS)) return kTooLarge;
+  const dim3 grid(static_cast<unsigned>(pages), static_cast<unsigned>(a.pool.kv_heads));
   const size_t lds = static_cast<size_t>(a.pool.dim) * a.pool.block;
   if (a.bf16) hipLaunchKernelGGL((kv_append_kernel<true, PER, THREADS>), grid, dim3(THREADS), lds, a.stream, a);
   else hipLaunchKernelGGL((kv_append_kernel<false, PER, THREADS>), grid, dim3(THREADS), lds, a.stream, a);
@@ -307,19 +310,17 @@ hipError_t launch_pages(const KvAppendArgs& a, dim3 grid) {
 }  // namespace
 
 hipError_t launch_kv_append(const KvAppendArgs& a) {
-  const unsigned heads = static_cast<unsigned>(a.pool.kv_heads);
   if (a.starts == nullptr) {
-    const dim3 grid(static_cast<unsigned>(a.seqs), heads);
+    const dim3 grid(static_cast<unsigned>(a.seqs), static_cast<unsigned>(a.pool.kv_heads));
     if (a.bf16) hipLaunchKernelGGL((kv_append_one_kernel<true>), grid, dim3(64), 0, a.stream, a);
     else hipLaunchKernelGGL((kv_append_one_kernel<false>), grid, dim3(64), 0, a.stream, a);
     return hipGetLastError();
   }
-  const dim3 grid(static_cast<unsigned>(a.tokens / a.pool.block + 2 * static_cast<int64_t>(a.seqs)), heads);
   switch (a.pool.dim * a.pool.block / 2048) {
-    case 8: return launch_pages<4, 512>(a, grid);
-    case 4: return launch_pages<4, 256>(a, grid);
-    case 2: return launch_pages<2, 256>(a, grid);
-    default: return launch_pages<1, 256>(a, grid);
+    case 8: return launch_pages<4, 512>(a);
+    case 4: return launch_pages<4, 256>(a);
+    case 2: return launch_pages<2, 256>(a);
+    default: return launch_pages<1, 256>(a);
   }
 }
 

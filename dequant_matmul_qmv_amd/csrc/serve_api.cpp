@@ -14,7 +14,11 @@ using mxq::report_hip;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-mxq_status finish(const char* who, hipError_t e) { return e == hipSuccess ? MXQ_OK : report_hip(who, e); }
+mxq_status finish(const char* who, hipError_t e) {
+  if (e == mxq::kTooLarge)
+    return report(MXQ_ERR_UNSUPPORTED, std::string(who) + ": more sequences, tokens and heads than one launch holds (split the call)");
+  return e == hipSuccess ? MXQ_OK : report_hip(who, e);
+}
 
 bool half_type(mxq_dtype t) { return t == MXQ_F16 || t == MXQ_BF16; }
 

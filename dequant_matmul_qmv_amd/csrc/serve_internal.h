@@ -15,6 +15,11 @@ void clear_error();
 mxq_status report(mxq_status s, const std::string& msg);
 mxq_status report_hip(const char* who, hipError_t e);
 
+// A launch holds less than 2^32 threads in its grid's first dimension.  Calls
+// that need more give kTooLarge, with nothing enqueued.
+constexpr hipError_t kTooLarge = hipErrorInvalidConfiguration;
+inline bool grid_fits(int64_t workgroups, int threads) { return workgroups < (int64_t{1} << 32) / threads; }
+
 // Runs `enqueue(workspace)` with `bytes` of device memory that stay the
 // stream's own until what it enqueues is done: the split workspace cache
 // (workspace.cpp), or, on a stream being captured, memory of the graph.

@@ -321,6 +321,8 @@ typedef struct mxq_kv_cache {
  * `width` pages, or more of them than lens[s]) are dropped.
  *   k, v    f16|bf16, element (t, h, d) at t * k_token + h * k_head + d
  *   table   i32, row s at s * table_stride, `width` entries; width * block < 2^31
+ * tokens and seqs are at most 2^24.  A call that needs a grid of 2^32 threads is
+ * MXQ_ERR_UNSUPPORTED: with seqs below 2^21 none does.
  */
 mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_token, int64_t k_head,
                          const void* v, int64_t v_token, int64_t v_head, const int32_t* table,
@@ -349,7 +351,9 @@ mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_tok
  * largest p_j times the largest scale of v in the sequence may be left out of
  * the sum over p_j v_j.  Results are the same bits from run to run.  Partial
  * results of a split key axis go to the split workspace (see above); MXQ_ERR_HIP
- * if that cannot be had.
+ * if that cannot be had.  tokens and seqs are at most 2^24.  A call that needs a
+ * grid of 2^32 threads is MXQ_ERR_UNSUPPORTED: with tokens * heads / 16 + seqs *
+ * kv_heads below 2^20 none does.
  */
 mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const mxq_kv_cache* cache,
                          const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,

@@ -10,6 +10,7 @@ from tests.gpu_util import note
 from tests.serve_util import HALF, append_ref, attention_ref, random_pool, rope_ref
 from tests.test_serve_attention import _call as _attention_call
 from tests.test_serve_attention import _check
+from tests.test_serve_rope_kv import _append as _append_call
 
 DEV = "cuda:0"
 
@@ -288,3 +289,27 @@ def test_rope_of_more_tokens_than_a_grid_holds(dim, rot):
         err = np.abs(out[part].double().cpu().numpy() - want)
         # a turn in f32 (2^-22 of the pair's size), rounded once to f16
         assert (err <= np.abs(want) * 2.0 ** -11 + 2.0 ** -25 + np.abs(want).max() * 2.0 ** -21).all(), at
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_a_grid_holds_are_refused():
+    """By an error that says so, before anything is launched; nothing is written."""
+    n = 2 ** 23
+    cache = mxq.KvCache.empty(1, 4, 16, 64, DEV)
+    table, lens = torch.zeros(n, 1, dtype=torch.int32, device=DEV), torch.ones(n, dtype=torch.int32, device=DEV)
+    starts = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    q = torch.ones(1, 4, 64, dtype=torch.float16, device=DEV)
+    out = torch.full_like(q, 7.0)
+    note("refused: too many sequences")
+    with pytest.raises(mxq.MxqError) as e:
+        mxq.mxq_attention(q, cache, table, lens, starts, out)
+    assert e.value.status == mxq.MXQ_ERR_UNSUPPORTED and "split the call" in str(e.value)
+    with pytest.raises(mxq.MxqError) as e:
+        mxq.mxq_kv_append(cache, q, q, table, lens, starts)
+    assert e.value.status == mxq.MXQ_ERR_UNSUPPORTED and "split the call" in str(e.value)
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all()) and int(torch.count_nonzero(cache.k_scale)) == 0
+
+
+def test_append_of_more_sequences_than_a_grid_holds():
+    assert _append_call(tokens=1, seqs=2 ** 23, starts=0x10000) == mxq.MXQ_ERR_UNSUPPORTED
