@@ -47,7 +47,7 @@ mxq_status check_paging(const std::string& f, const mxq::KvPool& pool, const int
     return report(MXQ_ERR_INVALID_ARG, f + ": without starts every sequence has one token (tokens == seqs)");
   if (tokens > (int64_t{1} << 24) || seqs > (int64_t{1} << 24))
     return report(MXQ_ERR_UNSUPPORTED, f + ": tokens and seqs must be at most 2^24");
-  if (width * pool.block > INT32_MAX) return report(MXQ_ERR_UNSUPPORTED, f + ": width * block must be below 2^31");
+  if (width > INT32_MAX / pool.block) return report(MXQ_ERR_UNSUPPORTED, f + ": width * block must be below 2^31");
   if (tokens == 0 || seqs == 0) return MXQ_OK;
   if (!lens || (width > 0 && !table)) return report(MXQ_ERR_INVALID_ARG, f + ": null table or lens");
   if (seqs > 1 && table_stride < width) return report(MXQ_ERR_INVALID_ARG, f + ": table rows overlap (table_stride < width)");
