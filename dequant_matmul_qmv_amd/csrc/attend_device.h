@@ -66,6 +66,11 @@ struct Band {
   }
 };
 constexpr float kLn2 = 0.69314718055994530942f;
+// One over a row's weight; 0 for a row without keys.
+__device__ __forceinline__ float over(float total) { return total > 0.0f || total != total ? 1.0f / total : 0.0f; }
+// A row's parts are kept divided by their weight, and joined by their weights
+// times this: sums of values near f32's largest or smallest stay in its range.
+constexpr float kJoinUnit = 1.0f / kLowLift;
 // Natural log-sum of weights held as 2^kLift times 2^(x - ref).
 __device__ __forceinline__ float log_sum(float ref, float total) { return (ref + log2f(total * kUnlift)) * kLn2; }
 

@@ -147,7 +147,7 @@ template <int DIM, int MT, bool BF16, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ? 1 : 2) void attend_few_kernel(AttendArgs a) {
   constexpr int U = DIM / 64, DB = DIM / 16, kRows = 16 * MT;
   __shared__ float join[WAVES][16][DIM + 4];
-  __shared__ float join_m[WAVES][16], join_l[WAVES][16];
+  __shared__ float join_m[WAVES][16], join_l[WAVES][16], join_vs[WAVES];
   const Part part = find_part<MT>(a, blockIdx.x, -1);
   if (!part.any) return;
   const int hk = a.pool.kv_heads, block = a.pool.block;
@@ -393,9 +393,10 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
       join_m[wave][rho] = m[mt];
       join_l[wave][rho] = weight;
     }
+    if (lane == 0) join_vs[wave] = top_vs;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
-      *reinterpret_cast<f4*>(&join[wave][rho][db * 16 + h * 4]) = acc[mt][db] * top_vs;
+      *reinterpret_cast<f4*>(&join[wave][rho][db * 16 + h * 4]) = acc[mt][db];
     __syncthreads();
     for (int u = threadIdx.x; u < 16 * (DIM / 4); u += 64 * WAVES) {
       const int row = u / (DIM / 4), d = (u - row * (DIM / 4)) * 4, i = mt * 16 + row;
@@ -404,21 +405,20 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) top = fmaxf(top, join_m[w][row]);
         const float ref = top == kNegInf ? 0.0f : top;
-        f4 y = f4{0, 0, 0, 0};
         float total = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-          const float e = __builtin_amdgcn_exp2f(join_m[w][row] - ref);
-          y += *reinterpret_cast<const f4*>(&join[w][row][d]) * e;
-          total += join_l[w][row] * e;
-        }
+        for (int w = 0; w < WAVES; ++w) total += join_l[w][row] * __builtin_amdgcn_exp2f(join_m[w][row] - ref);
+        const float inv = over(total);
+        f4 y = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+          y += *reinterpret_cast<const f4*>(&join[w][row][d]) * (__builtin_amdgcn_exp2f(join_m[w][row] - ref) * inv) * join_vs[w];
         if (alone) {
           const int tok = (row0 + i) / a.group, hq = head * a.group + (row0 + i) - tok * a.group;
           const int64_t at = static_cast<int64_t>(sp.t0 + tok) * a.heads + hq;
-          const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
           uint16_t o[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e] * inv);
+          for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e]);
           *reinterpret_cast<uint2*>(a.out + at * DIM + d) =
               uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
                     static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
@@ -470,9 +470,9 @@ __global__ __launch_bounds__(THREADS) void attend_join_kernel(AttendArgs a) {
     for (int i = 0; i < 4; ++i) {
       if (s0 + i * kTeams >= part.splits) continue;
       const float now = fmaxf(top, ml[i].x), ref = now == kNegInf ? 0.0f : now;
-      const float e0 = __builtin_amdgcn_exp2f(top - ref), e1 = __builtin_amdgcn_exp2f(ml[i].x - ref);
-      y = y * e0 + v[i] * e1;
-      total = total * e0 + ml[i].y * e1;
+      const float e0 = __builtin_amdgcn_exp2f(top - ref), w = ml[i].y * kJoinUnit * __builtin_amdgcn_exp2f(ml[i].x - ref);
+      y = y * e0 + v[i] * w;
+      total = total * e0 + w;
       top = now;
     }
   }
@@ -496,13 +496,13 @@ __global__ __launch_bounds__(THREADS) void attend_join_kernel(AttendArgs a) {
     total += team_l[t] * e;
   }
   const int64_t at = static_cast<int64_t>(tok) * a.heads + hq;
-  const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+  const float inv = over(total);
   uint16_t o[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e] * inv);
   *reinterpret_cast<uint2*>(a.out + at * DIM + d) = uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
                                                           static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
-  if (a.lse && d == 0) a.lse[at] = log_sum(ref, total);
+  if (a.lse && d == 0) a.lse[at] = log_sum(ref, total / kJoinUnit);
 }
 
 namespace {

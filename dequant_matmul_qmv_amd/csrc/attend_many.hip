@@ -395,18 +395,17 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
     }
   }
 
-  const float total = add_xor32(l);
+  const float total = add_xor32(l), inv = over(total);
   if (mine >= rows) return;
   if (a.many_splits == 1) {
     const int64_t at = static_cast<int64_t>(sp.t0 + tok) * a.heads + hq;
-    const float inv = total > 0.0f || total != total ? top_vs / total : 0.0f;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint16_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(acc[db][4 * i + e] * inv);
+        for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(acc[db][4 * i + e] * inv * top_vs);
         *reinterpret_cast<uint2*>(a.out + at * DIM + db * 32 + 8 * i + 4 * h) =
             uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
                   static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
@@ -419,7 +418,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<f4*>(a.many_part + at * DIM + db * 32 + 8 * i + 4 * h) =
-            f4{acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]} * top_vs;
+            f4{acc[db][4 * i], acc[db][4 * i + 1], acc[db][4 * i + 2], acc[db][4 * i + 3]} * inv * top_vs;
     if (h == 0) *reinterpret_cast<float2*>(a.many_ml + at * 2) = float2{m, total};
   }
 }
@@ -462,20 +461,20 @@ __global__ __launch_bounds__(256) void attend_many_join_kernel(AttendArgs a) {
     for (int e = 0; e < 8; ++e) {
       if (s0 + e >= a.many_splits) continue;
       const float now = fmaxf(top, ml[e].x), ref = now == kNegInf ? 0.0f : now;
-      const float e0 = __builtin_amdgcn_exp2f(top - ref), e1 = __builtin_amdgcn_exp2f(ml[e].x - ref);
-      y = y * e0 + v[e] * e1;
-      total = total * e0 + ml[e].y * e1;
+      const float e0 = __builtin_amdgcn_exp2f(top - ref), w = ml[e].y * kJoinUnit * __builtin_amdgcn_exp2f(ml[e].x - ref);
+      y = y * e0 + v[e] * w;
+      total = total * e0 + w;
       top = now;
     }
   }
   const int64_t at = static_cast<int64_t>(tok) * a.heads + hq;
-  const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+  const float inv = over(total);
   uint16_t o[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e] * inv);
   *reinterpret_cast<uint2*>(a.out + at * DIM + d) = uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
                                                           static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
-  if (a.lse && d == 0) a.lse[at] = log_sum(top == kNegInf ? 0.0f : top, total);
+  if (a.lse && d == 0) a.lse[at] = log_sum(top == kNegInf ? 0.0f : top, total / kJoinUnit);
 }
 
 namespace {

@@ -92,7 +92,7 @@ struct KvAppendArgs {
 hipError_t launch_kv_append(const KvAppendArgs& a);
 
 // Attention of new tokens over the cache.  Partial results of a key range, one
-// slot a workgroup: rows of dim f32 sums, then their maxima and weights.
+// slot a workgroup: rows of dim f32 means, then their maxima and weights.
 struct AttendArgs {
   KvPool pool;
   const uint16_t* q;
@@ -110,7 +110,7 @@ struct AttendArgs {
   bool bf16;
   hipStream_t stream;
   // set by the launcher
-  float* part;            // sums [slots, rows, dim]
+  float* part;            // means [slots, rows, dim]
   float* part_ml;         // (maximum, weight) [slots, rows, 2]
   int slots;              // of them
   int target;             // workgroups the few-row work is split for

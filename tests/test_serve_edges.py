@@ -313,3 +313,28 @@ def test_more_sequences_than_a_grid_holds_are_refused():
 
 def test_append_of_more_sequences_than_a_grid_holds():
     assert _append_call(tokens=1, seqs=2 ** 23, starts=0x10000) == mxq.MXQ_ERR_UNSUPPORTED
+
+
+# ---------------------------------------------------------------------------------------- values of any size
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [2.0 ** 118, 2.0 ** -110])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,new", [([900, 40], [1, 1]), ([5000, 300], [1, 1]), ([400, 30], [3, 5]), ([3001], [7]),
+                                      ([700], [700]), ([5001], [80])])
+def test_values_at_the_ends_of_their_range(lens, new, dim, size):
+    """v near the largest and the smallest bf16 numbers, with the key axis in one part and in several."""
+    gen = torch.Generator().manual_seed(len(lens) + dim + new[0])
+    block, blocks = 64, sum(-(-n // 64) for n in lens)
+    pool = list(random_pool(blocks, 1, block, dim, gen))
+    pool[3] *= size
+    tab, at = torch.full((len(lens), -(-max(lens) // block)), -1, dtype=torch.int32), 0
+    for s, n in enumerate(lens):
+        c = -(-n // block)
+        tab[s, :c] = torch.arange(at, at + c)
+        at += c
+    q = torch.randn(sum(new), 4, dim, generator=gen).bfloat16() * 0.1      # flat: the sum of all weights is large
+    ref = attention_ref(q, pool, tab, lens, new, 0, dim ** -0.5)
+    assert np.abs(ref[0]).max() < 3e38
+    note(f"attention v of {size}, {lens} {new}, dim {dim}")
+    out, lse = _attend(q, pool, tab, lens, new)
+    _check(out, lse, ref, f"v of {size}")
