@@ -8,7 +8,6 @@
 namespace mxq {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
-typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 
 // Eight int8 codes as exact f16: each byte, offset to c + 128, becomes the
 // mantissa of 1024 (0x6400 | u), and -1152 leaves c: 5 operations for 4 codes.

@@ -44,10 +44,15 @@ constexpr int kChunk = 64;      // keys a wave takes at a time
 constexpr int kLongRounds = 3;
 constexpr int kMinChunks = 4;   // at least one chunk for each wave of a workgroup
 // Tables of up to this many keys are not split: a workgroup of eight waves takes
-// all keys of its rows, in two rounds at most.  One sequence of 8 kv heads, split
-// and joined / not split: 11.5 / 9.2 us at 777 keys of 64 values (10.3 with four
-// waves), 11.1 / 12.1 us at 128 values; 11.1 / 8.9 us at 512 keys; inside a graph,
-// which then has no workspace to allocate, 20 / 7 .. 13 us.
+// all keys of its rows, in two rounds at most.  8 kv heads, split and joined / not
+// split, in us, a call among others and inside a graph (which then has no
+// workspace to allocate):
+//   1 sequence    64 values, 512 keys 11.3 / 8.8, 20.1 / 6.8; 1024 keys 11.3 / 8.8, 20.7 / 9.2
+//                128 values, 512 keys 11.2 / 8.7, 19.5 / 8.8; 1024 keys 11.2 / 12.0, 18.7 / 12.4
+//   32 sequences  64 values, 1024 keys 14.6 / 9.9, 23.0 / 10.5
+//                128 values, 1024 keys 22.9 / 16.0, 31.1 / 16.8
+// So 128 values, more than 512 keys and few sequences lose 1 us outside a graph
+// and win 6 inside one; all others win both ways.
 constexpr int kLoneKeys = 1024;
 constexpr float kTiny = 1e-30f;
 

@@ -83,7 +83,7 @@ __device__ __forceinline__ u4 load16(const uint16_t* p, bool wide) {
   return u4{d[0], d[1], d[2], d[3]};
 }
 
-// Four codes rescaled: those of `mask` bytes only.
+// Four codes rescaled.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   int c[4];
 #pragma unroll

@@ -314,7 +314,8 @@ typedef struct mxq_kv_cache {
  *           sequence, else fresh,
  *   new codes = clamp(rint(x * (1 / scale)), -127, 127); 0 if scale is 0,
  *   older codes = rint(code * (old scale / scale)), unchanged if that is 1,
- * quotients correctly rounded to f32, products in f32, ties to even.  Other
+ * quotients correctly rounded to f32 (1 / scale at most the largest one),
+ * products in f32, ties to even.  Other
  * codes of the page stay as they are.  k and v must be finite.  Pages that get
  * new tokens must not be shared by two sequences of one call.  New tokens
  * without a place (a table entry outside 0 .. blocks - 1, a position beyond

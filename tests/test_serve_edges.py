@@ -338,3 +338,30 @@ def test_values_at_the_ends_of_their_range(lens, new, dim, size):
     note(f"attention v of {size}, {lens} {new}, dim {dim}")
     out, lse = _attend(q, pool, tab, lens, new)
     _check(out, lse, ref, f"v of {size}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,new", [([300, 200, 90], [1, 1, 1]), ([300, 200, 90], [4, 3, 5]), ([300, 3000, 90], [150, 90, 80])])
+def test_a_bad_query_row_stays_its_own(lens, new, t):
+    """NaN and infinite queries beside others, in one wave and one workgroup: those keep their results."""
+    gen = torch.Generator().manual_seed(70 + sum(new))
+    block, blocks = 32, sum(-(-n // 32) for n in lens)
+    pool = random_pool(blocks, 2, block, 64, gen)
+    tab, at = torch.full((len(lens), -(-max(lens) // block)), -1, dtype=torch.int32), 0
+    for s, n in enumerate(lens):
+        c = -(-n // block)
+        tab[s, :c] = torch.arange(at, at + c)
+        at += c
+    q = torch.randn(sum(new), 8, 64, generator=gen).to(HALF[t])
+    bad = torch.rand(sum(new), 8, generator=gen) < 0.2
+    bad[0, 0], bad[-1, -1] = True, False
+    ref = attention_ref(q, pool, tab, lens, new, 0, 0.125)
+    spoilt = q.clone()
+    spoilt[bad] = torch.where(torch.rand(int(bad.sum()), 64, generator=gen) < 0.5, torch.nan, torch.inf).to(q.dtype)
+    note(f"attention with bad rows {new} {t}")
+    out, lse = _attend(spoilt, pool, tab, lens, new)
+    assert bool(torch.isnan(out.cpu()[bad]).all()) and bool(torch.isnan(lse.cpu()[bad]).all())
+    good = (~bad).numpy()
+    want, wlse, off, loff = ref
+    _check(out.cpu()[~bad], lse.cpu()[~bad], (want[good], wlse[good], off[good], loff[good]), "beside bad rows")
