@@ -24,12 +24,15 @@
 //
 // 32 rows a wave and 128 a workgroup: 256 rows in 8 waves stage half as often a
 // row, but their barrier costs more (six chunks of prompts, 128 values a head:
-// 353 against 335 us).  Measured: a prompt of 4001 tokens, 32 heads of 64 values,
-// 119 us (551 TFLOP/s); six chunks of up to 1024 tokens over up to 8192 keys, 128
-// values, window 4096, 335 us (565 TFLOP/s).  Without the staging they take 116 and
-// 264 us, without the exponentials 130 and 304: the vector ALU (of which the
-// codes' conversion is a fifth at 128 values) issues in 55 % (128 values) and 75 %
-// (64) of the cycles, the matrix cores in 25 .. 30 %.
+// 353 against 335 us).  No vector register is spilled; 34 .. 38 scalar ones are,
+// into lanes, and some are read back in the loop over stages.  Measured: a prompt
+// of 4001 tokens, 32 heads of 64 values, 120 us (546 TFLOP/s; 125 .. 140 on other
+// cards); six chunks of up to 1024 tokens over up to 8192 keys, 128 values, window
+// 4096, 335 us (565 TFLOP/s).  On a card where they take 142 and 335: without the
+// staging 113 and 255, without the exponentials 131 and 317, without the search
+// for small weights 123 and 300.  The vector ALU (of which the codes' conversion
+// is a fifth at 128 values) issues in 55 % (128 values) and 75 % (64) of the
+// cycles, the matrix cores in 25 .. 30 %.
 #include <cfloat>
 #include <climits>
 

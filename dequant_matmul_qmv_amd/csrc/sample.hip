@@ -38,9 +38,10 @@
 //           the rows are many) finds the end in
 //           the list and draws.  Where a bin has more tokens than a list (many
 //           equal logits) it searches the row itself
-// Measured: one row of 128256, top-k 40 and top-p, 14 us (draw 9, stats 2.7), or
-// 35 .. 37 with a prefix of thousands; 192 rows of mixed settings 118 us (stats 23,
-// draw 33, bins 22, wide 29, the draw after it 13); 17 rows of 32003 by min-p 20 us.
+// Measured: one row of 128256, top-k 40 and top-p, 13.5 .. 15.5 us by card (draw
+// 9, stats 2.9), or 36 .. 38 with a prefix of thousands; 192 rows of mixed settings
+// 118 us (stats 24, draw 33, bins 22, wide 29, the draw after it 13); 17 rows of
+// 32003 by min-p 20 us (draw 16).
 // One workgroup a row for everything took 323, 528 and 40 us.
 #include <cfloat>
 
