@@ -186,6 +186,8 @@ __device__ __forceinline__ double uniform_of(const SampleArgs& a, int row) {
 
 // A token's place in the descending order: its key, equals by index.
 __device__ __forceinline__ u64 word_of(uint32_t key, int i) { return (static_cast<u64>(key) << 20) | (0xFFFFFu - static_cast<uint32_t>(i)); }
+// The smallest word of a key.
+__device__ __forceinline__ u64 first_word(uint32_t key) { return static_cast<u64>(key) << 20; }
 __device__ __forceinline__ uint32_t key_in(u64 word) { return static_cast<uint32_t>(word >> 20); }
 __device__ __forceinline__ int index_in(u64 word) { return static_cast<int>(0xFFFFFu - (static_cast<uint32_t>(word) & 0xFFFFFu)); }
 
@@ -541,7 +543,7 @@ __device__ __forceinline__ void finish_row(const SampleArgs& a, Shared& sh, int 
   if (tid == 0) sh.listed = plan.state == kSearch ? kList + 1 : __hip_atomic_load(&a.plans[row].listed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   int listed = static_cast<int>(sh.listed);
-  u64 end = 0;
+  u64 end = first_word(plan.low);
   if (listed <= kList) {
     for (int i = tid; i < listed; i += kDrawThreads) {
       const u64 word = list[i];
@@ -555,7 +557,7 @@ __device__ __forceinline__ void finish_row(const SampleArgs& a, Shared& sh, int 
         mass = 0;
         return bins.of(key_in(word)) == where.k_bin;
       };
-      end = select_word(sh, item, listed, false, rule.k, where.k_count);
+      end = max(end, select_word(sh, item, listed, false, rule.k, where.k_count));
       u64 held = 0;
       for (int i = tid; i < listed; i += kDrawThreads)
         held += sh.word[i] >= end && bins.of(key_in(sh.word[i])) == where.k_bin ? sh.mass[i] : 0;
@@ -582,7 +584,10 @@ __device__ __forceinline__ void finish_row(const SampleArgs& a, Shared& sh, int 
       return true;
     };
     listed = 0;
-    if (limit_k) end = from = select_word(sh, item, n, false, rule.k, 0);
+    if (limit_k) {
+      from = select_word(sh, item, n, false, rule.k, 0);
+      end = max(end, from);
+    }
     if (limit_p) {
       double whole = plan.total;
       if (limit_k) {
@@ -856,7 +861,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
   }
   const int listed = static_cast<int>(sh.listed);
   const double least = floor ? static_cast<double>(rule.min_p) * kFix : 0.0;  // of a kept token's integer weight
-  u64 end = 0;
+  u64 end = first_word(low);  // of what is kept; all of the list where nothing limits it further
   if (small) {
     for (int i = tid; i < listed; i += kDrawThreads) sh.mass[i] = w.fixed(key_in(sh.word[i]));
     __syncthreads();
@@ -932,7 +937,7 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleArgs a)
         mass = sh.mass[i];
         return true;
       };
-      if (limit_k && rule.k < listed) end = select_word(sh, item, listed, false, rule.k, 0);
+      if (limit_k && rule.k < listed) end = max(end, select_word(sh, item, listed, false, rule.k, 0));
       if (limit_p) {
         if (limit_k) {
           held = 0;

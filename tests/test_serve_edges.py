@@ -11,6 +11,7 @@ from tests.serve_util import HALF, append_ref, attention_ref, random_pool, rope_
 from tests.test_serve_attention import _call as _attention_call
 from tests.test_serve_attention import _check
 from tests.test_serve_rope_kv import _append as _append_call
+from tests.test_serve_sample import _check as _check_draw
 
 DEV = "cuda:0"
 
@@ -365,3 +366,23 @@ def test_a_bad_query_row_stays_its_own(lens, new, t):
     good = (~bad).numpy()
     want, wlse, off, loff = ref
     _check(out.cpu()[~bad], lse.cpu()[~bad], (want[good], wlse[good], off[good], loff[good]), "beside bad rows")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("peaks", [40, 256, 257, 300, 1500, 2048, 2049])
+def test_top_k_of_exactly_the_peaks(peaks, t):
+    """One large token in each of `peaks` stretches of 64, the rest well below but with weight; top_k is their number,
+    one less, one more: where all that was listed is kept, the rest must not be."""
+    gen = torch.Generator().manual_seed(80 + peaks)
+    vocab = 64 * 2100 - 5
+    x = torch.rand(3, vocab, generator=gen)
+    for r in range(3):
+        at = torch.randperm(vocab // 64, generator=gen)[:peaks] * 64 + torch.randint(0, 64, (peaks,), generator=gen)
+        x[r, at] = 4 + 2 * torch.rand(peaks, generator=gen)
+    x = x.to({**HALF, "f32": torch.float32}[t])
+    for k in (peaks - 1, peaks, peaks + 1):
+        for p, m in ((1.0, 0.0), (0.9, 0.0), (1.0, 0.05)):
+            for v in (0.0, 0.11, 0.5, 0.77, 0.999):
+                u = torch.full((3,), v)
+                _check_draw(x, u, 1.3, k, p, m, f"peaks {peaks} k {k} p {p} min_p {m} u {v} {t}")
