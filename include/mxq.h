@@ -348,9 +348,9 @@ mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_tok
  * Rows of q and out that no sequence covers are neither read nor written.
  * Products of q and codes are exact, sums, maxima and weights f32, the
  * probabilities f16 relative to their row's largest (a bf16 q's smallest values
- * are rounded at 2^-25 of its row's largest).  A value below 2^-148 of the row's
- * largest p_j times the largest scale of v in the sequence may be left out of
- * the sum over p_j v_j.  Results are the same bits from run to run.  Partial
+ * are rounded at 2^-25 of its row's largest).  A key may be left out of the sum
+ * over p_j v_j if its p_j is below 2^-126 of the row's largest, or p_j times its
+ * scale of v below 2^-148 of that times the sequence's largest.  Results are the same bits from run to run.  Partial
  * results of a split key axis go to the split workspace (see above); MXQ_ERR_HIP
  * if that cannot be had.  tokens and seqs are at most 2^24.  A call that needs a
  * grid of 2^32 threads is MXQ_ERR_UNSUPPORTED: with tokens * heads / 16 + seqs *
