@@ -10,9 +10,10 @@
 // Which token a border falls on is a whole number, so weights are taken in f64.
 // Where threads add in no fixed order they add integers of 2^-43: such sums are
 // the same in any order, and a border is off by 2^-44 a token of a total that is
-// at least 1.  Other sums are f64 in a fixed order.  A token below 2^-44 of the
-// largest has the integer 0: it can neither be drawn nor move a border, and is
-// left out everywhere.
+// at least 1.  A token below 2^-44 of the largest has the integer 0: where a row
+// has limits it can neither be drawn nor move a border, and is left out.  Rows
+// without limits add pieces of 512 tokens as integers, the tokens of one piece in
+// f64, in a fixed order.
 //
 // The descending order is that of one number a token, its word: the logit as an
 // ordered 32-bit key, then the index, the lower the larger.  Words differ, so a

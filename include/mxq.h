@@ -350,11 +350,11 @@ mxq_status mxq_kv_append(const mxq_kv_cache* cache, const void* k, int64_t k_tok
  * probabilities f16 relative to their row's largest (a bf16 q's smallest values
  * are rounded at 2^-25 of its row's largest).  A key may be left out of the sum
  * over p_j v_j if its p_j is below 2^-126 of the row's largest, or p_j times its
- * scale of v below 2^-148 of that times the sequence's largest.  Results are the same bits from run to run.  Partial
- * results of a split key axis go to the split workspace (see above); MXQ_ERR_HIP
- * if that cannot be had.  tokens and seqs are at most 2^24.  A call that needs a
- * grid of 2^32 threads is MXQ_ERR_UNSUPPORTED: with tokens * heads / 16 + seqs *
- * kv_heads below 2^20 none does.
+ * scale of v below 2^-148 of that times the sequence's largest.  Results are the
+ * same bits from run to run.  Partial results of a split key axis go to the split
+ * workspace (see above); MXQ_ERR_HIP if that cannot be had.  tokens and seqs are
+ * at most 2^24.  A call that needs a grid of 2^32 threads is MXQ_ERR_UNSUPPORTED:
+ * with tokens * heads / 16 + seqs * kv_heads below 2^20 none does.
  */
 mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const mxq_kv_cache* cache,
                          const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
