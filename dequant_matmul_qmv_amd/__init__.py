@@ -7,8 +7,10 @@ launch), ``mxq_qmm`` (prefill), ``mxq_linear`` (either, plus an output bias),
 ``mxq_linear_a8`` (int8 activations, quantized per row in the kernel),
 ``mxq_dequant`` (bit-exact standalone dequant) and ``mxq_pack`` (host packer),
 the serving operators around the projections, ``mxq_rope`` (rotary positions),
-``KvCache`` and ``mxq_kv_append`` (an 8-bit paged key/value cache),
-``mxq_attention`` (over that cache), ``mxq_sample`` (the next token from logits),
+``mxq_norm_rope`` (with norms of each head, on several axes), ``KvCache``, ``KvCache4``
+and ``mxq_kv_append`` (paged key/value caches of 8 and 4 bits), ``mxq_rope_append`` (norms,
+rotation and append in one launch), ``mxq_attention`` (over either cache), ``mxq_sample``
+(the next token from logits),
 plus diagnostics (``mxq_describe``, ``mxq_describe_grouped``) and the split
 workspace controls (``mxq_release_workspaces``, ``mxq_workspace_bytes``).
 """
@@ -41,7 +43,7 @@ from ._lib import (  # noqa: F401
 )
 
 # the serving operators, bound on first use: their module needs torch, which the rest imports inside its calls
-_SERVE = ("KvCache", "mxq_attention", "mxq_kv_append", "mxq_rope", "mxq_sample")
+_SERVE = ("KvCache", "KvCache4", "mxq_attention", "mxq_kv_append", "mxq_norm_rope", "mxq_rope", "mxq_rope_append", "mxq_sample")
 
 
 def __getattr__(name):

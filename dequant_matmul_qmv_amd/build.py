@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxq.so")
 SOURCES = ["api.cpp", "workspace.cpp", "qmv.hip", "qmm.hip", "qsm.hip", "dequant.hip", "qmm_a8.hip", "probe.hip", "static_scratch.hip",
-           "serve_api.cpp", "rope.hip", "kv_append.hip", "attend_few.hip", "attend_many.hip", "sample.hip"]
+           "serve_api.cpp", "rope.hip", "kv_append.hip", "attend_few.hip", "attend_many.hip", "sample.hip",
+           "serve4_api.cpp", "norm_rope.hip", "rope_append.hip", "attend4_few.hip", "attend4_many.hip"]
 ARCH = "gfx950"
 
 

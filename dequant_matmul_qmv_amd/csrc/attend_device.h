@@ -1,4 +1,4 @@
-// Device helpers shared by the attention kernels over the 8-bit cache.
+// Device helpers shared by the attention kernels over the paged caches.
 #pragma once
 
 #include "lanes_device.h"
@@ -112,7 +112,8 @@ __device__ __forceinline__ float absmax8_bf16(u4 v) {
 struct SeqSpan {
   int t0, n, len;
 };
-__device__ __forceinline__ SeqSpan seq_span(const AttendArgs& a, int s) {
+template <typename Args>
+__device__ __forceinline__ SeqSpan seq_span(const Args& a, int s) {
   SeqSpan r;
   if (a.starts == nullptr) {
     r.t0 = s;
@@ -127,6 +128,7 @@ __device__ __forceinline__ SeqSpan seq_span(const AttendArgs& a, int s) {
 
 // The first key that a token at `pos` sees (negative positions see none; a
 // window up to 2^31 - 1 must not wrap there).
-__device__ __forceinline__ int first_seen(const AttendArgs& a, int pos) { return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0; }
+template <typename Args>
+__device__ __forceinline__ int first_seen(const Args& a, int pos) { return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0; }
 
 }  // namespace mxq

@@ -36,13 +36,13 @@
 #include <cfloat>
 #include <climits>
 
-#include "attend_device.h"
+#include "attend_split.h"
 
 namespace mxq {
 
 namespace {
 
-constexpr int kManyThreads = 256, kManyRows = 128, kStage = 64;
+constexpr int kManyThreads = 256, kStage = 64;
 constexpr float kTinyScale = 0x1p-100f;
 constexpr float kSlack = 1.75f;  // weights reach 2^(kLift + kSlack), below f16's largest
 
@@ -80,35 +80,7 @@ __device__ __forceinline__ u4 again(u4 w) {
   return w;
 }
 
-// Rows a sequence gives to this kernel, in tiles.
-__device__ __forceinline__ int tiles_of(const AttendArgs& a, int s) {
-  if (s >= a.seqs) return 0;
-  const SeqSpan q = seq_span(a, s);
-  const int64_t rows = static_cast<int64_t>(q.n) * a.group;
-  return rows > a.few_rows ? static_cast<int>((rows + kManyRows - 1) / kManyRows) : 0;
-}
-
 }  // namespace
-
-// (sequence, tile within it) of tile `index`, or with index < 0 the first tile
-// of sequence `seq` in `first`.  Whole waves.
-__device__ bool find_tile(const AttendArgs& a, int index, int& seq, int& first) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
-    const int count = tiles_of(a, s0 + lane);
-    const int sum = wave_scan(count);
-    const unsigned long long hit = index >= 0 ? __ballot(before + sum > index) : (seq < s0 + 64 ? 1ull << (seq - s0) : 0);
-    if (hit != 0) {
-      const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
-      seq = s0 + src;
-      first = before + __builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(count, src);
-      return true;
-    }
-    before += last_lane(sum);
-  }
-  return false;
-}
 
 template <int DIM, bool BF16>
 __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs a) {
@@ -426,60 +398,6 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   }
 }
 
-// Joins a row's parts where the key axis was split: a workgroup for each token
-// and as many query heads as it has groups of DIM / 4 lanes, one of them a group.
-// Eight parts are read at a time (24 parts of 51 tokens over 6204 keys, the
-// whole call: 33 us one by one; two parts of 1281 tokens of 16 heads: 16 us with
-// a workgroup a row).
-template <int DIM, bool BF16>
-__global__ __launch_bounds__(256) void attend_many_join_kernel(AttendArgs a) {
-  constexpr int kLanes = DIM / 4, kTeams = 256 / kLanes;
-  const int tok = blockIdx.x, hk = a.pool.kv_heads;
-  int lo = 0, hi = a.seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.starts[mid] <= tok) lo = mid; else hi = mid;
-  }
-  int seq = lo, first = 0;
-  const SeqSpan sp = seq_span(a, seq);
-  if (tok < sp.t0 || tok >= sp.t0 + sp.n || static_cast<int64_t>(sp.n) * a.group <= a.few_rows) return;
-  find_tile(a, -1, seq, first);
-  const int team = threadIdx.x / kLanes, d = (threadIdx.x - team * kLanes) * 4, hq = blockIdx.y * kTeams + team;
-  if (hq >= a.heads) return;
-  const int head = hq / a.group, i = (tok - sp.t0) * a.group + hq - head * a.group;
-  const int64_t tile = first + i / kManyRows;
-  float top = kNegInf, total = 0.0f;
-  f4 y = f4{0, 0, 0, 0};
-  for (int s0 = 0; s0 < a.many_splits; s0 += 8) {
-    float2 ml[8];
-    f4 v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int s = min(s0 + e, a.many_splits - 1);
-      const int64_t at = min((tile * a.many_splits + s) * hk + head, static_cast<int64_t>(a.many_units) - 1) * kManyRows + i % kManyRows;
-      ml[e] = *reinterpret_cast<const float2*>(a.many_ml + at * 2);
-      v[e] = *reinterpret_cast<const f4*>(a.many_part + at * DIM + d);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (s0 + e >= a.many_splits) continue;
-      const float now = fmaxf(top, ml[e].x), ref = now == kNegInf ? 0.0f : now;
-      const float e0 = __builtin_amdgcn_exp2f(top - ref), w = ml[e].y * kJoinUnit * __builtin_amdgcn_exp2f(ml[e].x - ref);
-      y = y * e0 + v[e] * w;
-      total = total * e0 + w;
-      top = now;
-    }
-  }
-  const int64_t at = static_cast<int64_t>(tok) * a.heads + hq;
-  const float inv = over(total);
-  uint16_t o[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e] * inv);
-  *reinterpret_cast<uint2*>(a.out + at * DIM + d) = uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
-                                                          static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
-  if (a.lse && d == 0) a.lse[at] = log_sum(top == kNegInf ? 0.0f : top, total / kJoinUnit);
-}
-
 namespace {
 
 template <int DIM, bool BF16>
@@ -492,23 +410,12 @@ hipError_t launch_many_of(const AttendArgs& a, unsigned grid) {
   hipError_t le = hipGetLastError();
   if (le != hipSuccess || a.many_splits == 1) return le;
   constexpr int kHeads = 256 / (DIM / 4);
-  hipLaunchKernelGGL((attend_many_join_kernel<DIM, BF16>), dim3(static_cast<unsigned>(a.tokens), static_cast<unsigned>((a.heads + kHeads - 1) / kHeads)),
+  hipLaunchKernelGGL((attend_many_join_kernel<DIM, BF16, AttendArgs>), dim3(static_cast<unsigned>(a.tokens), static_cast<unsigned>((a.heads + kHeads - 1) / kHeads)),
                      dim3(256), 0, a.stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
-
-int64_t many_tiles(const AttendArgs& a) {
-  const int64_t rows = static_cast<int64_t>(a.tokens) * a.group;
-  // every sequence of this kernel has more than few_rows rows, and at most one partial tile
-  const int64_t seqs = a.few_rows < 1 ? a.seqs : rows / a.few_rows;
-  return rows / kManyRows + (seqs < a.seqs ? seqs : a.seqs);
-}
-
-size_t many_part_bytes(const AttendArgs& a) {
-  return a.many_splits == 1 ? 0 : static_cast<size_t>(many_tiles(a)) * a.pool.kv_heads * a.many_splits * kManyRows * (a.pool.dim + 2) * 4;
-}
 
 hipError_t launch_many(const AttendArgs& given, float* ws) {
   AttendArgs a = given;

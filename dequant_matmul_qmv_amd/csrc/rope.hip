@@ -10,8 +10,7 @@
 // Bound: HBM, q and k read once and written once.  One workgroup holds one
 // token, computes its rot / 2 cosines and sines once into LDS (every head
 // shares them), and walks the heads 16 bytes a lane.
-#include "mxq_device.h"
-#include "serve_internal.h"
+#include "turn_device.h"
 
 namespace mxq {
 
@@ -19,26 +18,6 @@ namespace {
 
 constexpr int kMaxRot = 256;
 constexpr double kInvTwoPi = 0.15915494309189533577;
-
-template <bool BF16>
-__device__ __forceinline__ void widen8(u4 v, float (&f)[8]) {
-  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = sb_to_f32<BF16>(static_cast<uint16_t>(d[i]));
-    f[2 * i + 1] = sb_to_f32<BF16>(static_cast<uint16_t>(d[i] >> 16));
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ u4 narrow8(const float (&f)[8]) {
-  uint32_t d[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    d[i] = static_cast<uint32_t>(f32_to_act_bits<BF16>(f[2 * i])) |
-           (static_cast<uint32_t>(f32_to_act_bits<BF16>(f[2 * i + 1])) << 16);
-  return u4{d[0], d[1], d[2], d[3]};
-}
 
 // Cosine and sine of a whole angle, for this token's pairs.
 __device__ __forceinline__ void fill_turns(const float* inv_freq, int pos, int half, float* cs, float* sn) {

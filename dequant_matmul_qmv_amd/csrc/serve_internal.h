@@ -64,6 +64,31 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs& a);
 
+// Norms and turns of heads: a weight for q and one for k (null: no norm), the
+// pairs' frequencies and the axis of positions that each turns by.
+struct TurnArgs {
+  const float* inv_freq;
+  const int32_t* positions;  // [axes, tokens]; null: a token's place in its sequence
+  int64_t axis_stride;
+  const int32_t* axis;       // [rot / 2]; null: axis 0
+  int axes, rot;
+  bool interleaved;
+  const void* weight[2];     // of q, of k
+  bool weight_f32;           // else of the values' type
+  double eps;
+};
+struct NormRopeArgs {
+  RopeSide side[2];  // q, k
+  TurnArgs turn;
+  int64_t tokens;
+  int dim;
+  bool bf16;
+  hipStream_t stream;
+  // set by the launcher
+  int batch;         // tokens of a workgroup
+};
+hipError_t launch_norm_rope(const NormRopeArgs& a);
+
 // The paged cache: k codes [blocks, kv_heads, block, dim], v codes [blocks,
 // kv_heads, dim, block], scales [blocks, kv_heads].
 struct KvPool {
@@ -71,6 +96,16 @@ struct KvPool {
   int8_t* v;
   float* k_scale;
   float* v_scale;
+  int64_t blocks;
+  int kv_heads, block, dim;
+};
+// The cache of 4 bits: k words [blocks, kv_heads, block, dim / 8], v words
+// [blocks, kv_heads, block / 8, dim], scale words [blocks, kv_heads, block].
+struct KvPool4 {
+  uint32_t* k;
+  uint32_t* v;
+  uint16_t* k_scale;
+  uint16_t* v_scale;
   int64_t blocks;
   int kv_heads, block, dim;
 };
@@ -91,10 +126,38 @@ struct KvAppendArgs {
 };
 hipError_t launch_kv_append(const KvAppendArgs& a);
 
+// The append that norms and rotates keys on the way, and queries beside them.
+template <typename Pool>
+struct RopeAppendArgsOf {
+  Pool pool;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t k_token, k_head, v_token, v_head;
+  const int32_t* table;
+  int64_t table_stride;
+  int width;
+  const int32_t* lens;
+  const int32_t* starts;  // null: one token for each sequence
+  int tokens, seqs;
+  bool bf16;
+  bool wide;              // rows of k and v are 16-byte aligned
+  hipStream_t stream;
+  RopeSide q;             // heads 0: none
+  bool q_wide;            // q's rows, in and out, are 16-byte aligned
+  TurnArgs turn;
+  // set by the launcher
+  int pages, units;       // workgroups of pages (8 bits), of groups of 8 tokens
+};
+using RopeAppendArgs = RopeAppendArgsOf<KvPool>;
+using RopeAppend4Args = RopeAppendArgsOf<KvPool4>;
+hipError_t launch_rope_append(const RopeAppendArgs& a);
+hipError_t launch_rope_append4(const RopeAppend4Args& a);
+
 // Attention of new tokens over the cache.  Partial results of a key range, one
 // slot a workgroup: rows of dim f32 means, then their maxima and weights.
-struct AttendArgs {
-  KvPool pool;
+template <typename Pool>
+struct AttendArgsOf {
+  Pool pool;
   const uint16_t* q;
   int64_t q_token, q_head;
   uint16_t* out;          // [tokens, heads, dim]
@@ -122,12 +185,14 @@ struct AttendArgs {
   int many_splits;        // parts of its key axis
   int many_units;         // workgroups
 };
-// The many-row kernel (attend_many.hip): its tiles at most, the bytes of its
-// partial results, its launch (with the second one that joins them).
-int64_t many_tiles(const AttendArgs& a);
-size_t many_part_bytes(const AttendArgs& a);
+using AttendArgs = AttendArgsOf<KvPool>;
+using Attend4Args = AttendArgsOf<KvPool4>;
+// The many-row kernels (attend_many.hip, attend4_many.hip), with the second
+// launch that joins their parts.
 hipError_t launch_many(const AttendArgs& a, float* ws);
+hipError_t launch_many(const Attend4Args& a, float* ws);
 hipError_t launch_attend(const AttendArgs& a, const DeviceInfo& dev);
+hipError_t launch_attend4(const Attend4Args& a, const DeviceInfo& dev);
 
 // What sampling's kernels leave of a row for the later ones.
 struct SamplePlan {

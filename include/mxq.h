@@ -362,6 +362,119 @@ mxq_status mxq_attention(const void* q, int64_t q_token, int64_t q_head, const m
                          float scale, void* out, float* lse, mxq_dtype dtype, void* stream);
 
 /*
+ * How heads are normed and rotated (a host structure, read during the call):
+ *   y_d = x_d * r * w_d, r = 1 / sqrt(sum x^2 / dim + eps), of q where q_weight is
+ *         given and of k where k_weight is, over the whole head;
+ * then pair i < rot / 2 turns as in mxq_rope, by positions[a][t] * inv_freq[i], a the
+ * axis of the pair (text has one; frames have time, height and width).  The mean of
+ * squares, r, the angle, its cosine and its sine are taken in f64 and rounded to f32
+ * once each; products and sums after them are f32 operations of their own, and the
+ * result is rounded once to the storage type.  Angles are below 2^50.
+ */
+typedef struct mxq_rotation {
+  const float* inv_freq;      /* [rot / 2] */
+  const int32_t* positions;   /* [axes, tokens], row a at a * position_stride */
+  int64_t position_stride;
+  const int32_t* axis;        /* [rot / 2], the axis of each pair (counted as the nearest of 0 .. axes - 1 where it is none), or null: axis 0 */
+  int32_t axes;               /* 1 .. 2^16 */
+  int32_t rot;                /* even, 0 .. dim */
+  int32_t interleaved;        /* pairs (x[2i], x[2i+1]), else (x[i], x[rot/2 + i]) */
+  mxq_dtype weight_dtype;     /* MXQ_F32, or the type of q and k */
+  const void* q_weight;       /* [dim], or null: no norm */
+  const void* k_weight;
+  double eps;                 /* >= 0, finite */
+} mxq_rotation;
+
+/*
+ * mxq_norm_rope -- q and k normed head by head and rotated in one pass.
+ *
+ * q, k, their outputs, tokens, heads, kv_heads and dim as in mxq_rope (dim at most
+ * 256; outputs may be the inputs themselves); positions must be given where rot > 0.
+ * Rows that are 16-byte aligned with dim and rot multiples of 16 run on wider
+ * accesses.  rot == 0: norms alone.
+ */
+mxq_status mxq_norm_rope(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                         int64_t k_head, void* q_out, int64_t q_out_token, int64_t q_out_head, void* k_out,
+                         int64_t k_out_token, int64_t k_out_head, const mxq_rotation* rotation, int64_t tokens,
+                         int heads, int kv_heads, int dim, mxq_dtype dtype, void* stream);
+
+/*
+ * A paged key/value cache held in 4 bits.  Each token and kv head has a scale and a
+ * zero point for its key and for its value: a code c stands for (c - zero) * scale.
+ *   k       u32 [blocks, kv_heads, block, dim / 8]   8 neighbouring values of a token a word
+ *   v       u32 [blocks, kv_heads, block / 8, dim]   one value of 8 neighbouring tokens a word
+ *   k_scale, v_scale  u16 [blocks, kv_heads, block]
+ * Field j of a word is bits 4j .. 4j + 3.  A scale word is an f16 number, not negative
+ * and at most 4064, whose lowest 4 bits are replaced by the zero point: 7 significant
+ * bits are left for the scale (multiples of 2^-20 below f16's normal range), so that
+ * every value is exact in f16.  block in {16, 32, 64, 128}, dim in {64, 128}; all four
+ * 16-byte aligned.  A sequence's tokens j * block .. are in page table[s][j].
+ */
+typedef struct mxq_kv_cache4 {
+  uint32_t* k;
+  uint32_t* v;
+  uint16_t* k_scale;
+  uint16_t* v_scale;
+  int64_t blocks;
+  int32_t kv_heads;
+  int32_t block;
+  int32_t dim;
+} mxq_kv_cache4;
+
+/*
+ * mxq_rope_append -- new keys normed, rotated and quantized into the 8-bit cache,
+ * new values quantized beside them, queries normed and rotated into q_out: what
+ * mxq_norm_rope and mxq_kv_append do one after the other, with the same codes, in
+ * one launch and without the turned keys in memory.
+ *
+ * Sequences, their new rows, table and lens, and what becomes of new tokens without a
+ * place, as in mxq_kv_append.  A null `positions` stands for each row's place in its
+ * sequence (lens[s] minus the number of its new rows from it on); it may be negative
+ * where there are more new rows than tokens.  Every row that a sequence covers gets
+ * its q_out, with or without a place; others are neither read nor written.
+ *   q, q_out  as in mxq_rope; heads a multiple of the cache's kv_heads, or 0 (q and
+ *             q_out may then be null); q_out may be q
+ *   k, v      as in mxq_kv_append; k must be finite after its norm
+ */
+mxq_status mxq_rope_append(const mxq_kv_cache* cache, const void* q, int64_t q_token, int64_t q_head, void* q_out,
+                           int64_t q_out_token, int64_t q_out_head, const void* k, int64_t k_token, int64_t k_head,
+                           const void* v, int64_t v_token, int64_t v_head, const mxq_rotation* rotation,
+                           const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
+                           const int32_t* starts, int64_t tokens, int64_t seqs, int heads, mxq_dtype dtype,
+                           void* stream);
+
+/*
+ * mxq_rope_append4 -- the same into the 4-bit cache.  Of each new token, kv head, and
+ * key (rotated, in its storage type) or value, with lo = min(0, min x), hi = max(0, max x):
+ *   scale = (hi - lo) / 15 up to the next number that a scale word holds, at most 4064,
+ *   zero = rint(-lo * (1 / scale)), at most 15,
+ *   code = clamp(rint(x * (1 / scale)) + zero, 0, 15); scale, zero and codes are 0 where hi = lo,
+ * the range and its fifteenth in f64, 1 / scale correctly rounded to f32, products in
+ * f32, ties to even.  Values beyond 15 * 4064 of zero saturate.  Codes of other tokens
+ * stay as they are.  `rotation` may be null: keys as they are (then heads must be 0).
+ */
+mxq_status mxq_rope_append4(const mxq_kv_cache4* cache, const void* q, int64_t q_token, int64_t q_head, void* q_out,
+                            int64_t q_out_token, int64_t q_out_head, const void* k, int64_t k_token, int64_t k_head,
+                            const void* v, int64_t v_token, int64_t v_head, const mxq_rotation* rotation,
+                            const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
+                            const int32_t* starts, int64_t tokens, int64_t seqs, int heads, mxq_dtype dtype,
+                            void* stream);
+
+/*
+ * mxq_attention4 -- mxq_attention over the 4-bit cache.
+ *
+ * The same sum, masks, sequences, arguments, limits and errors.  Keys and values are
+ * exact in f16 and so are f16 queries (a bf16 q's smallest values are rounded at 2^-25
+ * of its row's largest); sums, maxima and weights are f32.  The probabilities are f16
+ * relative to their row's largest: to 2^-11 of their value, or 2^-39 of that largest
+ * where they are below 2^-28 of it.  Scores and v must be finite.
+ */
+mxq_status mxq_attention4(const void* q, int64_t q_token, int64_t q_head, const mxq_kv_cache4* cache,
+                          const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
+                          const int32_t* starts, int64_t tokens, int64_t seqs, int heads, int64_t window,
+                          float scale, void* out, float* lse, mxq_dtype dtype, void* stream);
+
+/*
  * The settings of mxq_sample: device arrays of one value a row, or (null) the
  * value for all rows.
  */
