@@ -3,9 +3,10 @@ through in one call, then each step feeds every sequence its last token, from a 
 
 Per layer: one fused q/k/v projection (mxq_linear), rotary positions on views of it (mxq_rope, in place), the new
 keys and values into the 8-bit paged cache (mxq_kv_append), attention over it (mxq_attention), the output projection
-and a gated MLP; then lm_head and the next token's draw (mxq_sample).
+and a gated MLP; then lm_head and the next token's draw (mxq_sample).  With norms of each head's queries and keys, the
+norms, the rotation and the append are one call (mxq_rope_append); the cache may be held in 4 bits (KvCache4).
 
-    python examples/generate.py [--steps 32] [--graph]
+    python examples/generate.py [--steps 32] [--graph] [--norms] [--bits 4]
 """
 
 import argparse
@@ -38,7 +39,8 @@ def norm(x):
 
 
 class Decoder:
-    def __init__(self, layers=2, hidden=512, heads=8, kv_heads=2, dim=64, ffn=1024, vocab=4099, pages=64, block=16, seed=0):
+    def __init__(self, layers=2, hidden=512, heads=8, kv_heads=2, dim=64, ffn=1024, vocab=4099, pages=64, block=16, seed=0,
+                 norms=False, bits=8):
         gen = torch.Generator().manual_seed(seed)
         self.heads, self.kv_heads, self.dim, self.ffn, self.block = heads, kv_heads, dim, ffn, block
         self.embed = torch.randn(vocab, hidden, generator=gen).half().to(DEV)
@@ -46,19 +48,26 @@ class Decoder:
                         Linear(2 * ffn, hidden, gen), Linear(hidden, ffn, gen)) for _ in range(layers)]
         self.head = Linear(vocab, hidden, gen)
         self.inv_freq = (500000.0 ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)).float().to(DEV)
-        self.caches = [mxq.KvCache.empty(pages, kv_heads, block, dim, DEV) for _ in range(layers)]
+        self.norms = None
+        if norms:
+            self.norms = [[(1 + 0.2 * torch.randn(dim, generator=gen)).half().to(DEV) for _ in range(2)] for _ in range(layers)]
+        kind = mxq.KvCache if bits == 8 else mxq.KvCache4
+        self.caches = [kind.empty(pages, kv_heads, block, dim, DEV) for _ in range(layers)]
 
     def __call__(self, ids, positions, table, lens, starts=None):
         """Logits of each sequence's last token.  `lens` counts the new tokens; `starts` as in mxq_kv_append."""
         x, n = self.embed[ids], ids.shape[0]
         q_end, k_end = self.heads * self.dim, (self.heads + self.kv_heads) * self.dim
-        for (qkv_proj, o_proj, up, down), cache in zip(self.layers, self.caches):
+        for i, ((qkv_proj, o_proj, up, down), cache) in enumerate(zip(self.layers, self.caches)):
             qkv = qkv_proj(norm(x))
             q = qkv[:, :q_end].view(n, self.heads, self.dim)
             k = qkv[:, q_end:k_end].view(n, self.kv_heads, self.dim)
             v = qkv[:, k_end:].view(n, self.kv_heads, self.dim)
-            mxq.mxq_rope(q, k, self.inv_freq, positions, q, k)
-            mxq.mxq_kv_append(cache, k, v, table, lens, starts)
+            if self.norms:
+                mxq.mxq_rope_append(cache, q, k, v, self.inv_freq, table, lens, starts, *self.norms[i], q, positions=positions)
+            else:
+                mxq.mxq_rope(q, k, self.inv_freq, positions, q, k)
+                mxq.mxq_kv_append(cache, k, v, table, lens, starts)
             y = mxq.mxq_attention(q, cache, table, lens, starts)
             x = x + o_proj(y.view(n, q_end))
             g = up(norm(x))
@@ -115,9 +124,11 @@ def main():
     args = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     args.add_argument("--steps", type=int, default=32)
     args.add_argument("--graph", action="store_true")
+    args.add_argument("--norms", action="store_true")
+    args.add_argument("--bits", type=int, choices=(4, 8), default=8)
     args = args.parse_args()
     prompts = [[1, 5, 9, 200, 31], list(range(100, 140)), [7]]
-    for tokens in generate(Decoder(pages=256), prompts, args.steps, args.graph).tolist():
+    for tokens in generate(Decoder(pages=256, norms=args.norms, bits=args.bits), prompts, args.steps, args.graph).tolist():
         print(tokens)
 
 
