@@ -7,37 +7,46 @@
 
 namespace mxq {
 
-// A word's 8 codes as f16 pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7), each 2^-24 of
-// its value: the field is the mantissa of a subnormal number.
-__device__ __forceinline__ h8 codes_tiny(uint32_t w) {
-  return as_h8(u4{w & 0x000F000Fu, (w >> 4) & 0x000F000Fu, (w >> 8) & 0x000F000Fu, (w >> 12) & 0x000F000Fu});
-}
-constexpr float kTinyUnit = 16777216.0f;  // 2^24
-
-// 16 + c of a pair whose codes are in bits 6 .. 9 of each half.
-constexpr uint32_t kMagic16 = 0x4C004C00u, kCode16 = 0x03C003C0u;
-__device__ __forceinline__ h2 with16(uint32_t bits) { return as_h2(and_or(bits, kCode16, kMagic16)); }
-
-// Scales and zero points of 8 neighbouring tokens, as pairs in codes' order.
-struct Scales8 {
-  h2 scale[4], zero16[4];  // zero16: 16 + z
+// A word's 8 codes as f16 pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7), each 64 + c: the
+// field becomes mantissa bits 4 .. 7 under the exponent of 64.  Seven operations.
+// (Codes as the mantissas of subnormal numbers take five, but a product's sums lose
+// bits then: 2^-18 of its terms were seen, as if aligned by their exponent fields.)
+// Plain code: the compiler knows the wait states that a matrix instruction needs before
+// it reads what a vector one wrote; mask and exponent in registers let it use one
+// v_and_or_b32.
+struct Fields {
+  uint32_t mask = 0x00F000F0u, magic = kMagic64;
+  __device__ __forceinline__ Fields() { asm("" : "+s"(mask), "+v"(magic)); }
+  __device__ __forceinline__ h2 with64(uint32_t bits) const { return as_h2((bits & mask) | magic); }
+  __device__ __forceinline__ h8 codes64(uint32_t w) const {
+    return as_h8(u4{as_u32(with64(w << 4)), as_u32(with64(w)), as_u32(with64(w >> 4)), as_u32(with64(w >> 8))});
+  }
 };
-__device__ __forceinline__ Scales8 scales8(u4 words) {
+
+// Scales and zero points (as 64 + z) of 8 neighbouring tokens, as pairs in codes' order.
+struct Scales8 {
+  h2 scale[4], zero64[4];
+};
+__device__ __forceinline__ Scales8 scales8(const Fields& f, u4 words) {
   const u4 w = perm_x_w4(words);
   const uint32_t d[4] = {w.x, w.y, w.z, w.w};
   Scales8 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r.scale[i] = as_h2(d[i] & 0x7FF07FF0u);
-    r.zero16[i] = with16(d[i] << 6);
+    r.zero64[i] = f.with64(d[i] << 4);
   }
   return r;
 }
-// The values of a word, in the same order: differences of codes and products with
-// scales are exact.
-__device__ __forceinline__ h8 values8(uint32_t w, const Scales8& s) {
-  return as_h8(u4{as_u32((with16(w << 6) - s.zero16[0]) * s.scale[0]), as_u32((with16(w << 2) - s.zero16[1]) * s.scale[1]),
-                  as_u32((with16(w >> 2) - s.zero16[2]) * s.scale[2]), as_u32((with16(w >> 6) - s.zero16[3]) * s.scale[3])});
+// c - z of a word of v, and the values of a word, in codes' order: differences of
+// codes and products with scales are exact.
+__device__ __forceinline__ h8 differences8(const Fields& f, uint32_t w, const Scales8& s) {
+  return as_h8(u4{as_u32(f.with64(w << 4) - s.zero64[0]), as_u32(f.with64(w) - s.zero64[1]), as_u32(f.with64(w >> 4) - s.zero64[2]),
+                  as_u32(f.with64(w >> 8) - s.zero64[3])});
+}
+__device__ __forceinline__ h8 values8(const Fields& f, uint32_t w, const Scales8& s) {
+  return as_h8(u4{as_u32((f.with64(w << 4) - s.zero64[0]) * s.scale[0]), as_u32((f.with64(w) - s.zero64[1]) * s.scale[1]),
+                  as_u32((f.with64(w >> 4) - s.zero64[2]) * s.scale[2]), as_u32((f.with64(w >> 8) - s.zero64[3]) * s.scale[3])});
 }
 
 // Scale words of tokens that are not there (from `n` on, of 8) as zero: what they

@@ -2,23 +2,26 @@
 // step's form (one token), and short drafts.
 //
 //   x = (q . c - z sum q) * s * scale,  p = exp(x - max x),
-//   out = sum p (c' - z') s' / sum p
+//   out = sum p s' (c' - z') / sum p
 //
 // with c, z, s a key's codes, zero point and scale, c', z', s' a value's; masks as
 // for the 8-bit cache.
 //
-// Bound: HBM, the cache read once (keys * kv heads * (dim + 4) bytes).  The key axis
-// is divided over workgroups as there (attend_split.h).
+// Bound: HBM, the cache read once (keys * kv heads * (dim + 4) bytes), and beside it
+// the vector ALU, which unpacks two codes where the 8-bit cache has one in the same
+// byte.  The key axis is divided over workgroups as there (attend_split.h).
 //
-// Both products run on the matrix cores straight from registers.  S^T = K Q^T, keys
-// as 16 rows, leaves lane group h four keys of one query row in each tile; with the
-// rows of two tiles dealt out so that those are the 8 tokens that a word of v holds,
-// in the order in which its codes unpack, the weights are the operand of
-// O^T = V^T P^T in place.  k's codes go in as f16 subnormals, unscaled: a key's scale
-// and zero point are applied to its score.  v's become values, exact in f16.
+// Both products run on the matrix cores straight from registers.  S^T = K Q^T, keys as
+// 16 rows, leaves lane group h four keys of one query row in each tile; with the rows
+// of two tiles dealt out so that those are the 8 tokens that a word of v holds, in the
+// order in which its codes unpack, the weights are the operand of O^T = V^T P^T in
+// place.  k's codes go in as 64 + c, and a score starts from -(64 + z) sum q; its key's
+// scale multiplies it afterwards.  v's go in as c - z, and their scale multiplies the
+// weight.
 //
-// Rounding: q, keys and values exact; sums, maxima and weights f32; P is f16, held as
-// 2^14 times its value (the weights are summed before that rounding).
+// Rounding: q and codes exact (a bf16 q to 2^-25 of its row's largest); sums, maxima and
+// weights f32.  P holds the weight times its value's scale over 2^k, 2^k the first power
+// of two that no scale so far reaches, in f16: normal down to 2^-27 of the largest.
 #include <climits>
 
 #include "attend4_device.h"
@@ -33,15 +36,16 @@ struct Raw4 {
   uint32_t k[4][DIM / 32];  // tiles of 16 keys; a key's values h * DIM / 4 ..
   u4 v[2][DIM / 64];        // halves of 32 keys; 4 values of 8 tokens
   u4 ks[2], vs[2];          // scale words of those 8 tokens
-  bool ok[2];               // their page is there
 };
 
+// The pages of a chunk's halves, the same in the whole wave (and of the second 16
+// tokens of each half, where pages have no more); -1: none.
 struct Pages4 {
-  int k[2], v[2];  // pages of the lane's k rows and of its v tokens; -1: none
+  int at[2][2];
 };
 
 template <int N>
-__device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[N]) {
   if constexpr (N == 4) {
     const u4 x = *reinterpret_cast<const u4*>(p);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
@@ -51,10 +55,17 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) 
   }
 }
 
+__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b) {
+  typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, b)));
+}
+
+constexpr float kSlack4 = 1.75f;  // weights reach 2^(kLift + kSlack4), below f16's largest
+
 }  // namespace
 
-template <int DIM, int MT, bool BF16, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ? 1 : 2) void attend4_few_kernel(Attend4Args a) {
+template <int DIM, int MT, int WAVES, bool SMALL>
+__global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES == kFewWaves ? 1 : 2) void attend4_few_kernel(Attend4Args a) {
   constexpr int KW = DIM / 32, DP = DIM / 64, kRows = 16 * MT;
   __shared__ float join[WAVES][16][DIM + 4];
   __shared__ float join_m[WAVES][16], join_l[WAVES][16];
@@ -63,14 +74,84 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
   const int hk = a.pool.kv_heads, block = a.pool.block, block_log2 = 31 - __builtin_clz(block);
   const int head = part.nth % hk, rest = part.nth / hk, rg = rest % part.share.groups, split = rest / part.share.groups;
   const SeqSpan sp = seq_span(a, part.seq);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rho = lane & 15, h = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rho = lane & 15, h = lane >> 4;
   const int row0 = rg * kRows, rows = min(kRows, sp.n * a.group - row0);
   const int pos0 = sp.len - sp.n;
-  const int limit = min(sp.len, a.width * block);
+  const int limit = __builtin_amdgcn_readfirstlane(min(sp.len, a.width * block));
+
+  const int32_t* table = a.table + static_cast<int64_t>(part.seq) * a.table_stride;
+  const int c_begin = part.share.c0 + split * part.step;
+  const int c_end = min(c_begin + part.step, part.share.c0 + part.share.chunks);
+  // the lane's row of 32 keys in the first tile (2 further in the second), its words of k and v
+  const int k_row = 8 * (rho >> 2) + 4 * (rho & 1) + ((rho >> 1) & 1);
+  const uint32_t k_at = static_cast<uint32_t>(k_row * (DIM / 8) + h * KW) * 4, v_at = static_cast<uint32_t>(h * DIM + rho * 4) * 4;  // bytes
+
+  auto pages_of = [&](int c) {
+    Pages4 p;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g == 1 && !SMALL) {
+          p.at[u][1] = p.at[u][0];
+          continue;
+        }
+        // (a chunk past the end may lie past 2^31)
+        const uint32_t j = (static_cast<uint32_t>(c) * kChunk + u * 32 + g * 16) >> block_log2;
+        p.at[u][g] = j < static_cast<uint32_t>(a.width) ? table[j] : -1;
+      }
+    return p;
+  };
+  // Is the page there, and (a page past the sequence's end may be anyone's, or never written) some of its keys?
+  auto there = [&](int c, const Pages4& p, int u, int g) {
+    return p.at[u][g] >= 0 && p.at[u][g] < static_cast<int>(a.pool.blocks) && c * kChunk + u * 32 + g * 16 < limit;
+  };
+  // tokens before a half (or its second 16 tokens), in all of the pool's
+  auto tokens_before = [&](int c, const Pages4& p, int u, int g) {
+    const int64_t page = p.at[u][g] >= 0 && p.at[u][g] < static_cast<int>(a.pool.blocks) ? p.at[u][g] : 0;
+    // (of the second 16 tokens: less 16, which the lanes there have in their offset)
+    return (page * hk + head) * block + ((c * kChunk + u * 32) & (block - 1)) - (SMALL ? 16 * g : 0);
+  };
+  auto load_k = [&](int c, const Pages4& p, Raw4<DIM>& r) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const char* kp = reinterpret_cast<const char*>(a.pool.k) + tokens_before(c, p, u, 0) * (DIM / 2);
+      if constexpr (SMALL) {
+        const char* second = reinterpret_cast<const char*>(a.pool.k) + tokens_before(c, p, u, 1) * (DIM / 2);
+        kp = rho >= 8 ? second : kp;
+      }
+      load_words<KW>(kp + k_at, r.k[2 * u]);
+      load_words<KW>(kp + (k_at + DIM), r.k[2 * u + 1]);
+    }
+  };
+  auto load_v = [&](int c, const Pages4& p, Raw4<DIM>& r) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      int64_t at = tokens_before(c, p, u, 0);
+      if constexpr (SMALL) {
+        const int64_t second = tokens_before(c, p, u, 1);
+        at = h >= 2 ? second : at;
+      }
+      const char* vp = reinterpret_cast<const char*>(a.pool.v) + at * (DIM / 2);
+#pragma unroll
+      for (int d = 0; d < DP; ++d) r.v[u][d] = *reinterpret_cast<const u4*>(vp + (v_at + d * 256));
+      r.ks[u] = *reinterpret_cast<const u4*>(reinterpret_cast<const char*>(a.pool.k_scale + at) + static_cast<uint32_t>(16 * h));
+      r.vs[u] = *reinterpret_cast<const u4*>(reinterpret_cast<const char*>(a.pool.v_scale + at) + static_cast<uint32_t>(16 * h));
+    }
+  };
+
+  // the first chunk is on its way while the queries are read
+  Raw4<DIM> raw;
+  const int c_first = __builtin_amdgcn_readfirstlane(c_begin + wave);
+  Pages4 now_at = pages_of(c_first), ahead = pages_of(c_first + WAVES);  // past the end: -1, or a page that is not used
+  if (c_first < c_end) {
+    load_k(c_first, now_at, raw);
+    load_v(c_first, now_at, raw);
+  }
 
   // query rows of this lane (one of 16 for each mt): fragments, sums, key ranges
-  h8 qf[MT][KW];
-  float factor[MT], q_sum[MT];
+  __shared__ u4 q_rows[MT][KW][64];  // the fragments of a wave: the same in all
+  float factor[MT], start[MT];
   int from[MT], upto[MT];
   int all_from = 0, all_upto = INT_MAX;
 #pragma unroll
@@ -80,26 +161,24 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
     const int tok = real ? i / a.group : 0, hq = head * a.group + (real ? i - tok * a.group : 0);
     const uint16_t* q = a.q + static_cast<int64_t>(sp.t0 + tok) * a.q_token + static_cast<int64_t>(hq) * a.q_head;
     u4 raw[KW];
+    float inverse = 1.0f, sum = 0.0f;
 #pragma unroll
-    for (int m = 0; m < KW; ++m) raw[m] = *reinterpret_cast<const u4*>(q + h * (DIM / 4) + m * 8);
-    float inverse = 1.0f;
-    if constexpr (BF16) {
+    for (int w = 0; w < KW; ++w) raw[w] = *reinterpret_cast<const u4*>(q + h * (DIM / 4) + w * 8);
+    if (a.bf16) {
       float top = 0.0f, fac;
 #pragma unroll
-      for (int m = 0; m < KW; ++m) top = fmaxf(top, absmax8_bf16(raw[m]));
-      top = max_xor16(max_xor32(top));
-      row_factor(top, fac, inverse);
+      for (int w = 0; w < KW; ++w) top = fmaxf(top, absmax8_bf16(raw[w]));
+      row_factor(max_xor16(max_xor32(top)), fac, inverse);
 #pragma unroll
-      for (int m = 0; m < KW; ++m) raw[m] = bf16_to_scaled_f16(raw[m], fac);
+      for (int w = 0; w < KW; ++w) raw[w] = bf16_to_scaled_f16(raw[w], fac);
     }
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      sum += sum8_f32(raw[w]);
+      if (wave == 0) q_rows[mt][w][lane] = perm_x_w4(raw[w]);
+    }
+    start[mt] = -add_xor16(add_xor32(sum));
     factor[mt] = a.scale2 * inverse;
-    float sum = 0.0f;
-#pragma unroll
-    for (int m = 0; m < KW; ++m) {
-      sum += sum8_f32(raw[m]);
-      qf[mt][m] = as_h8(perm_x_w4(raw[m]));
-    }
-    q_sum[mt] = add_xor16(add_xor32(sum));
     const int pos = pos0 + tok;
     upto[mt] = min(pos + 1, limit);  // rows past the last repeat the first; they are not stored
     from[mt] = first_seen(a, pos);
@@ -114,52 +193,14 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
     all_from = max(all_from, __shfl_xor(all_from, d));
     all_upto = min(all_upto, __shfl_xor(all_upto, d));
   }
+  __syncthreads();
+  all_from = __builtin_amdgcn_readfirstlane(all_from);
+  all_upto = __builtin_amdgcn_readfirstlane(all_upto);
 
-  const int32_t* table = a.table + static_cast<int64_t>(part.seq) * a.table_stride;
-  const int c_begin = part.share.c0 + split * part.step;
-  const int c_end = min(c_begin + part.step, part.share.c0 + part.share.chunks);
-  const int k_row = 8 * (rho >> 2) + 4 * (rho & 1) + ((rho >> 1) & 1);  // of 32 keys; 2 more in the second tile
-
-  auto pages_of = [&](int c) {
-    Pages4 p;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      // (a chunk past the end may lie past 2^31)
-      const uint32_t key = static_cast<uint32_t>(c) * kChunk + u * 32, width = a.width;
-      const uint32_t jk = (key + 8 * (rho >> 2)) >> block_log2, jv = (key + 8 * h) >> block_log2;
-      p.k[u] = jk < width ? table[jk] : -1;
-      p.v[u] = jv < width ? table[jv] : -1;
-    }
-    return p;
-  };
-  auto load_k = [&](int c, const Pages4& p, Raw4<DIM>& r) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t page = p.k[u] >= 0 && p.k[u] < static_cast<int>(a.pool.blocks) ? p.k[u] : 0;
-      const int slot = (c * kChunk + u * 32 + k_row) & (block - 1);
-      const uint32_t* kp = a.pool.k + ((page * hk + head) * block + slot) * (DIM / 8) + h * KW;
-      load_words<KW>(kp, r.k[2 * u]);
-      load_words<KW>(kp + 2 * (DIM / 8), r.k[2 * u + 1]);
-    }
-  };
-  auto load_v = [&](int c, const Pages4& p, Raw4<DIM>& r) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int key = c * kChunk + u * 32 + 8 * h;
-      // a page past the sequence's end may be anyone's, or never written
-      r.ok[u] = p.v[u] >= 0 && p.v[u] < static_cast<int>(a.pool.blocks) && key < limit;
-      const int64_t ph = static_cast<int64_t>(r.ok[u] ? p.v[u] : 0) * hk + head;
-      const int slot = key & (block - 1);
-      const uint32_t* vp = a.pool.v + (ph * (block / 8) + slot / 8) * DIM + rho * 4;
-#pragma unroll
-      for (int d = 0; d < DP; ++d) r.v[u][d] = *reinterpret_cast<const u4*>(vp + d * 64);
-      r.ks[u] = *reinterpret_cast<const u4*>(a.pool.k_scale + ph * block + slot);
-      r.vs[u] = *reinterpret_cast<const u4*>(a.pool.v_scale + ph * block + slot);
-    }
-  };
-
+  const Fields fields;
   f4 acc[MT][4 * DP];
   float m[MT], l[MT];
+  int unit = 0;  // k + 14: the exponent field of the largest scale
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     m[mt] = kNegInf;
@@ -168,109 +209,153 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
     for (int d = 0; d < 4 * DP; ++d) acc[mt][d] = f4{0, 0, 0, 0};
   }
 
-  // one chunk: as soon as k's registers are free they take the next chunk's
-  // rows, and v's do after the second product
-  auto step = [&](int c, Raw4<DIM>& r, Pages4& ahead) {
+  // one chunk: k's registers take the next chunk's rows before the second product (not
+  // before the softmax, which needs registers too: 53 and 50 us for 96 sequences of up
+  // to 8192 keys), v's do after it
+  auto step = [&](int c, Raw4<DIM>& r) {
     const bool more = c + WAVES < c_end;
+    bool whole = c * kChunk >= all_from && c * kChunk <= all_upto - kChunk;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int g = 0; g < (SMALL ? 2 : 1); ++g) whole = whole && there(c, now_at, u, g);
     f4 s[MT][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[mt][t] = f4{0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const h8 k = codes_tiny(r.k[t][w]);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) s[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[mt][w], s[mt][t], 0, 0, 0);
-      }
-    }
-    if (more) load_k(c + WAVES, ahead, r);
-    const bool whole = __all(r.ok[0] && r.ok[1]) && c * kChunk >= all_from && c * kChunk <= all_upto - kChunk;
-    if (!whole) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) r.vs[u] = first_words(r.vs[u], r.ok[u] ? min(limit - (c * kChunk + u * 32 + 8 * h), 8) : 0);
-    }
-    float mx[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) mx[mt] = kNegInf;
+    h2 k_scale[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const u4 w4 = perm_x_w4(r.ks[u]);
-      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      const Scales8 sc = scales8(fields, r.ks[u]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {  // key e of the 8, in codes' order
-        const uint32_t pair = w[e >> 1];
-        const h2 sc = as_h2(pair & 0x7FF07FF0u);
-        const float scale = static_cast<float>(e & 1 ? sc.y : sc.x), zero = static_cast<float>((pair >> (16 * (e & 1))) & 15u);
-        const int key = c * kChunk + u * 32 + 8 * h + (e >> 1) + 4 * (e & 1);
+      for (int i = 0; i < 4; ++i) {
+        k_scale[u][i] = sc.scale[i];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          float x = __builtin_fmaf(s[mt][2 * u + (e >> 2)][e & 3], kTinyUnit, -zero * q_sum[mt]) * scale * factor[mt];
-          if (!whole) x = r.ok[u] && key >= from[mt] && key < upto[mt] ? x : kNegInf;
-          mx[mt] = fmaxf(mx[mt], x);
-          s[mt][2 * u + (e >> 2)][e & 3] = x;
+          f4& t = s[mt][2 * u + (i >> 1)];
+          t[2 * (i & 1)] = __builtin_fmaf(static_cast<float>(sc.zero64[i].x), start[mt], 0.0f);
+          t[2 * (i & 1) + 1] = __builtin_fmaf(static_cast<float>(sc.zero64[i].y), start[mt], 0.0f);
         }
       }
     }
-    u4 pf[MT][2];
+    {
+      asm volatile("" ::: "memory");  // read here each time: 16 registers less
+      h8 qf[MT][KW];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int w = 0; w < KW; ++w) qf[mt][w] = as_h8(q_rows[mt][w][lane]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const h8 k = fields.codes64(r.k[t][w]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) s[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[mt][w], s[mt][t], 0, 0, 0);
+        }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool ok = SMALL && h >= 2 ? there(c, now_at, u, 1) : there(c, now_at, u, 0);
+        r.vs[u] = first_words(r.vs[u], ok ? min(limit - (c * kChunk + u * 32 + 8 * h), 8) : 0);
+      }
+    }
+    // the largest scale so far, as an exponent field
+    const uint32_t big = max_pairs(max_pairs(max_pairs(r.vs[0].x, r.vs[0].y), max_pairs(r.vs[0].z, r.vs[0].w)),
+                                   max_pairs(max_pairs(r.vs[1].x, r.vs[1].y), max_pairs(r.vs[1].z, r.vs[1].w)));
+    int field = static_cast<int>(max(big & 0xFFFFu, big >> 16) >> 10);
+    float shrink = 1.0f;
+    if (__any(field > unit)) {
+#pragma unroll
+      for (int d = 16; d < 64; d *= 2) field = max(field, __shfl_xor(field, d));
+      field = __builtin_amdgcn_readfirstlane(field);
+      shrink = __uint_as_float(static_cast<uint32_t>(127 - (field - unit)) << 23);
+      unit = field;
+    }
+    const float lift = kLift + 14.0f - static_cast<float>(unit);
+    float base[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float now = fmaxf(m[mt], max_xor16(max_xor32(mx[mt])));
-      const float ref = now == kNegInf ? 0.0f : now;
-      const float alpha = __builtin_amdgcn_exp2f(m[mt] - ref);
-      m[mt] = now;
-      float sum = 0.0f;
-      uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(s[mt][i >> 2][i & 3] - ref + kLift);
-        const float p1 = __builtin_amdgcn_exp2f(s[mt][i >> 2][(i & 3) + 1] - ref + kLift);
-        sum += p0 + p1;
-        const h2 pk = {static_cast<_Float16>(p0), static_cast<_Float16>(p1)};
-        w[i / 2] = as_u32(pk);
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const h2 sc = k_scale[t >> 1][2 * (t & 1) + (i >> 1)];
+          s[mt][t][i] *= __builtin_fmaf(static_cast<float>(i & 1 ? sc.y : sc.x), factor[mt], 0.0f);
+        }
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bool ok = SMALL && h >= 2 ? there(c, now_at, t >> 1, 1) : there(c, now_at, t >> 1, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = c * kChunk + (t >> 1) * 32 + 8 * h + 2 * (t & 1) + (i >> 1) + 4 * (i & 1);
+            s[mt][t][i] = ok && key >= from[mt] && key < upto[mt] ? s[mt][t][i] : kNegInf;
+          }
+        }
       }
-      l[mt] = l[mt] * alpha + sum;
-      pf[mt][0] = u4{w[0], w[1], w[2], w[3]};
-      pf[mt][1] = u4{w[4], w[5], w[6], w[7]};
+      float mx = kNegInf;
 #pragma unroll
-      for (int d = 0; d < 4 * DP; ++d) acc[mt][d] *= alpha;
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[mt][t][i]);
+      float now = fmaxf(m[mt], max_xor16(max_xor32(mx)));
+      // the reference moves only where weights would leave f16's range
+      if (!__any(now > m[mt] + kSlack4)) now = m[mt];
+      const float ref = now == kNegInf ? 0.0f : now;
+      const float down = __builtin_amdgcn_exp2f(m[mt] - ref) * shrink;
+      m[mt] = now;
+      base[mt] = ref - lift;
+      if (__any(down != 1.0f)) {
+        l[mt] *= down;
+#pragma unroll
+        for (int d = 0; d < 4 * DP; ++d) acc[mt][d] *= down;
+      }
     }
+    if (more) load_k(c + WAVES, ahead, r);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const Scales8 sc = scales8(r.vs[u]);
+      const Scales8 sc = scales8(fields, r.vs[u]);
+      u4 pf[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f4& t = s[mt][2 * u + (i >> 1)];
+          const float p0 = __builtin_amdgcn_exp2f(t[2 * (i & 1)] - base[mt]), p1 = __builtin_amdgcn_exp2f(t[2 * (i & 1) + 1] - base[mt]);
+          l[mt] += p0 + p1;
+          const h2 pk = {static_cast<_Float16>(__builtin_fmaf(p0, static_cast<float>(sc.scale[i].x), 0.0f)),
+                         static_cast<_Float16>(__builtin_fmaf(p1, static_cast<float>(sc.scale[i].y), 0.0f))};
+          d[i] = as_u32(pk);
+        }
+        pf[mt] = u4{d[0], d[1], d[2], d[3]};
+      }
 #pragma unroll
       for (int d = 0; d < DP; ++d) {
-        const uint32_t w[4] = {r.v[u][d].x, r.v[u][d].y, r.v[u][d].z, r.v[u][d].w};
+        const uint32_t v[4] = {r.v[u][d].x, r.v[u][d].y, r.v[u][d].z, r.v[u][d].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const h8 v = values8(w[e], sc);
+          const h8 codes = differences8(fields, v[e], sc);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            acc[mt][d * 4 + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_h8(pf[mt][u]), acc[mt][d * 4 + e], 0, 0, 0);
+            acc[mt][d * 4 + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, as_h8(pf[mt]), acc[mt][d * 4 + e], 0, 0, 0);
         }
       }
     }
     if (more) {
       load_v(c + WAVES, ahead, r);
+      now_at = ahead;
       ahead = pages_of(c + 2 * WAVES);
     }
   };
 
-  int c = c_begin + wave;
-  if (c < c_end) {
-    Raw4<DIM> raw;
-    Pages4 ahead = pages_of(c);
-    load_k(c, ahead, raw);
-    load_v(c, ahead, raw);
-    ahead = pages_of(c + WAVES);   // past the end: -1, or a page that is not used
-    for (; c < c_end; c += WAVES) step(c, raw, ahead);
-  }
+  for (int c = c_first; c < c_end; c += WAVES) step(c, raw);
 
-  // join the waves, 16 rows at a time
+  // join the waves, 16 rows at a time; weights in units of 2^-kLift, whatever the scales
   const bool alone = part.splits == 1;
+  const float scale_unit = __uint_as_float(static_cast<uint32_t>(127 + unit - 14) << 23);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const float weight = add_xor16(add_xor32(l[mt]));
+    const float weight = add_xor16(add_xor32(l[mt])) * scale_unit;
     if (h == 0) {
       join_m[wave][rho] = m[mt];
       join_l[wave][rho] = weight;
@@ -281,7 +366,7 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<f4*>(&join[wave][rho][d * 64 + h * 16 + i * 4]) =
-            f4{acc[mt][d * 4][i], acc[mt][d * 4 + 1][i], acc[mt][d * 4 + 2][i], acc[mt][d * 4 + 3][i]};
+            f4{acc[mt][d * 4][i], acc[mt][d * 4 + 1][i], acc[mt][d * 4 + 2][i], acc[mt][d * 4 + 3][i]} * scale_unit;
     __syncthreads();
     for (int u = threadIdx.x; u < 16 * (DIM / 4); u += 64 * WAVES) {
       const int row = u / (DIM / 4), d = (u - row * (DIM / 4)) * 4, i = mt * 16 + row;
@@ -303,7 +388,7 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
           const int64_t at = static_cast<int64_t>(sp.t0 + tok) * a.heads + hq;
           uint16_t o[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = f32_to_act_bits<BF16>(y[e]);
+          for (int e = 0; e < 4; ++e) o[e] = a.bf16 ? f32_to_bf16_bits(y[e]) : f32_to_f16_bits(y[e]);
           *reinterpret_cast<uint2*>(a.out + at * DIM + d) =
               uint2{static_cast<uint32_t>(o[0]) | (static_cast<uint32_t>(o[1]) << 16),
                     static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
@@ -322,11 +407,14 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
 namespace {
 
 struct Parts4 {
+  // Three workgroups a compute unit are what its registers hold (three sequences of
+  // 131000 keys: 90 us with three, 100 with five, 105 with eight).
+  static constexpr int kPerUnit = 3, kLongChunks = INT_MAX;
   template <int DIM, int MT, int WAVES>
   static hipError_t launch(const Attend4Args& a, unsigned slots) {
     const dim3 grid(slots), block(64 * WAVES);
-    if (a.bf16) hipLaunchKernelGGL((attend4_few_kernel<DIM, MT, true, WAVES>), grid, block, 0, a.stream, a);
-    else hipLaunchKernelGGL((attend4_few_kernel<DIM, MT, false, WAVES>), grid, block, 0, a.stream, a);
+    if (a.pool.block == 16) hipLaunchKernelGGL((attend4_few_kernel<DIM, MT, WAVES, true>), grid, block, 0, a.stream, a);
+    else hipLaunchKernelGGL((attend4_few_kernel<DIM, MT, WAVES, false>), grid, block, 0, a.stream, a);
     return hipGetLastError();
   }
 };

@@ -157,14 +157,15 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend4_many_kernel(Attend4Ar
     vs = first_words(*reinterpret_cast<const u4*>(a.pool.v_scale + ph * block + slot), ok ? min(limit - key, 8) : 0);
     there = ok;
   };
+  const Fields fields;
   auto put = [&](Stage4<DIM>& st) {
     const uint32_t both = ks | (ks << 16);
-    const h2 scale = as_h2(both & 0x7FF07FF0u), zero16 = with16(both << 6);
-    const Scales8 k_scales{{scale, scale, scale, scale}, {zero16, zero16, zero16, zero16}}, v_scales = scales8(vs);
+    const h2 scale = as_h2(both & 0x7FF07FF0u), zero = fields.with64(both << 4);
+    const Scales8 k_scales{{scale, scale, scale, scale}, {zero, zero, zero, zero}}, v_scales = scales8(fields, vs);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      st.k[k_at<DIM>(kr, kc * W + w)] = __builtin_bit_cast(u4, values8(kraw[w], k_scales));
-      st.v[v_at(vd + w, vg)] = __builtin_bit_cast(u4, values8(vraw[w], v_scales));
+      st.k[k_at<DIM>(kr, kc * W + w)] = __builtin_bit_cast(u4, values8(fields, kraw[w], k_scales));
+      st.v[v_at(vd + w, vg)] = __builtin_bit_cast(u4, values8(fields, vraw[w], v_scales));
     }
     if ((tid & 63) == 0) st.there[tid >> 6] = there;  // of both 8-token groups: a page has 16 tokens at least
   };

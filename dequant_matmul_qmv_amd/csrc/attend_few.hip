@@ -357,6 +357,10 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM >= 256 && WAVES == kFewWaves ?
 namespace {
 
 struct Parts {
+  // Four workgroups a compute unit, or two where four would still have three chunks a
+  // wave (64 sequences up to 8192 keys: 45 us with four, 48 with two; 8 of 16384: 59
+  // and 55; two of 131071: 105 and 101).
+  static constexpr int kPerUnit = 4, kLongChunks = 3 * kFewWaves;
   template <int DIM, int MT, int WAVES>
   static hipError_t launch(const AttendArgs& a, unsigned slots) {
     const dim3 grid(slots), block(64 * WAVES);

@@ -13,7 +13,6 @@ namespace {
 
 constexpr int kFewWaves = 4;    // of a workgroup; twice that where it takes all keys
 constexpr int kChunk = 64;      // keys a wave takes at a time
-constexpr int kLongRounds = 3;
 constexpr int kMinChunks = 4;   // at least one chunk for each wave of a workgroup
 // Tables of up to this many keys are not split: a workgroup of eight waves takes
 // all keys of its rows, in two rounds at most.  8 kv heads, split and joined / not
@@ -66,12 +65,11 @@ __device__ Part find_part(const Args& a, int slot, int seq) {
     total += static_cast<long long>(mine.chunks) * mine.groups * hk;
   }
   total = wave_sum(total);
-  // Four workgroups a compute unit, or two where four would still have
-  // kLongRounds chunks a wave (64 sequences up to 8192 keys: 45 us with four, 48
-  // with two; 8 of 16384: 59 and 55; two of 131071: 105 and 101); parts of whole
-  // rounds of the four waves (64 sequences: 48 us with parts of 9 chunks, 45 with 12).
+  // As many workgroups a compute unit as the kernel asks for, or half of them where
+  // they would have its long parts; parts of whole rounds of the four waves (8 bits, 64
+  // sequences: 48 us with parts of 9 chunks, 45 with 12).
   long long even = (total + a.target - 1) / a.target;
-  if (even >= kLongRounds * kFewWaves) even *= 2;
+  if (even >= a.long_chunks) even *= 2;
   Part p{};
   p.step = static_cast<int>((max(even, static_cast<long long>(a.min_chunks)) + kFewWaves - 1) / kFewWaves * kFewWaves);
   int before = 0;
@@ -320,7 +318,8 @@ hipError_t launch_attend_parts(const Args& given, const DeviceInfo& dev) {
   const bool few = a.starts == nullptr || a.seqs > 1 || all_rows <= kFewRows;
   const bool many = a.starts != nullptr && all_rows > kFewRows;
   a.few_rows = !many ? INT_MAX : few ? kFewRows : 0;
-  a.target = dev.num_cu * 4;
+  a.target = dev.num_cu * Parts::kPerUnit;
+  a.long_chunks = Parts::kLongChunks;
   // the most new tokens of a sequence that the few-row kernel takes
   a.join_new = a.starts == nullptr ? 1 : many ? (kFewRows / a.group > 0 ? kFewRows / a.group : 1) : a.tokens;
 
