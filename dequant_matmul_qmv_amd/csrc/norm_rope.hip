@@ -6,17 +6,24 @@
 // a pair's angle being its frequency times the position on its axis (one axis for
 // text; time, height and width for frames).
 //
-// Bound: HBM, q and k read once and written once.  A lane holds 16 values of a
-// head, both halves of 8 pairs; dim / 16 neighbours hold the head and add their
-// squares by DPP.  A workgroup takes a few tokens: it computes their turns once
-// into LDS, where every head reads them, while the first loads are on their way.
+// Bound: HBM, q and k read once and written once, with the vector ALU close behind (a
+// mean of squares in f64, two products and a turn for each value).  A lane holds 16
+// values of a head, both halves of 8 pairs; dim / 16 neighbours hold the head and add
+// their squares by DPP.  A lane keeps its place in the token, and its weights, for all
+// of the workgroup's tokens, and loads the next token's values before it turns one; the
+// turns of all of them are computed once into LDS, while the first loads are on their way.
 #include "turn_device.h"
 
 namespace mxq {
 
 namespace {
 
-constexpr int kMaxDim = 256, kMaxTurns = 512;
+constexpr int kMaxDim = 256, kMaxTurns = 1024;
+constexpr int kMostThreads = 512;
+// Workgroups of a long call, two for each compute unit: what a workgroup does before its
+// first token costs as much as 1.5 tokens of 40 heads (8191 of them: 75 us with one token a
+// workgroup, 53 with two, 36.5 with 4, 39.2 with 8, 35.5 with 16, those of two whole rounds).
+constexpr int kWorkgroups = 512;
 constexpr int64_t kL2Bytes = 32 << 20;    // of the eight dies
 constexpr int64_t kPartTokens = 1 << 23;  // of a launch, whose grid ends below 2^32 threads
 
@@ -25,36 +32,28 @@ constexpr int64_t kPartTokens = 1 << 23;  // of a launch, whose grid ends below 
 // 16-byte rows, dim and rot multiples of 16.  STREAM: what the call moves does not
 // stay in the L2s anyway, so loads and stores pass them by.
 template <bool BF16, bool INTER, bool STREAM>
-__global__ __launch_bounds__(256) void norm_rope_wide_kernel(NormRopeArgs a) {
+__global__ __launch_bounds__(kMostThreads) void norm_rope_wide_kernel(NormRopeArgs a) {
   __shared__ Turn turns[kMaxTurns];
-  __shared__ float weights[2][kMaxDim];
   const int half = a.turn.rot / 2, turned = a.turn.rot / 16, used = a.dim / 16;
   const int log2 = used > 8 ? 4 : used > 4 ? 3 : used > 2 ? 2 : used - 1, lanes = 1 << log2;
   const int heads = a.side[0].heads + a.side[1].heads, per = heads << log2, tid = threadIdx.x;
+  // the lane's place: its token of those that the workgroup has at a time, its head and
+  // its 16-byte pieces there (the two halves of 8 pairs; interleaved, two that neighbours'
+  // pieces lie beside; behind the turned part, neighbours)
+  const int place = static_cast<int>(blockIdx.y) * kMostThreads + tid, sub = a.abreast == 1 ? 0 : static_cast<int>(__umulhi(place, a.per_inverse));
+  const int slot = place - sub * per, c = slot & (lanes - 1);
+  int head = slot >> log2;
+  const bool here = head < heads && sub < a.abreast && c < used;
+  const int side = head < a.side[0].heads ? 0 : 1;
+  if (side == 1) head -= a.side[0].heads;
+  const int lo_at = INTER || c < turned ? 8 * c : 16 * c, hi_at = INTER ? 8 * (used + c) : c < turned ? half + 8 * c : 16 * c + 8;
+  const bool lo_turns = INTER ? lo_at < a.turn.rot : c < turned, hi_turns = INTER && hi_at < a.turn.rot;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.batch;
-  const int tokens = a.tokens - t0 < a.batch ? static_cast<int>(a.tokens - t0) : a.batch, all = tokens * per;
-  const int c = tid & (lanes - 1);  // the lane's place in its heads
-  // its 16-byte pieces there: the two halves of 8 pairs, or neighbours
-  const bool turns_here = c < turned;
-  const int lo_at = INTER || !turns_here ? 16 * c : 8 * c, hi_at = INTER || !turns_here ? 16 * c + 8 : half + 8 * c;
-  struct Unit {
-    bool real;
-    int tok, side;
-    const uint16_t* in;
-    uint16_t* out;
-  };
-  const auto unit = [&](int u) {
-    Unit w{u < all && c < used, 0, 0, nullptr, nullptr};
-    if (!w.real) return w;
-    w.tok = a.batch == 1 ? 0 : u / per;
-    int head = (u - w.tok * per) >> log2;
-    w.side = head < a.side[0].heads ? 0 : 1;
-    const RopeSide& s = a.side[w.side];
-    if (w.side == 1) head -= a.side[0].heads;
-    w.in = s.in + (t0 + w.tok) * s.in_token + head * s.in_head;
-    w.out = s.out + (t0 + w.tok) * s.out_token + head * s.out_head;
-    return w;
-  };
+  const int tokens = a.tokens - t0 < a.batch ? static_cast<int>(a.tokens - t0) : a.batch;
+  const RopeSide& s = a.side[side];
+  const uint16_t* in = s.in + (t0 + sub) * s.in_token + head * s.in_head;
+  uint16_t* out = s.out + (t0 + sub) * s.out_token + head * s.out_head;
+  const int64_t in_step = a.abreast * s.in_token, out_step = a.abreast * s.out_token;
   const auto get = [](const uint16_t* p) {
     const u4* v = reinterpret_cast<const u4*>(p);
     if constexpr (STREAM) return __builtin_nontemporal_load(v);
@@ -65,73 +64,73 @@ __global__ __launch_bounds__(256) void norm_rope_wide_kernel(NormRopeArgs a) {
     if constexpr (STREAM) __builtin_nontemporal_store(x, v);
     else *v = x;
   };
-  const bool norms = a.turn.weight[0] != nullptr || a.turn.weight[1] != nullptr;
-  const auto turn = [&](const Unit& w, u4 lo, u4 hi) {
+  // loads are answered in order: those of the first turn and of the weights come first
+  TurnInput mine{0, 0.0f};
+  const int all_turns = tokens * half;
+  const auto input = [&](int i) {
+    const int tok = static_cast<int>(__umulhi(i, a.half_inverse));
+    return turn_input(a.turn, i - tok * half, t0 + tok, 0);
+  };
+  if (tid < all_turns) mine = input(tid);
+  const bool norm = a.turn.weight[side] != nullptr && here, norms = a.turn.weight[0] != nullptr || a.turn.weight[1] != nullptr;
+  float wx[8], wz[8];
+  if (norm) {
+    weights8<BF16>(a.turn, side, lo_at, wx);
+    weights8<BF16>(a.turn, side, hi_at, wz);
+  }
+  u4 lo = u4{0, 0, 0, 0}, hi = lo;
+  if (here && sub < tokens) {
+    lo = get(in + lo_at);
+    hi = get(in + hi_at);
+  }
+  if (tid < all_turns) turns[tid] = mine.turn();
+  for (int i = tid + blockDim.x; i < all_turns; i += blockDim.x) turns[i] = input(i).turn();
+  __syncthreads();
+  const Turn* t = turns + sub * half;
+  for (int tok = sub; tok - sub < tokens; tok += a.abreast) {  // whole waves: their lanes add squares
     float x[8], z[8];
     widen8<BF16>(lo, x);
     widen8<BF16>(hi, z);
+    in += in_step;
+    if (here && tok + a.abreast < tokens) {
+      lo = get(in + lo_at);
+      hi = get(in + hi_at);
+    }
     if (norms) {
-      const float r = inverse_norm(group_sum(squares(x) + squares(z), lanes), a.dim, a.turn.eps);
-      if (a.turn.weight[w.side] != nullptr) {
+      const float r = inverse_norm(group_sum(squares(x) + squares(z), lanes), a.turn.inv_dim, a.turn.eps);
+      if (norm) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] = normed(x[i], r, weights[w.side][lo_at + i]);
-          z[i] = normed(z[i], r, weights[w.side][hi_at + i]);
+          x[i] = normed(x[i], r, wx[i]);
+          z[i] = normed(z[i], r, wz[i]);
         }
       }
     }
-    if (!w.real) return;
-    if (turns_here) {
-      const Turn* t = turns + w.tok * half + 8 * c;
+    if (here && tok < tokens) {
+      if constexpr (INTER) {
+        const auto turn4 = [](float(&y)[8], const Turn* by) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (INTER) {
-          float(&y)[8] = i < 4 ? x : z;
-          const float p = y[2 * i & 7], q = y[(2 * i & 7) + 1];
-          y[2 * i & 7] = turned_first(p, q, t[i]);
-          y[(2 * i & 7) + 1] = turned_second(p, q, t[i]);
-        } else {
+          for (int i = 0; i < 8; i += 2) {
+            const float p = y[i], q = y[i + 1];
+            y[i] = turned_first(p, q, by[i / 2]);
+            y[i + 1] = turned_second(p, q, by[i / 2]);
+          }
+        };
+        if (lo_turns) turn4(x, t + lo_at / 2);
+        if (hi_turns) turn4(z, t + hi_at / 2);
+      } else if (lo_turns) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
           const float p = x[i], q = z[i];
-          x[i] = turned_first(p, q, t[i]);
-          z[i] = turned_second(p, q, t[i]);
+          x[i] = turned_first(p, q, t[lo_at + i]);
+          z[i] = turned_second(p, q, t[lo_at + i]);
         }
       }
+      put(out + lo_at, round8<BF16>(x));
+      put(out + hi_at, round8<BF16>(z));
     }
-    put(w.out + lo_at, narrow8<BF16>(x));
-    put(w.out + hi_at, narrow8<BF16>(z));
-  };
-  // the first units are on their way while the turns are computed
-  constexpr int kAhead = 2;
-  u4 lo[kAhead], hi[kAhead];
-#pragma unroll
-  for (int e = 0; e < kAhead; ++e) {
-    lo[e] = hi[e] = u4{0, 0, 0, 0};
-    const Unit w = unit(tid + e * 256);
-    if (w.real) {
-      lo[e] = get(w.in + lo_at);
-      hi[e] = get(w.in + hi_at);
-    }
-  }
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (a.turn.weight[s] != nullptr)
-      for (int d = tid; d < a.dim; d += 256) weights[s][d] = weight_at<BF16>(a.turn, s, d);
-  for (int i = tid; i < tokens * half; i += 256) {
-    const int tok = i / half;
-    turns[i] = turn_of(a.turn, i - tok * half, t0 + tok, 0);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < kAhead; ++e)
-    if (e * 256 < all) turn(unit(tid + e * 256), lo[e], hi[e]);
-  for (int u0 = kAhead * 256; u0 < all; u0 += 256) {  // whole waves: their lanes add squares
-    const Unit w = unit(tid + u0);
-    u4 x = u4{0, 0, 0, 0}, z = x;
-    if (w.real) {
-      x = get(w.in + lo_at);
-      z = get(w.in + hi_at);
-    }
-    turn(w, x, z);
+    out += out_step;
+    t += a.abreast * half;
   }
 }
 
@@ -158,7 +157,7 @@ __global__ __launch_bounds__(256) void norm_rope_narrow_kernel(NormRopeArgs a) {
       sum = __builtin_fma(static_cast<double>(x[j]), static_cast<double>(x[j]), sum);
     }
     if (a.turn.weight[side] != nullptr) {  // the same for a whole wave
-      const float r = inverse_norm(wave_sum(sum), a.dim, a.turn.eps);
+      const float r = inverse_norm(wave_sum(sum), a.turn.inv_dim, a.turn.eps);
 #pragma unroll
       for (int j = 0; j < kMaxDim / 64; ++j)
         if (lane + 64 * j < a.dim) x[j] = normed(x[j], r, weight_at<BF16>(a.turn, side, lane + 64 * j));
@@ -187,13 +186,16 @@ __global__ __launch_bounds__(256) void norm_rope_narrow_kernel(NormRopeArgs a) {
 namespace {
 
 template <bool BF16, bool INTER>
-hipError_t launch_wide(const NormRopeArgs& a, unsigned grid) {
+hipError_t launch_wide(const NormRopeArgs& a, dim3 grid, dim3 block) {
   if (4 * a.tokens * (a.side[0].heads + a.side[1].heads) * a.dim > kL2Bytes)
-    hipLaunchKernelGGL((norm_rope_wide_kernel<BF16, INTER, true>), dim3(grid), dim3(256), 0, a.stream, a);
+    hipLaunchKernelGGL((norm_rope_wide_kernel<BF16, INTER, true>), grid, block, 0, a.stream, a);
   else
-    hipLaunchKernelGGL((norm_rope_wide_kernel<BF16, INTER, false>), dim3(grid), dim3(256), 0, a.stream, a);
+    hipLaunchKernelGGL((norm_rope_wide_kernel<BF16, INTER, false>), grid, block, 0, a.stream, a);
   return hipGetLastError();
 }
+
+// ceil(2^32 / d): __umulhi with it divides numbers up to 2^16 by d up to 2^12.
+uint32_t over32(int d) { return static_cast<uint32_t>(((uint64_t{1} << 32) + d - 1) / d); }
 
 hipError_t launch_part(NormRopeArgs a) {
   bool wide = a.dim % 16 == 0 && a.turn.rot % 16 == 0;
@@ -207,10 +209,29 @@ hipError_t launch_part(NormRopeArgs a) {
     else hipLaunchKernelGGL((norm_rope_narrow_kernel<false>), grid, dim3(256), 0, a.stream, a);
     return hipGetLastError();
   }
-  a.batch = 1;
-  const unsigned grid = static_cast<unsigned>((a.tokens + a.batch - 1) / a.batch);
-  if (a.turn.interleaved) return a.bf16 ? launch_wide<true, true>(a, grid) : launch_wide<false, true>(a, grid);
-  return a.bf16 ? launch_wide<true, false>(a, grid) : launch_wide<false, false>(a, grid);
+  // tokens abreast: as many as fill whole waves best; then as many times those as leave
+  // each compute unit several workgroups
+  const int half = a.turn.rot / 2, used = a.dim / 16, lanes = used > 8 ? 16 : used > 4 ? 8 : used > 2 ? 4 : used;
+  const int per = (a.side[0].heads + a.side[1].heads) * lanes;
+  a.abreast = 1;
+  int threads = (per + 63) / 64 * 64;
+  for (int n = 2; n * per <= kMostThreads && n * int64_t{512} <= a.tokens; ++n) {
+    const int t = (n * per + 63) / 64 * 64;
+    if (static_cast<int64_t>(n) * threads > static_cast<int64_t>(a.abreast) * t) {
+      a.abreast = n;
+      threads = t;
+    }
+  }
+  int64_t times = (a.tokens + a.abreast * int64_t{kWorkgroups} - 1) / (a.abreast * int64_t{kWorkgroups});
+  if (times > 16) times = 16;
+  if (times * a.abreast * half > kMaxTurns) times = kMaxTurns / (a.abreast * half);
+  a.batch = a.abreast * static_cast<int>(times < 1 ? 1 : times);
+  a.per_inverse = over32(per);
+  a.half_inverse = half > 0 ? over32(half) : 0;
+  const dim3 grid(static_cast<unsigned>((a.tokens + a.batch - 1) / a.batch), static_cast<unsigned>((threads + kMostThreads - 1) / kMostThreads));
+  const dim3 block(static_cast<unsigned>(threads < kMostThreads ? threads : kMostThreads));
+  if (a.turn.interleaved) return a.bf16 ? launch_wide<true, true>(a, grid, block) : launch_wide<false, true>(a, grid, block);
+  return a.bf16 ? launch_wide<true, false>(a, grid, block) : launch_wide<false, false>(a, grid, block);
 }
 
 }  // namespace

@@ -59,7 +59,7 @@ struct Turner {
     widen8<BF16>(p.own, x);
     widen8<BF16>(p.mate, z);
     if (turn->weight[side] != nullptr) {
-      const float r = inverse_norm(group_sum(squares(x), dim / 8), dim, turn->eps);
+      const float r = inverse_norm(group_sum(squares(x), dim / 8), turn->inv_dim, turn->eps);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         x[j] = normed(x[j], r, weights[side][c * 8 + j]);
@@ -80,7 +80,7 @@ struct Turner {
         y[j] = d < half ? turned_first(x[j], z[j], t) : turned_second(z[j], x[j], t);
       }
     }
-    return narrow8<BF16>(y);
+    return round8<BF16>(y);
   }
 };
 

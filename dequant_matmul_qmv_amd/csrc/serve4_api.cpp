@@ -42,7 +42,9 @@ mxq_status check_rotation(const std::string& f, const mxq_rotation* r, int64_t t
   out->weight[0] = r->q_weight;
   out->weight[1] = r->k_weight;
   out->weight_f32 = r->weight_dtype == MXQ_F32;
+  out->weight_wide = aligned(r->q_weight, 16) && aligned(r->k_weight, 16);
   out->eps = r->eps;
+  out->inv_dim = dim > 0 ? 1.0 / dim : 0.0;
   return MXQ_OK;
 }
 

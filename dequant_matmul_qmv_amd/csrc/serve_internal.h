@@ -75,7 +75,8 @@ struct TurnArgs {
   bool interleaved;
   const void* weight[2];     // of q, of k
   bool weight_f32;           // else of the values' type
-  double eps;
+  bool weight_wide;          // 16-byte aligned
+  double eps, inv_dim;       // inv_dim: 1 / dim
 };
 struct NormRopeArgs {
   RopeSide side[2];  // q, k
@@ -86,6 +87,8 @@ struct NormRopeArgs {
   hipStream_t stream;
   // set by the launcher
   int batch;         // tokens of a workgroup
+  int abreast;       // of them at a time
+  uint32_t per_inverse, half_inverse;  // 2^32 over a token's lanes, over rot / 2
 };
 hipError_t launch_norm_rope(const NormRopeArgs& a);
 

@@ -68,16 +68,43 @@ __device__ __forceinline__ Turn turn_by(int pos, float inv_freq) {
   return Turn{quadrant == 1 || quadrant == 2 ? -co : co, quadrant >= 2 ? -si : si};
 }
 
-// Pair i's turn of row t; `place` is the row's place in its sequence.
-__device__ __forceinline__ Turn turn_of(const TurnArgs& a, int i, int64_t t, int place) {
+// What pair i's turn of row t is made of; `place` is the row's place in its sequence.
+// Loads are answered in order, so these come before those of the rows: the turn is then
+// computed while the rows are on their way.
+struct TurnInput {
+  int pos;
+  float inv_freq;
+  __device__ __forceinline__ Turn turn() const { return turn_by(pos, inv_freq); }
+};
+__device__ __forceinline__ TurnInput turn_input(const TurnArgs& a, int i, int64_t t, int place) {
   const int axis = a.axis != nullptr ? min(max(a.axis[i], 0), a.axes - 1) : 0;
-  return turn_by(a.positions != nullptr ? a.positions[axis * a.axis_stride + t] : place, a.inv_freq[i]);
+  return TurnInput{a.positions != nullptr ? a.positions[axis * a.axis_stride + t] : place, a.inv_freq[i]};
+}
+__device__ __forceinline__ Turn turn_of(const TurnArgs& a, int i, int64_t t, int place) { return turn_input(a, i, t, place).turn(); }
+
+// Eight f32 values rounded to storage.  (The values are made opaque: a sum and its
+// rounding must not become one operation.)
+template <bool BF16>
+__device__ __forceinline__ u4 round8(const float (&f)[8]) {
+  uint32_t d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x = f[2 * i], y = f[2 * i + 1];
+    asm("" : "+v"(x), "+v"(y));
+    if constexpr (BF16) {
+      d[i] = pack_bf16_pair(x, y);
+    } else {
+      const h2 p = {static_cast<_Float16>(x), static_cast<_Float16>(y)};
+      d[i] = as_u32(p);
+    }
+  }
+  return u4{d[0], d[1], d[2], d[3]};
 }
 
 // f32(1 / sqrt(sum / dim + eps)): the instruction's estimate and two steps of
 // Newton's iteration in f64.
-__device__ __forceinline__ float inverse_norm(double sum, int dim, double eps) {
-  const double m = sum / static_cast<double>(dim) + eps;
+__device__ __forceinline__ float inverse_norm(double sum, double inv_dim, double eps) {
+  const double m = __builtin_fma(sum, inv_dim, eps);
   double y = __builtin_amdgcn_rsq(m);
   if (m > 0.0 && m < __builtin_inf()) {
 #pragma unroll
@@ -123,6 +150,22 @@ template <bool BF16>
 __device__ __forceinline__ float weight_at(const TurnArgs& a, int side, int d) {
   if (a.weight_f32) return static_cast<const float*>(a.weight[side])[d];
   return sb_to_f32<BF16>(static_cast<const uint16_t*>(a.weight[side])[d]);
+}
+// Eight of them, from a multiple of 8 on.
+template <bool BF16>
+__device__ __forceinline__ void weights8(const TurnArgs& a, int side, int d, float (&w)[8]) {
+  if (!a.weight_wide) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = weight_at<BF16>(a, side, d + i);
+  } else if (a.weight_f32) {
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    const f4* p = reinterpret_cast<const f4*>(static_cast<const float*>(a.weight[side]) + d);
+    const f4 x = p[0], y = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = x[i], w[4 + i] = y[i];
+  } else {
+    widen8<BF16>(*reinterpret_cast<const u4*>(static_cast<const uint16_t*>(a.weight[side]) + d), w);
+  }
 }
 
 }  // namespace mxq
