@@ -79,7 +79,8 @@ def _load():
 # The current stream's handle without the Stream object around it (1.7 us of a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = torch.cuda.current_device
+# The current device's index, without the check that the runtime has started: the tensors are on it.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _empty_like = torch.empty_like
 
 
@@ -194,22 +195,24 @@ def _weight(who, name, w, dim, dtype, dev):
 
 def _rotation(who, dev, n, dim, dtype, inv_freq, positions, axes, q_weight, k_weight, eps, interleaved):
     """The checked ``mxq_rotation`` of a call on n tokens."""
-    if inv_freq.dtype != _f32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    shape = inv_freq.shape
+    if inv_freq.dtype != _f32 or len(shape) != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"{who}: inv_freq must be a contiguous float32 vector")
-    half = inv_freq.shape[0]
+    half = shape[0]
     if 2 * half > dim:
         raise ValueError(f"{who}: {half} frequencies rotate {2 * half} values, a head has {dim}")
     if inv_freq.device != dev:
         _elsewhere(who, dev, inv_freq=inv_freq)
-    at, stride, rows, ap = None, n, 1, None
+    at, rows, ap = None, 1, None
     if positions is not None:
-        if positions.dtype != _i32 or positions.dim() not in (1, 2) or positions.shape[-1] != n or not positions.is_contiguous():
+        shape = positions.shape
+        if positions.dtype != _i32 or len(shape) not in (1, 2) or shape[-1] != n or not positions.is_contiguous():
             raise ValueError(f"{who}: positions must be a contiguous int32 tensor of shape [{n}] or [axes, {n}]")
         if positions.device != dev:
             _elsewhere(who, dev, positions=positions)
         at = positions.data_ptr()
-        if positions.dim() == 2:
-            rows = positions.shape[0]
+        if len(shape) == 2:
+            rows = shape[0]
     if axes is not None:
         if axes.dtype != _i32 or axes.shape != (half,) or not axes.is_contiguous():
             _ints(who, "axes", axes, (half,))
@@ -227,7 +230,7 @@ def _rotation(who, dev, n, dim, dtype, inv_freq, positions, axes, q_weight, k_we
         if qw is not None and k_code != code:
             raise ValueError(f"{who}: q_weight and k_weight must be of one type")
         code = k_code
-    return _RotationStruct(inv_freq.data_ptr(), at, stride, ap, rows, 2 * half, 1 if interleaved else 0,
+    return _RotationStruct(inv_freq.data_ptr(), at, n, ap, rows, 2 * half, 1 if interleaved else 0,
                            code, qw, kw, eps)
 
 

@@ -34,23 +34,21 @@ constexpr int64_t kPartTokens = 1 << 23;  // of a launch, whose grid ends below 
 template <bool BF16, bool INTER, bool STREAM>
 __global__ __launch_bounds__(kMostThreads) void norm_rope_wide_kernel(NormRopeArgs a) {
   __shared__ Turn turns[kMaxTurns];
-  const int half = a.turn.rot / 2, turned = a.turn.rot / 16, used = a.dim / 16;
+  const int half = a.turn.rot / 2, used = a.dim / 16;
   const int log2 = used > 8 ? 4 : used > 4 ? 3 : used > 2 ? 2 : used - 1, lanes = 1 << log2;
   const int heads = a.side[0].heads + a.side[1].heads, per = heads << log2, tid = threadIdx.x;
   // the lane's place: its token of those that the workgroup has at a time, its head and
-  // its 16-byte pieces there (the two halves of 8 pairs; interleaved, two that neighbours'
-  // pieces lie beside; behind the turned part, neighbours)
+  // its pieces there
   const int place = static_cast<int>(blockIdx.y) * kMostThreads + tid, sub = a.abreast == 1 ? 0 : static_cast<int>(__umulhi(place, a.per_inverse));
   const int slot = place - sub * per, c = slot & (lanes - 1);
   int head = slot >> log2;
   const bool here = head < heads && sub < a.abreast && c < used;
   const int side = head < a.side[0].heads ? 0 : 1;
   if (side == 1) head -= a.side[0].heads;
-  const int lo_at = INTER || c < turned ? 8 * c : 16 * c, hi_at = INTER ? 8 * (used + c) : c < turned ? half + 8 * c : 16 * c + 8;
-  const bool lo_turns = INTER ? lo_at < a.turn.rot : c < turned, hi_turns = INTER && hi_at < a.turn.rot;
+  const HeadLane at = head_lane<INTER>(c, used, a.turn.rot);
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.batch;
   const int tokens = a.tokens - t0 < a.batch ? static_cast<int>(a.tokens - t0) : a.batch;
-  const RopeSide& s = a.side[side];
+  const RopeSide s = side == 0 ? a.side[0] : a.side[1];
   const uint16_t* in = s.in + (t0 + sub) * s.in_token + head * s.in_head;
   uint16_t* out = s.out + (t0 + sub) * s.out_token + head * s.out_head;
   const int64_t in_step = a.abreast * s.in_token, out_step = a.abreast * s.out_token;
@@ -72,16 +70,16 @@ __global__ __launch_bounds__(kMostThreads) void norm_rope_wide_kernel(NormRopeAr
     return turn_input(a.turn, i - tok * half, t0 + tok, 0);
   };
   if (tid < all_turns) mine = input(tid);
-  const bool norm = a.turn.weight[side] != nullptr && here, norms = a.turn.weight[0] != nullptr || a.turn.weight[1] != nullptr;
+  const bool norm = side_weight(a.turn, side) != nullptr && here, norms = a.turn.weight[0] != nullptr || a.turn.weight[1] != nullptr;
   float wx[8], wz[8];
   if (norm) {
-    weights8<BF16>(a.turn, side, lo_at, wx);
-    weights8<BF16>(a.turn, side, hi_at, wz);
+    weights8<BF16>(a.turn, side, at.lo, wx);
+    weights8<BF16>(a.turn, side, at.hi, wz);
   }
   u4 lo = u4{0, 0, 0, 0}, hi = lo;
   if (here && sub < tokens) {
-    lo = get(in + lo_at);
-    hi = get(in + hi_at);
+    lo = get(in + at.lo);
+    hi = get(in + at.hi);
   }
   if (tid < all_turns) turns[tid] = mine.turn();
   for (int i = tid + blockDim.x; i < all_turns; i += blockDim.x) turns[i] = input(i).turn();
@@ -93,8 +91,8 @@ __global__ __launch_bounds__(kMostThreads) void norm_rope_wide_kernel(NormRopeAr
     widen8<BF16>(hi, z);
     in += in_step;
     if (here && tok + a.abreast < tokens) {
-      lo = get(in + lo_at);
-      hi = get(in + hi_at);
+      lo = get(in + at.lo);
+      hi = get(in + at.hi);
     }
     if (norms) {
       const float r = inverse_norm(group_sum(squares(x) + squares(z), lanes), a.turn.inv_dim, a.turn.eps);
@@ -107,27 +105,9 @@ __global__ __launch_bounds__(kMostThreads) void norm_rope_wide_kernel(NormRopeAr
       }
     }
     if (here && tok < tokens) {
-      if constexpr (INTER) {
-        const auto turn4 = [](float(&y)[8], const Turn* by) {
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float p = y[i], q = y[i + 1];
-            y[i] = turned_first(p, q, by[i / 2]);
-            y[i + 1] = turned_second(p, q, by[i / 2]);
-          }
-        };
-        if (lo_turns) turn4(x, t + lo_at / 2);
-        if (hi_turns) turn4(z, t + hi_at / 2);
-      } else if (lo_turns) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = x[i], q = z[i];
-          x[i] = turned_first(p, q, t[lo_at + i]);
-          z[i] = turned_second(p, q, t[lo_at + i]);
-        }
-      }
-      put(out + lo_at, round8<BF16>(x));
-      put(out + hi_at, round8<BF16>(z));
+      turn16<INTER>(x, z, at, t);
+      put(out + at.lo, round8<BF16>(x));
+      put(out + at.hi, round8<BF16>(z));
     }
     out += out_step;
     t += a.abreast * half;
@@ -145,7 +125,7 @@ __global__ __launch_bounds__(256) void norm_rope_narrow_kernel(NormRopeArgs a) {
   for (int h0 = 0; h0 < heads; h0 += 4) {
     const int h = h0 + wave, side = h < a.side[0].heads ? 0 : 1, head = side == 0 ? h : h - a.side[0].heads;
     const bool real = h < heads;
-    const RopeSide& s = a.side[side];
+    const RopeSide s = side == 0 ? a.side[0] : a.side[1];
     const uint16_t* in = s.in + t * s.in_token + head * s.in_head;
     uint16_t* out = s.out + t * s.out_token + head * s.out_head;
     float x[kMaxDim / 64];
@@ -156,7 +136,7 @@ __global__ __launch_bounds__(256) void norm_rope_narrow_kernel(NormRopeArgs a) {
       x[j] = real && d < a.dim ? sb_to_f32<BF16>(in[d]) : 0.0f;
       sum = __builtin_fma(static_cast<double>(x[j]), static_cast<double>(x[j]), sum);
     }
-    if (a.turn.weight[side] != nullptr) {  // the same for a whole wave
+    if (side_weight(a.turn, side) != nullptr) {  // the same for a whole wave
       const float r = inverse_norm(wave_sum(sum), a.turn.inv_dim, a.turn.eps);
 #pragma unroll
       for (int j = 0; j < kMaxDim / 64; ++j)

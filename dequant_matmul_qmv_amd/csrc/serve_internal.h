@@ -149,7 +149,8 @@ struct RopeAppendArgsOf {
   bool q_wide;            // q's rows, in and out, are 16-byte aligned
   TurnArgs turn;
   // set by the launcher
-  int pages, units;       // workgroups of pages (8 bits), of groups of 8 tokens
+  int pages, units;       // pages (8 bits) and groups of 8 tokens, at most
+  int q_all, q_units, q_blocks;  // blocks of a row's heads, those of a workgroup, and a group's workgroups
 };
 using RopeAppendArgs = RopeAppendArgsOf<KvPool>;
 using RopeAppend4Args = RopeAppendArgsOf<KvPool4>;

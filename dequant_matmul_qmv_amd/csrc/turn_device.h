@@ -145,11 +145,55 @@ __device__ __forceinline__ float turned_second(float a, float b, Turn t) {
   return x + y;
 }
 
-// A side's norm weight d in f32.
+// A lane's 16-byte pieces of a head of 16 * `used` values, of which it is lane c: the two
+// halves of 8 pairs; interleaved, two that neighbours' pieces lie beside; behind the turned
+// part, neighbours.  rot is a multiple of 16.
+struct HeadLane {
+  int lo, hi;
+  bool lo_turns, hi_turns;  // hi_turns: interleaved; the halves turn together
+};
+template <bool INTER>
+__device__ __forceinline__ HeadLane head_lane(int c, int used, int rot) {
+  const bool turned = c < rot / 16;
+  HeadLane l;
+  l.lo = INTER || turned ? 8 * c : 16 * c;
+  l.hi = INTER ? 8 * (used + c) : turned ? rot / 2 + 8 * c : 16 * c + 8;
+  l.lo_turns = INTER ? l.lo < rot : turned;
+  l.hi_turns = INTER && l.hi < rot;
+  return l;
+}
+// Its values turned, by the row's table.
+template <bool INTER>
+__device__ __forceinline__ void turn16(float (&x)[8], float (&z)[8], const HeadLane& l, const Turn* t) {
+  if constexpr (INTER) {
+    const auto turn4 = [](float(&y)[8], const Turn* by) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float p = y[i], q = y[i + 1];
+        y[i] = turned_first(p, q, by[i / 2]);
+        y[i + 1] = turned_second(p, q, by[i / 2]);
+      }
+    };
+    if (l.lo_turns) turn4(x, t + l.lo / 2);
+    if (l.hi_turns) turn4(z, t + l.hi / 2);
+  } else if (l.lo_turns) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = x[i], q = z[i];
+      x[i] = turned_first(p, q, t[l.lo + i]);
+      z[i] = turned_second(p, q, t[l.lo + i]);
+    }
+  }
+}
+
+// A side's weights.  (A side that differs by lane must not index the arguments: they would
+// be copied to scratch memory, and every pointer in them with them.)
+__device__ __forceinline__ const void* side_weight(const TurnArgs& a, int side) { return side == 0 ? a.weight[0] : a.weight[1]; }
+// Norm weight d in f32.
 template <bool BF16>
 __device__ __forceinline__ float weight_at(const TurnArgs& a, int side, int d) {
-  if (a.weight_f32) return static_cast<const float*>(a.weight[side])[d];
-  return sb_to_f32<BF16>(static_cast<const uint16_t*>(a.weight[side])[d]);
+  if (a.weight_f32) return static_cast<const float*>(side_weight(a, side))[d];
+  return sb_to_f32<BF16>(static_cast<const uint16_t*>(side_weight(a, side))[d]);
 }
 // Eight of them, from a multiple of 8 on.
 template <bool BF16>
@@ -159,12 +203,12 @@ __device__ __forceinline__ void weights8(const TurnArgs& a, int side, int d, flo
     for (int i = 0; i < 8; ++i) w[i] = weight_at<BF16>(a, side, d + i);
   } else if (a.weight_f32) {
     typedef float f4 __attribute__((ext_vector_type(4)));
-    const f4* p = reinterpret_cast<const f4*>(static_cast<const float*>(a.weight[side]) + d);
+    const f4* p = reinterpret_cast<const f4*>(static_cast<const float*>(side_weight(a, side)) + d);
     const f4 x = p[0], y = p[1];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = x[i], w[4 + i] = y[i];
   } else {
-    widen8<BF16>(*reinterpret_cast<const u4*>(static_cast<const uint16_t*>(a.weight[side]) + d), w);
+    widen8<BF16>(*reinterpret_cast<const u4*>(static_cast<const uint16_t*>(side_weight(a, side)) + d), w);
   }
 }
 

@@ -345,6 +345,35 @@ def test_values_of_4_bits(t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1, -1])
+def test_every_scale_of_4_bits(sign):
+    """Heads whose range is 15 times each scale there is, f16's values: the smallest steps, all mantissas and exponents.
+    Their other values lie at and beside the middles between codes, where an inverse a step off would show."""
+    dim, block = 64, 128
+    scales = torch.cat([torch.arange(1, 64) * 2.0 ** -20] + [torch.arange(64, 128) * 2.0 ** e for e in range(-20, 6)]).double()
+    scales = scales[scales <= 4064]
+    middle = (torch.arange(dim) % 15 + 0.5).double()
+    middle[15:30] *= 1 - 2.0 ** -11
+    middle[30:45] *= 1 + 2.0 ** -11
+    x = (scales[:, None] * middle).half()
+    x[:, -1] = (15 * scales).half()                             # 11 bits at most: exact
+    assert torch.equal(x[:, -1].double(), 15 * scales) and float(x.max()) < 65504
+    x = sign * x[:, None]
+    n = x.shape[0]
+    blocks = -(-n // block)
+    table = torch.arange(blocks, dtype=torch.int32)[None]
+    pool = random_pool4(blocks, 1, block, dim, torch.Generator().manual_seed(2))
+    want = append4_ref(pool, x, x.flip(0), table, [n], [n], block)
+    cache = _cache(pool)
+    mxq.mxq_kv_append(cache, x.to(DEV), x.flip(0).to(DEV), table.to(DEV), _i32([n]), _i32([0, n]))
+    torch.cuda.synchronize()
+    for name, a, b in zip(("k", "v", "k_scale", "v_scale"), _tensors(cache), want):
+        assert np.array_equal(a.numpy().view(b.dtype), b), name
+    held = _tensors(cache)[2].numpy().view(np.uint16).reshape(-1)[:n] & 0xFFF0
+    assert np.array_equal(held.view(np.float16).astype(np.float64), scales.numpy())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("new", [1, 70])
 def test_the_longest_sequence(bits, new):
