@@ -102,9 +102,16 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
       }
     return p;
   };
+  Pages4 now_at;  // of the chunk at hand
   // Is the page there, and (a page past the sequence's end may be anyone's, or never written) some of its keys?
-  auto there = [&](int c, const Pages4& p, int u, int g) {
-    return p.at[u][g] >= 0 && p.at[u][g] < static_cast<int>(a.pool.blocks) && c * kChunk + u * 32 + g * 16 < limit;
+  auto there = [&](int c, const Pages4& p, int u, int g) -> bool {
+    return (static_cast<uint32_t>(p.at[u][g]) < static_cast<uint32_t>(a.pool.blocks)) & (c * kChunk + u * 32 + g * 16 < limit);
+  };
+  // The same for the lane's 8 tokens of a half.
+  auto lane_there = [&](int c, int u) -> bool {
+    if constexpr (!SMALL) return there(c, now_at, u, 0);
+    const bool first = there(c, now_at, u, 0), second = there(c, now_at, u, 1);
+    return h >= 2 ? second : first;
   };
   // tokens before a half (or its second 16 tokens), in all of the pool's
   auto tokens_before = [&](int c, const Pages4& p, int u, int g) {
@@ -143,7 +150,8 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
   // the first chunk is on its way while the queries are read
   Raw4<DIM> raw;
   const int c_first = __builtin_amdgcn_readfirstlane(c_begin + wave);
-  Pages4 now_at = pages_of(c_first), ahead = pages_of(c_first + WAVES);  // past the end: -1, or a page that is not used
+  now_at = pages_of(c_first);
+  Pages4 ahead = pages_of(c_first + WAVES);  // past the end: -1, or a page that is not used
   if (c_first < c_end) {
     load_k(c_first, now_at, raw);
     load_v(c_first, now_at, raw);
@@ -214,11 +222,11 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
   // to 8192 keys), v's do after it
   auto step = [&](int c, Raw4<DIM>& r) {
     const bool more = c + WAVES < c_end;
-    bool whole = c * kChunk >= all_from && c * kChunk <= all_upto - kChunk;
+    bool whole = (c * kChunk >= all_from) & (c * kChunk <= all_upto - kChunk);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int g = 0; g < (SMALL ? 2 : 1); ++g) whole = whole && there(c, now_at, u, g);
+      for (int g = 0; g < (SMALL ? 2 : 1); ++g) whole = whole & there(c, now_at, u, g);
     f4 s[MT][4];
     h2 k_scale[2][4];
 #pragma unroll
@@ -254,8 +262,7 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
     if (!whole) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bool ok = SMALL && h >= 2 ? there(c, now_at, u, 1) : there(c, now_at, u, 0);
-        r.vs[u] = first_words(r.vs[u], ok ? min(limit - (c * kChunk + u * 32 + 8 * h), 8) : 0);
+        r.vs[u] = first_words(r.vs[u], lane_there(c, u) ? max(min(limit - (c * kChunk + u * 32 + 8 * h), 8), 0) : 0);
       }
     }
     // the largest scale so far, as an exponent field
@@ -283,12 +290,14 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
         }
       if (!whole) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const bool ok = SMALL && h >= 2 ? there(c, now_at, t >> 1, 1) : there(c, now_at, t >> 1, 0);
+        for (int u = 0; u < 2; ++u) {
+          // of the lane's 8 tokens, the seen ones are `seen` from `begin` on
+          const int key = c * kChunk + u * 32 + 8 * h, begin = max(from[mt] - key, 0), end = min(upto[mt] - key, 8);
+          const uint32_t seen = lane_there(c, u) ? max(end - begin, 0) : 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = c * kChunk + (t >> 1) * 32 + 8 * h + 2 * (t & 1) + (i >> 1) + 4 * (i & 1);
-            s[mt][t][i] = ok && key >= from[mt] && key < upto[mt] ? s[mt][t][i] : kNegInf;
+          for (int j = 0; j < 8; ++j) {
+            f4& t = s[mt][2 * u + ((j & 3) >> 1)];
+            t[2 * (j & 1) + (j >> 2)] = static_cast<uint32_t>(j - begin) < seen ? t[2 * (j & 1) + (j >> 2)] : kNegInf;
           }
         }
       }

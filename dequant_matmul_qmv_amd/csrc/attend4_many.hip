@@ -121,9 +121,10 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend4_many_kernel(Attend4Ar
   const int kt = tid >> 2, kc = tid & 3, vg = tid >> 5, vd = (tid & 31) * W;
   // the row of S^T at which key kt's score is where its token is in a word of v
   const int place = 2 * (kt & 3) + ((kt >> 2) & 1), kr = (kt & ~15) + 4 * ((kt >> 3) & 1) + (place & 3) + 8 * (place >> 2);
-  uint32_t kraw[W], vraw[W], ks = 0;
+  uint32_t kraw[W], vraw[W];
+  uint16_t ks = 0;
   u4 vs = u4{0, 0, 0, 0};
-  int pk, pv, there = 0;
+  int pk = -1, pv = -1, valid = 0;  // the next stage's pages; of a group's 8 tokens, those that are there
   const int block_log2 = 31 - __builtin_clz(block);
   const uint32_t nb = static_cast<uint32_t>(a.pool.blocks);
   auto pages = [&](int s) {
@@ -141,25 +142,24 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend4_many_kernel(Attend4Ar
       w[0] = x.x, w[1] = x.y;
     }
   };
+  // what is fetched is first looked at by `put`, after the products of the stage before
   auto fetch = [&](int s) {
-    {
-      const int64_t p = static_cast<uint32_t>(pk) < nb ? pk : 0;
-      const int64_t at = (p * hk + head) * block + ((s * kStage + kt) & (block - 1));
-      load_words(a.pool.k + at * (DIM / 8) + kc * W, kraw);
-      ks = a.pool.k_scale[at];
-    }
     // a page past the sequence's end may be anyone's, or never written
     const int key = s * kStage + vg * 8;
     const bool ok = static_cast<uint32_t>(pv) < nb && key < limit;
-    const int64_t ph = static_cast<int64_t>(ok ? pv : 0) * hk + head;
-    const int slot = key & (block - 1);
-    load_words(a.pool.v + (ph * (block / 8) + slot / 8) * DIM + vd, vraw);
-    vs = first_words(*reinterpret_cast<const u4*>(a.pool.v_scale + ph * block + slot), ok ? min(limit - key, 8) : 0);
-    there = ok;
+    const int64_t p = static_cast<uint32_t>(pk) < nb ? pk : 0, q = ok ? pv : 0;
+    const int64_t k_token = (p * hk + head) << block_log2, v_token = (q * hk + head) << block_log2;
+    const uint32_t k_slot = (s * kStage + kt) & (block - 1), v_slot = key & (block - 1);
+    load_words(a.pool.k + k_token * (DIM / 8) + (k_slot * (DIM / 8) + kc * W), kraw);
+    ks = (a.pool.k_scale + k_token)[k_slot];
+    load_words(a.pool.v + v_token * (DIM / 8) + (v_slot * (DIM / 8) + vd), vraw);
+    vs = *reinterpret_cast<const u4*>(a.pool.v_scale + v_token + v_slot);
+    valid = ok ? max(min(limit - key, 8), 0) : 0;
   };
   const Fields fields;
   auto put = [&](Stage4<DIM>& st) {
-    const uint32_t both = ks | (ks << 16);
+    if (__any(valid < 8)) vs = first_words(vs, valid);
+    const uint32_t both = ks * 0x10001u;
     const h2 scale = as_h2(both & 0x7FF07FF0u), zero = fields.with64(both << 4);
     const Scales8 k_scales{{scale, scale, scale, scale}, {zero, zero, zero, zero}}, v_scales = scales8(fields, vs);
 #pragma unroll
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend4_many_kernel(Attend4Ar
       st.k[k_at<DIM>(kr, kc * W + w)] = __builtin_bit_cast(u4, values8(fields, kraw[w], k_scales));
       st.v[v_at(vd + w, vg)] = __builtin_bit_cast(u4, values8(fields, vraw[w], v_scales));
     }
-    if ((tid & 63) == 0) st.there[tid >> 6] = there;  // of both 8-token groups: a page has 16 tokens at least
+    if ((tid & 63) == 0) st.there[tid >> 6] = valid > 0;  // of both 8-token groups: a page has 16 tokens at least
   };
 
   f16x acc[DB];
@@ -199,12 +199,16 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend4_many_kernel(Attend4Ar
     float c = factor, mx = kNegInf;
     if (!(all_there && s * kStage >= all_from && s * kStage <= all_upto - kStage)) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int g = 0; g < 4; ++g) {
+        // of the lane's 8 tokens, the seen ones are `seen` from `begin` on
+        const int key = s * kStage + g * 16 + 8 * h, begin = max(from - key, 0), end = min(upto - key, 8);
+        const uint32_t seen = st.there[g] ? max(end - begin, 0) : 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int g = 2 * b + (i >> 3), j = i & 7, key = s * kStage + g * 16 + 8 * h + (j >> 1) + 4 * (j & 1);
-          x[b][i] = st.there[g] && key >= from && key < upto ? x[b][i] * factor : kNegInf;
+        for (int j = 0; j < 8; ++j) {
+          const int i = 8 * (g & 1) + j, token = (j >> 1) + 4 * (j & 1);
+          x[g >> 1][i] = static_cast<uint32_t>(token - begin) < seen ? x[g >> 1][i] * factor : kNegInf;
         }
+      }
       c = 1.0f;
     }
 #pragma unroll
