@@ -811,7 +811,9 @@ int64_t most_units(const Args& a) { return a.tokens / kGroup + 2 * static_cast<i
 hipError_t launch_rope_append(const RopeAppendArgs& given) {
   if (given.starts == nullptr) return launch_one(given);
   RopeAppendArgs a = given;
-  a.pages = static_cast<int>(a.tokens / a.pool.block + 2 * static_cast<int64_t>(a.seqs));
+  const int64_t pages = a.tokens / a.pool.block + 2 * static_cast<int64_t>(a.seqs);
+  if (!grid_fits(pages, 256) || !grid_fits(most_units(a), 256)) return kTooLarge;  // (and both are within an int)
+  a.pages = static_cast<int>(pages);
   a.units = a.q.heads > 0 ? static_cast<int>(most_units(a)) : 0;
   switch (a.pool.dim * a.pool.block / 2048) {
     case 8: return launch_pages<4, 512>(a);
@@ -824,8 +826,8 @@ hipError_t launch_rope_append(const RopeAppendArgs& given) {
 hipError_t launch_rope_append4(const RopeAppend4Args& given) {
   if (given.starts == nullptr) return launch_one(given);
   RopeAppend4Args a = given;
+  if (!grid_fits(most_units(a), mode_of(a) != kAnyRows ? kGroupThreads : 256)) return kTooLarge;
   a.units = static_cast<int>(most_units(a));
-  if (!grid_fits(a.units, 256)) return kTooLarge;
   if (mode_of(a) != kAnyRows) {
     a.q_all = ((a.q.heads + 2 * a.pool.kv_heads) * (a.pool.dim / 16) + 63) / 64;
     a.q_units = units_of(a.q_all, a.units);

@@ -85,6 +85,13 @@ def test_refusals(bits):
     assert _call(bits, heads=0, blocks=0, k=None, v=None, ks=None, vs=None, **{n: v for n, v in ok.items() if n not in ("lens", "table")}) == mxq.MXQ_OK
 
 
+@pytest.mark.parametrize("bits,tokens,seqs", [(4, 2 ** 31 - 1, 1), (4, 80000000, 1), (4, 2, 2 ** 31 - 1), (4, 2, 2 ** 30),
+                                              (8, 2 ** 31 - 1, 1), (8, 2, 2 ** 31 - 1), (8, 2, 2 ** 30)])
+def test_refusals_of_grids(bits, tokens, seqs):
+    """A launch of 2^32 threads or more is refused by name before anything is enqueued."""
+    assert _call(bits, tokens=tokens, seqs=seqs, starts=P) == mxq.MXQ_ERR_UNSUPPORTED
+
+
 def test_cache_refusals_without_a_gpu():
     z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t)  # noqa: E731
     with pytest.raises(TypeError):
