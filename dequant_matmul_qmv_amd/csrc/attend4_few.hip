@@ -9,7 +9,10 @@
 //
 // Bound: HBM, the cache read once (keys * kv heads * (dim + 4) bytes), and beside it
 // the vector ALU, which unpacks two codes where the 8-bit cache has one in the same
-// byte.  The key axis is divided over workgroups as there (attend_split.h).
+// byte.  The key axis is divided over workgroups as there (attend_split.h).  Measured: three
+// sequences of 131000 keys of 128 values 90 us (4.6 TB/s; over 8 bits 191), 96 of up to
+// 8192 keys 49 (8 bits 68).  Short parts cost their code's instruction fetches: masked
+// chunks are handled without branches (one sequence of 913 keys 10.7 -> 10.2 us).
 //
 // Both products run on the matrix cores straight from registers.  S^T = K Q^T, keys as
 // 16 rows, leaves lane group h four keys of one query row in each tile; with the rows

@@ -10,7 +10,9 @@
 // scale and its zero point share a 16-bit word, f16 with z as its lowest bits.
 // A quotient is taken in f64 and rounded to f32 once.
 //
-// Bound: HBM for prompts, launch and dependent loads for single tokens.
+// Bound: the vector ALU and HBM for prompts (4 bits, 224 MB in 53 us: 4.2 TB/s; without
+// norms 181 MB in 38), dependent loads for single tokens (lens, table, scale or words: 64
+// tokens into 4 bits 6.0 us) and, for 8 bits, v's stores of a byte to a line (256 tokens 10.6).
 #include "append_device.h"
 #include "turn_device.h"
 
