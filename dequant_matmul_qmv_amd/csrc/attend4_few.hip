@@ -11,7 +11,7 @@
 // the vector ALU, which unpacks two codes where the 8-bit cache has one in the same
 // byte.  The key axis is divided over workgroups as there (attend_split.h).  Measured: three
 // sequences of 131000 keys of 128 values 90 us (4.6 TB/s; over 8 bits 191), 96 of up to
-// 8192 keys 49 (8 bits 68).  Short parts cost their code's instruction fetches: masked
+// 8192 keys 44 (8 bits 68).  Short parts cost their code's instruction fetches: masked
 // chunks are handled without branches (one sequence of 913 keys 10.7 -> 10.2 us).
 //
 // Both products run on the matrix cores straight from registers.  S^T = K Q^T, keys as
@@ -72,8 +72,10 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
   constexpr int KW = DIM / 32, DP = DIM / 64, kRows = 16 * MT;
   __shared__ float join[WAVES][16][DIM + 4];
   __shared__ float join_m[WAVES][16], join_l[WAVES][16];
-  const Part part = find_part<MT>(a, blockIdx.x, -1);
-  if (!part.any) return;
+  // (a workgroup of more waves takes all keys of its rows: parts are one each)
+  const Part part = WAVES == kFewWaves ? find_part_long_first<MT>(a, blockIdx.x) : find_part<MT>(a, blockIdx.x, -1);
+  // (starts that descend may give more parts than there are slots: not taken)
+  if (!part.any || static_cast<uint32_t>(part.base + part.nth) >= static_cast<uint32_t>(a.slots)) return;
   const int hk = a.pool.kv_heads, block = a.pool.block, block_log2 = 31 - __builtin_clz(block);
   const int head = part.nth % hk, rest = part.nth / hk, rg = rest % part.share.groups, split = rest / part.share.groups;
   const SeqSpan sp = seq_span(a, part.seq);
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
                     static_cast<uint32_t>(o[2]) | (static_cast<uint32_t>(o[3]) << 16)};
           if (a.lse && d == 0) a.lse[at] = log_sum(ref, total);
         } else {
-          const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + i;
+          const int64_t at = static_cast<int64_t>(part.base + part.nth) * kRows + i;
           *reinterpret_cast<f4*>(a.part + at * DIM + d) = y;
           if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = float2{top, total};
         }

@@ -54,12 +54,11 @@ struct Part {
   Share share;
 };
 
-// Where slot `slot` lies, or (slot < 0) sequence `seq`.  Run by whole waves.
+// Chunks of a part.  `mine` is left with the lane's share of up to 64 sequences.
 template <int MT, typename Args>
-__device__ Part find_part(const Args& a, int slot, int seq) {
+__device__ __forceinline__ int part_step(const Args& a, Share& mine) {
   const int lane = threadIdx.x & 63, hk = a.pool.kv_heads;
   long long total = 0;
-  Share mine{};
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     mine = share_of<MT>(a, s0 + lane);
     total += static_cast<long long>(mine.chunks) * mine.groups * hk;
@@ -70,8 +69,16 @@ __device__ Part find_part(const Args& a, int slot, int seq) {
   // sequences: 48 us with parts of 9 chunks, 45 with 12).
   long long even = (total + a.target - 1) / a.target;
   if (even >= a.long_chunks) even *= 2;
+  return static_cast<int>((max(even, static_cast<long long>(a.min_chunks)) + kFewWaves - 1) / kFewWaves * kFewWaves);
+}
+
+// Where slot `slot` lies, or (slot < 0) sequence `seq`.  Run by whole waves.
+template <int MT, typename Args>
+__device__ Part find_part(const Args& a, int slot, int seq) {
+  const int lane = threadIdx.x & 63, hk = a.pool.kv_heads;
+  Share mine{};
   Part p{};
-  p.step = static_cast<int>((max(even, static_cast<long long>(a.min_chunks)) + kFewWaves - 1) / kFewWaves * kFewWaves);
+  p.step = part_step<MT>(a, mine);
   int before = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     if (a.seqs > 64) mine = share_of<MT>(a, s0 + lane);
@@ -92,6 +99,49 @@ __device__ Part find_part(const Args& a, int slot, int seq) {
       return p;
     }
     before += last_lane(sum);
+  }
+  return p;
+}
+
+// The part that workgroup `index` takes where long parts go first: whole ones, then the
+// sequences' ends of at least half a part, then the others.  What is left for the last
+// workgroups is short (96 sequences of 5 .. 8192 keys over 4 bits: 44 us, by sequence 49,
+// with two kinds instead of three 51).  Its slot is base + nth, as above.
+template <int MT, typename Args>
+__device__ Part find_part_long_first(const Args& a, int index) {
+  const int lane = threadIdx.x & 63, hk = a.pool.kv_heads;
+  Share last{};
+  Part p{};
+  p.step = part_step<MT>(a, last);
+  const bool kept = a.seqs <= 128;  // in registers: `first` and `last`
+  const Share first = a.seqs > 64 && kept ? share_of<MT>(a, lane) : last;
+#pragma unroll 1
+  for (int kind = 0; kind < 3; ++kind) {
+    int before = 0, slots = 0;
+    for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+      const Share mine = kept ? (s0 == 0 ? first : last) : share_of<MT>(a, s0 + lane);
+      const int rows = mine.groups * hk, whole = mine.chunks / p.step, rest = mine.chunks - whole * p.step;
+      const int splits = max(1, whole + (rest > 0)), end = rest >= p.step / 2 ? 1 : 2;
+      const int count = rows * (kind == 0 ? whole : kind == end ? splits - whole : 0), all = rows * splits;
+      const int sum = wave_scan(count), all_sum = wave_scan(all);
+      const unsigned long long hit = __ballot(before + sum > index);
+      if (hit != 0) {
+        const int src = __builtin_amdgcn_readfirstlane(__ffsll(hit) - 1);
+        p.any = true;
+        p.seq = s0 + src;
+        p.base = slots + __builtin_amdgcn_readlane(all_sum, src) - __builtin_amdgcn_readlane(all, src);
+        p.nth = index - before - (__builtin_amdgcn_readlane(sum, src) - __builtin_amdgcn_readlane(count, src)) +
+                (kind > 0 ? __builtin_amdgcn_readlane(rows * whole, src) : 0);
+        p.splits = __builtin_amdgcn_readlane(splits, src);
+        p.share.c0 = __builtin_amdgcn_readlane(mine.c0, src);
+        p.share.chunks = __builtin_amdgcn_readlane(mine.chunks, src);
+        p.share.groups = __builtin_amdgcn_readlane(mine.groups, src);
+        return p;
+      }
+      before += last_lane(sum);
+      slots += last_lane(all_sum);
+    }
+    index -= before;
   }
   return p;
 }
