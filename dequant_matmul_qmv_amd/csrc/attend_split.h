@@ -54,16 +54,9 @@ struct Part {
   Share share;
 };
 
-// Chunks of a part.  `mine` is left with the lane's share of up to 64 sequences.
-template <int MT, typename Args>
-__device__ __forceinline__ int part_step(const Args& a, Share& mine) {
-  const int lane = threadIdx.x & 63, hk = a.pool.kv_heads;
-  long long total = 0;
-  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
-    mine = share_of<MT>(a, s0 + lane);
-    total += static_cast<long long>(mine.chunks) * mine.groups * hk;
-  }
-  total = wave_sum(total);
+// Chunks of a part, of all sequences' `total`.
+template <typename Args>
+__device__ __forceinline__ int part_step(const Args& a, long long total) {
   // As many workgroups a compute unit as the kernel asks for, or half of them where
   // they would have its long parts; parts of whole rounds of the four waves (8 bits, 64
   // sequences: 48 us with parts of 9 chunks, 45 with 12).
@@ -76,9 +69,14 @@ __device__ __forceinline__ int part_step(const Args& a, Share& mine) {
 template <int MT, typename Args>
 __device__ Part find_part(const Args& a, int slot, int seq) {
   const int lane = threadIdx.x & 63, hk = a.pool.kv_heads;
+  long long total = 0;
   Share mine{};
+  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+    mine = share_of<MT>(a, s0 + lane);
+    total += static_cast<long long>(mine.chunks) * mine.groups * hk;
+  }
   Part p{};
-  p.step = part_step<MT>(a, mine);
+  p.step = part_step(a, wave_sum(total));
   int before = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += 64) {
     if (a.seqs > 64) mine = share_of<MT>(a, s0 + lane);
@@ -110,9 +108,14 @@ __device__ Part find_part(const Args& a, int slot, int seq) {
 template <int MT, typename Args>
 __device__ Part find_part_long_first(const Args& a, int index) {
   const int lane = threadIdx.x & 63, hk = a.pool.kv_heads;
+  long long total = 0;
   Share last{};
+  for (int s0 = 0; s0 < a.seqs; s0 += 64) {
+    last = share_of<MT>(a, s0 + lane);
+    total += static_cast<long long>(last.chunks) * last.groups * hk;
+  }
   Part p{};
-  p.step = part_step<MT>(a, last);
+  p.step = part_step(a, wave_sum(total));
   const bool kept = a.seqs <= 128;  // in registers: `first` and `last`
   const Share first = a.seqs > 64 && kept ? share_of<MT>(a, lane) : last;
 #pragma unroll 1
