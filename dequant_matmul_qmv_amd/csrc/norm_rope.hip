@@ -39,7 +39,9 @@ __global__ __launch_bounds__(kMostThreads) void norm_rope_wide_kernel(NormRopeAr
   const int heads = a.side[0].heads + a.side[1].heads, per = heads << log2, tid = threadIdx.x;
   // the lane's place: its token of those that the workgroup has at a time, its head and
   // its pieces there
-  const int place = static_cast<int>(blockIdx.y) * kMostThreads + tid, sub = a.abreast == 1 ? 0 : static_cast<int>(__umulhi(place, a.per_inverse));
+  const int place = static_cast<int>(blockIdx.y) * kMostThreads + tid;
+  // (one lane a token: 1 has no inverse below 2^32)
+  const int sub = a.abreast == 1 ? 0 : per == 1 ? place : static_cast<int>(__umulhi(place, a.per_inverse));
   const int slot = place - sub * per, c = slot & (lanes - 1);
   int head = slot >> log2;
   const bool here = head < heads && sub < a.abreast && c < used;
@@ -174,7 +176,8 @@ hipError_t launch_wide(const NormRopeArgs& a, dim3 grid, dim3 block) {
   return hipGetLastError();
 }
 
-// ceil(2^32 / d): __umulhi with it divides numbers up to 2^16 by d up to 2^12.
+// ceil(2^32 / d): __umulhi with it divides numbers up to 2^16 by d of 2 up to 2^12 (of 1 it
+// would be 2^32: the kernel does not divide there).
 uint32_t over32(int d) { return static_cast<uint32_t>(((uint64_t{1} << 32) + d - 1) / d); }
 
 hipError_t launch_part(NormRopeArgs a) {
