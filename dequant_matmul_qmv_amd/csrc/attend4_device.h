@@ -49,14 +49,19 @@ __device__ __forceinline__ h8 values8(const Fields& f, uint32_t w, const Scales8
                   as_u32((f.with64(w >> 4) - s.zero64[2]) * s.scale[2]), as_u32((f.with64(w >> 8) - s.zero64[3]) * s.scale[3])});
 }
 
-// Scale words of tokens that are not there (from `n` on, of 8; n within 16 bits) as zero:
-// what they hold may be anything.
-__device__ __forceinline__ u4 first_words(u4 w, int n) {
+// Scale words of 8 tokens, those from `n` on (n within 16 bits) as zero: where tokens are
+// not there, what they hold may be anything.
+__device__ __forceinline__ uint32_t pair_below(int i, int n) {
   typedef short s2 __attribute__((ext_vector_type(2)));
-  const s2 have = {static_cast<short>(n), static_cast<short>(n)};
-  // (the sign of i - n, all over its 16 bits: nothing to branch on)
-  const auto keep = [have](uint32_t x, short i) { return x & __builtin_bit_cast(uint32_t, (s2{i, static_cast<short>(i + 1)} - have) >> 15); };
-  return u4{keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6)};
+  // (the signs of i - n and i + 1 - n, all over their 16 bits: nothing to branch on)
+  return __builtin_bit_cast(uint32_t, (s2{static_cast<short>(i), static_cast<short>(i + 1)} - s2{static_cast<short>(n), static_cast<short>(n)}) >> 15);
+}
+__device__ __forceinline__ u4 first_words(u4 w, int n) {
+  return u4{w.x & pair_below(0, n), w.y & pair_below(2, n), w.z & pair_below(4, n), w.w & pair_below(6, n)};
+}
+// The same for those before `n`.
+__device__ __forceinline__ u4 words_from(u4 w, int n) {
+  return u4{w.x & ~pair_below(0, n), w.y & ~pair_below(2, n), w.z & ~pair_below(4, n), w.w & ~pair_below(6, n)};
 }
 
 }  // namespace mxq

@@ -24,7 +24,8 @@
 //
 // Rounding: q and codes exact (a bf16 q to 2^-25 of its row's largest); sums, maxima and
 // weights f32.  P holds the weight times its value's scale over 2^k, 2^k the first power
-// of two that no scale so far reaches, in f16: normal down to 2^-27 of the largest.
+// of two that no scale the row has seen so far reaches, in f16: normal down to 2^-27 of the
+// largest.  k is a row's own: a key that it does not see costs it nothing.
 #include <climits>
 
 #include "attend4_device.h"
@@ -68,7 +69,7 @@ constexpr float kSlack4 = 1.75f;  // weights reach 2^(kLift + kSlack4), below f1
 }  // namespace
 
 template <int DIM, int MT, int WAVES, bool SMALL>
-__global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES == kFewWaves ? 1 : 2) void attend4_few_kernel(Attend4Args a) {
+__global__ __launch_bounds__(64 * WAVES, MT * DIM <= 128 ? 3 : WAVES == kFewWaves ? 1 : 2) void attend4_few_kernel(Attend4Args a) {
   constexpr int KW = DIM / 32, DP = DIM / 64, kRows = 16 * MT;
   __shared__ float join[WAVES][16][DIM + 4];
   __shared__ float join_m[WAVES][16], join_l[WAVES][16];
@@ -213,9 +214,10 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
   const Fields fields;
   f4 acc[MT][4 * DP];
   float m[MT], l[MT];
-  int unit = 0;  // k + 14: the exponent field of the largest scale
+  int unit[MT];  // k + 14: the exponent field of the largest scale that the row has seen
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
+    unit[mt] = 0;
     m[mt] = kNegInf;
     l[mt] = 0.0f;
 #pragma unroll
@@ -266,23 +268,15 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
     }
     if (!whole) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 2; ++u)
         r.vs[u] = first_words(r.vs[u], lane_there(c, u) ? max(min(limit - (c * kChunk + u * 32 + 8 * h), 8), 0) : 0);
-      }
     }
-    // the largest scale so far, as an exponent field
-    const uint32_t big = max_pairs(max_pairs(max_pairs(r.vs[0].x, r.vs[0].y), max_pairs(r.vs[0].z, r.vs[0].w)),
-                                   max_pairs(max_pairs(r.vs[1].x, r.vs[1].y), max_pairs(r.vs[1].z, r.vs[1].w)));
-    int field = static_cast<int>(max(big & 0xFFFFu, big >> 16) >> 10);
-    float shrink = 1.0f;
-    if (__any(field > unit)) {
-#pragma unroll
-      for (int d = 16; d < 64; d *= 2) field = max(field, __shfl_xor(field, d));
-      field = __builtin_amdgcn_readfirstlane(field);
-      shrink = __uint_as_float(static_cast<uint32_t>(127 - (field - unit)) << 23);
-      unit = field;
-    }
-    const float lift = kLift + 14.0f - static_cast<float>(unit);
+    // the largest scale of the lane's tokens, as an exponent field
+    const auto field_of = [](u4 x, u4 y) {
+      const uint32_t big = max_pairs(max_pairs(max_pairs(x.x, x.y), max_pairs(x.z, x.w)), max_pairs(max_pairs(y.x, y.y), max_pairs(y.z, y.w)));
+      return static_cast<int>(max(big & 0xFFFFu, big >> 16) >> 10);
+    };
+    const int all_field = field_of(r.vs[0], r.vs[1]);
     float base[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -293,18 +287,30 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
           const h2 sc = k_scale[t >> 1][2 * (t & 1) + (i >> 1)];
           s[mt][t][i] *= __builtin_fmaf(static_cast<float>(i & 1 ? sc.y : sc.x), factor[mt], 0.0f);
         }
+      int field = all_field;
       if (!whole) {
+        u4 vs[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           // of the lane's 8 tokens, the seen ones are `seen` from `begin` on
           const int key = c * kChunk + u * 32 + 8 * h, begin = max(from[mt] - key, 0), end = min(upto[mt] - key, 8);
           const uint32_t seen = lane_there(c, u) ? max(end - begin, 0) : 0;
+          vs[u] = words_from(first_words(r.vs[u], max(end, 0)), min(begin, 8));
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             f4& t = s[mt][2 * u + ((j & 3) >> 1)];
             t[2 * (j & 1) + (j >> 2)] = static_cast<uint32_t>(j - begin) < seen ? t[2 * (j & 1) + (j >> 2)] : kNegInf;
           }
         }
+        field = field_of(vs[0], vs[1]);
+      }
+      float shrink = 1.0f;
+      if (__any(field > unit[mt])) {
+        field = max(field, unit[mt]);
+#pragma unroll
+        for (int d = 16; d < 64; d *= 2) field = max(field, __shfl_xor(field, d));
+        shrink = __uint_as_float(static_cast<uint32_t>(127 - (field - unit[mt])) << 23);
+        unit[mt] = field;
       }
       float mx = kNegInf;
 #pragma unroll
@@ -317,7 +323,7 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
       const float ref = now == kNegInf ? 0.0f : now;
       const float down = __builtin_amdgcn_exp2f(m[mt] - ref) * shrink;
       m[mt] = now;
-      base[mt] = ref - lift;
+      base[mt] = ref - (kLift + 14.0f - static_cast<float>(unit[mt]));
       if (__any(down != 1.0f)) {
         l[mt] *= down;
 #pragma unroll
@@ -366,9 +372,9 @@ __global__ __launch_bounds__(64 * WAVES, MT == 1 ? 3 : MT * DIM >= 256 && WAVES 
 
   // join the waves, 16 rows at a time; weights in units of 2^-kLift, whatever the scales
   const bool alone = part.splits == 1;
-  const float scale_unit = __uint_as_float(static_cast<uint32_t>(127 + unit - 14) << 23);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
+    const float scale_unit = __uint_as_float(static_cast<uint32_t>(127 + unit[mt] - 14) << 23);
     const float weight = add_xor16(add_xor32(l[mt])) * scale_unit;
     if (h == 0) {
       join_m[wave][rho] = m[mt];
