@@ -48,3 +48,60 @@ def test_one_head_of_16_values(rot, t):
     for n in (1, 63, 513, 1023, 1024, 1500, 5003, 40001):
         for heads, kv in ((1, 0), (0, 1)):
             _run(n, heads, kv, 16, rot, n % 2 == 1, t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n,heads,kv,dim,rot", [
+    (513, 3, 0, 16, 16), (1024, 2, 1, 16, 16), (40001, 2, 1, 16, 0),                    # up to 64 tokens at a time
+    (513, 4, 2, 64, 64), (1023, 5, 1, 80, 48), (1025, 3, 1, 48, 32), (1500, 2, 0, 32, 32), (5003, 16, 4, 64, 32),
+    (777, 4, 2, 256, 256), (5000, 4, 2, 256, 256),                                      # the table of turns sets how many
+    (1100, 56, 14, 128, 64),                                                            # a token of more than a workgroup's lanes
+    (600, 3, 1, 250, 18), (1300, 2, 1, 128, 20)])                                       # one token a workgroup
+def test_many_tokens(n, heads, kv, dim, rot, inter):
+    """Tokens at a time, one after the other, and last ones that fill neither; no norm, one, both, in f32 and in the type."""
+    for norms, f32, t in ((3, False, "bf16"), (n % 3, True, "f16")):
+        _run(n, heads, kv, dim, rot, inter, t, norms, f32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+def test_many_tokens_on_several_axes(inter):
+    for n, heads, kv, dim, rot in ((1500, 3, 1, 64, 32), (5003, 16, 4, 64, 64), (700, 5, 1, 128, 100)):
+        _run(n, heads, kv, dim, rot, inter, "f16", axes=3, far=5000)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("n,heads,kv,dim,rot,inter", [(8191, 8, 2, 128, 128, False), (2500, 32, 8, 128, 128, True),
+                                                      (9001, 12, 4, 64, 32, False), (33333, 12, 4, 16, 16, True)])
+def test_more_than_the_caches_hold(n, heads, kv, dim, rot, inter, t):
+    """Calls of more than 32 MB, which pass the L2s by."""
+    assert 4 * n * (heads + kv) * dim > 32 << 20
+    _run(n, heads, kv, dim, rot, inter, t)
+
+
+@pytest.mark.gpu
+def test_more_tokens_than_a_launch_takes():
+    """2^23 tokens and some: the second launch's rows, with its positions on each axis, and the seam."""
+    n, dim, rot = 2 ** 23 + 70, 16, 16
+    gen = torch.Generator().manual_seed(4)
+    f = frequencies(rot)
+    rows = torch.cat((torch.arange(0, 40), torch.arange(2 ** 23 - 40, n)))
+    x = torch.randn(rows.shape[0], 1, dim, generator=gen).half()
+    pos = torch.randint(-5000, 5000, (2, rows.shape[0]), generator=gen, dtype=torch.int32)
+    w = (1 + 0.3 * torch.randn(dim, generator=gen)).half()
+    axes = (torch.arange(rot // 2) % 2).int()
+    q = torch.ones(n, 1, dim, dtype=torch.float16, device=DEV)
+    at = torch.zeros(2, n, dtype=torch.int32, device=DEV)
+    q[rows.to(DEV)], at[:, rows.to(DEV)] = x.to(DEV), pos.to(DEV)
+    out, whole = _guarded(n, 1, dim, torch.float16)
+    note("norm_rope past 2^23 tokens")
+    mxq.mxq_norm_rope(q, None, f.to(DEV), at, w.to(DEV), None, out, axes=axes.to(DEV))
+    torch.cuda.synchronize()
+    _check(out[rows.to(DEV)], x, w, 1e-6, f, pos, axes, False, "seam")
+    middle = out[40:2 ** 23 - 40]                     # tokens alike
+    assert bool((middle == middle[:1]).all())
+    _check(middle[:1], torch.ones(1, 1, dim, dtype=torch.float16), w, 1e-6, f, torch.zeros(2, 1, dtype=torch.int32), axes, False, "middle")
+    whole = whole.view(torch.int16)
+    assert bool((whole[:GUARD] == -3).all()) and bool((whole[GUARD + n:] == -3).all())
