@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * WAVES, MT * DIM <= 128 ? 3 : WAVES == kFewWave
   __shared__ float join[WAVES][16][DIM + 4];
   __shared__ float join_m[WAVES][16], join_l[WAVES][16];
   // (a workgroup of more waves takes all keys of its rows: parts are one each)
-  const Part part = WAVES == kFewWaves ? find_part_long_first<MT>(a, blockIdx.x) : find_part<MT>(a, blockIdx.x, -1);
+  const Part part = WAVES == kFewWaves && long_first_pays(a) ? find_part_long_first<MT>(a, blockIdx.x) : find_part<MT>(a, blockIdx.x, -1);
   // (starts that descend may give more parts than there are slots: not taken)
   if (!part.any || static_cast<uint32_t>(part.base + part.nth) >= static_cast<uint32_t>(a.slots)) return;
   const int hk = a.pool.kv_heads, block = a.pool.block, block_log2 = 31 - __builtin_clz(block);

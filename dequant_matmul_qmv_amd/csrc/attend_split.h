@@ -101,6 +101,17 @@ __device__ Part find_part(const Args& a, int slot, int seq) {
   return p;
 }
 
+// Whether long parts go first.  The search for them reads lens again for each of three kinds
+// where there are more sequences than two registers hold: that costs more than it gives
+// unless sequences may be long.  Heads of 128 over 4 bits, in us, long first / by sequence:
+//   up to 8192 keys   129 sequences 60 / 67, 192 84 / 95, 256 122 / 133, 512 263 / 249
+//   up to 2048 keys   256 sequences 71 / 61, 1024 538 / 325
+constexpr int kKeptSeqs = 128;
+template <typename Args>
+__device__ __forceinline__ bool long_first_pays(const Args& a) {
+  return a.seqs <= kKeptSeqs || 24 * static_cast<int64_t>(a.seqs) <= static_cast<int64_t>(a.width) * a.pool.block;
+}
+
 // The part that workgroup `index` takes where long parts go first: whole ones, then the
 // sequences' ends of at least half a part, then the others.  What is left for the last
 // workgroups is short (96 sequences of 5 .. 8192 keys over 4 bits: 44 us, by sequence 49,
@@ -116,7 +127,7 @@ __device__ Part find_part_long_first(const Args& a, int index) {
   }
   Part p{};
   p.step = part_step(a, wave_sum(total));
-  const bool kept = a.seqs <= 128;  // in registers: `first` and `last`
+  const bool kept = a.seqs <= kKeptSeqs;  // in registers: `first` and `last`
   const Share first = a.seqs > 64 && kept ? share_of<MT>(a, lane) : last;
 #pragma unroll 1
   for (int kind = 0; kind < 3; ++kind) {

@@ -121,3 +121,18 @@ def test_attention_of_many_sequences(kind, seqs, t):
         note(f"attention4, {seqs} sequences, {kind}, dim {dim}, up to {longest} keys, {t}")
         out, lse = _run(q, pool, table, lens, new, window, one=kind == "one")
         check_attention(out, lse, attention4_ref(q, pool, table, lens, new, window, dim ** -0.5), f"{seqs} {kind}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seqs,longest", [(129, 5000), (200, 5000), (200, 4700), (130, 9000)])
+def test_parts_of_many_sequences(seqs, longest):
+    """More sequences than registers hold, tables on both sides of where long parts stop going first."""
+    gen = torch.Generator().manual_seed(seqs + longest)
+    lens = _ragged(seqs, seqs + 5, longest)
+    blocks, table = paging(lens, 32, gen)
+    pool = _poison(list(random_pool4(blocks, 1, 32, 64, gen)), table, lens, 32)
+    for new in ([1] * seqs, [min(n, 1 + i % 3) for i, n in enumerate(lens)]):
+        q = torch.randn(sum(new), 2, 64, generator=gen).half()
+        note(f"attention4, {seqs} sequences of up to {longest} keys, new={new[:4]}")
+        out, lse = _run(q, pool, table, lens, new, one=max(new) == 1)
+        check_attention(out, lse, attention4_ref(q, pool, table, lens, new, 0, 64 ** -0.5), f"{seqs} of {longest}")
