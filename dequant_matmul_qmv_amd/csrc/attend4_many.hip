@@ -2,8 +2,8 @@
 // 4-bit paged cache; the mathematics is that of the few-row kernel.
 //
 // Bound: the matrix cores and, beside them, the exponentials (one for each score,
-// against 4 * dim flops): a prompt of 4001 tokens of 32 heads of 64 takes 112 .. 115 us
-// (49 at a library product's rate), six chunks of heads of 128 304 .. 309 (135).  A workgroup holds 128 rows (query heads that share a kv
+// against 4 * dim flops): a prompt of 4001 tokens of 32 heads of 64 takes 112 .. 116 us
+// (49 at a library product's rate), six chunks of heads of 128 304 .. 310 (135).  A workgroup holds 128 rows (query heads that share a kv
 // head, times new tokens), 32 a wave, and walks the keys 64 at a time.  A stage's
 // codes become their values, exact in f16, on their way into LDS for all four waves;
 // the next stage's words are fetched meanwhile.

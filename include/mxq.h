@@ -465,10 +465,11 @@ mxq_status mxq_rope_append4(const mxq_kv_cache4* cache, const void* q, int64_t q
  *
  * The same sum, masks, sequences, arguments, limits and errors.  Keys and values are
  * exact in f16 and so are f16 queries (a bf16 q's smallest values are rounded at 2^-25
- * of its row's largest); sums, maxima and weights are f32.  The probabilities (of few
- * rows, times their value's scale) are f16 relative to their row's largest (times the
- * largest scale of the keys that the row sees): to 2^-11 of their value, or 2^-38 of that
- * largest where they are below 2^-27 of it.  Scores and v must be finite.
+ * of its row's largest); sums, maxima and weights are f32 (of few rows, a score's terms
+ * are up to 79 |q| times the key's scale).  The probabilities (of few rows, times their
+ * value's scale) are f16 relative to their row's largest (times the largest scale of the
+ * keys that the row sees): to 2^-11 of their value, or 2^-38 of that largest where they
+ * are below 2^-27 of it.  Scores and v must be finite.
  */
 mxq_status mxq_attention4(const void* q, int64_t q_token, int64_t q_head, const mxq_kv_cache4* cache,
                           const int32_t* table, int64_t table_stride, int64_t width, const int32_t* lens,
