@@ -376,7 +376,8 @@ class KvCache4(_Cache):
     ``k_scale`` and ``v_scale`` int16 [blocks, kv_heads, block], f16 numbers whose lowest 4 bits
     are the zero point; contiguous, on one device; block 16, 32, 64 or 128, dim 64 or 128.
     Pages, tables and attributes as in ``KvCache``; ``mxq_kv_append``, ``mxq_rope_append`` and
-    ``mxq_attention`` take either."""
+    ``mxq_attention`` take either.  Over this one, attention leaves out weights (times scales)
+    below 2^-38 of a row's largest, which ``KvCache`` keeps: include/mxq.h."""
 
     __slots__ = ()
     _attend, _turned = "mxq_attention4", "mxq_rope_append4"
